@@ -1,6 +1,7 @@
 """DSpark per-round speculative-decoding hot path on AMD MI355X (gfx950).
 
-Python binding of the C ABI in ``include/dspark.h`` (``libdspark.so``, built
+Python binding of the C ABI in ``include/dspark.h`` and
+``include/dspark_serving.h`` (``libdspark.so``, built
 in-tree by ``build.py``).  The functions ``dspark_*`` mirror the C entry points
 one to one and only marshal arguments; every step of the path runs in the HIP
 kernels.  Importing this package does not load the library; the first call
@@ -14,6 +15,11 @@ from ._abi import (  # noqa: F401
     dspark_schedule, dspark_schedule_workspace, dspark_status_string, dspark_tv_overlap,
     dspark_tv_overlap_workspace, dspark_trace_collect, dspark_trace_enable, dspark_trace_entry,
     dspark_train_losses, dspark_train_losses_workspace, dspark_draft_rnn, dspark_verify_rnn,
-    dspark_verify, dspark_verify_workspace, library, trace_summary)
+    dspark_verify, dspark_verify_workspace, library, trace_summary,
+    dspark_logprobs, dspark_logprobs_workspace, dspark_logprobs_backward, dspark_cache_workspace,
+    dspark_cache_fork, dspark_cache_reserve, dspark_cache_commit, dspark_cache_release,
+    dspark_cache_compact, dspark_cache_attend, dspark_cache_attend_workspace)
 from .api import (draft, draft_rnn, schedule, train_losses, tv_overlap, verify, verify_rnn,
                   Workspace)  # noqa: F401
+from .serving import (cache_attend, cache_commit, cache_compact, cache_fork, cache_release,
+                      cache_reserve, logprobs, logprobs_backward, PagedCache)  # noqa: F401

@@ -66,6 +66,25 @@ def library():
         L.dspark_train_losses_workspace.restype = _sz
         L.dspark_train_losses.argtypes = ([_i] * 5 + [_f] + [_vp] * 7 + [_f, _f, _f]
                                           + [_vp] * 3 + [_sz, _vp])
+        # dspark_serving.h
+        _i64 = C.c_int64
+        L.dspark_logprobs_workspace.argtypes = [_i, _i, _i, _i]
+        L.dspark_logprobs_workspace.restype = _sz
+        L.dspark_logprobs.argtypes = ([_i, _i, _i64, _i, _f, _vp, _vp, _i, _i, _vp, _i] + [_vp] * 6
+                                      + [_sz, _vp])
+        L.dspark_logprobs_backward.argtypes = ([_i, _i, _i64, _i, _f, _vp, _vp, _i, _i] + [_vp] * 5
+                                               + [_i, _vp, _vp, _vp, _i64, _vp, _sz, _vp])
+        L.dspark_cache_workspace.argtypes = [_i, _i]
+        L.dspark_cache_workspace.restype = _sz
+        L.dspark_cache_fork.argtypes = [_i] * 5 + [_vp] * 9 + [_sz, _vp]
+        L.dspark_cache_reserve.argtypes = [_i] * 4 + [_vp] * 9 + [_sz, _vp, _vp, _sz, _vp]
+        L.dspark_cache_commit.argtypes = [_i] * 4 + [_vp] * 9 + [_sz, _vp]
+        L.dspark_cache_release.argtypes = [_i] * 5 + [_vp] * 8 + [_sz, _vp]
+        L.dspark_cache_compact.argtypes = [_i] * 4 + [_vp] * 8 + [_sz, _vp, _vp, _sz, _vp]
+        L.dspark_cache_attend_workspace.argtypes = [_i] * 6
+        L.dspark_cache_attend_workspace.restype = _sz
+        L.dspark_cache_attend.argtypes = ([_i] * 9 + [_f, _i, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                                          _i64, _i64] + [_vp] * 6 + [_sz, _vp])
         L.dspark_device_error.argtypes = [_vp, _vp, _vp]
         L.dspark_clear_device_error.argtypes = [_vp, _vp]
         L.dspark_trace_enable.argtypes = [_i]
@@ -75,7 +94,10 @@ def library():
         for name in ("dspark_draft", "dspark_draft_noalloc", "dspark_schedule", "dspark_verify",
                      "dspark_tv_overlap", "dspark_train_losses", "dspark_draft_rnn", "dspark_verify_rnn",
                      "dspark_device_error", "dspark_clear_device_error", "dspark_trace_enable",
-                     "dspark_trace_collect", "dspark_trace_entry"):
+                     "dspark_trace_collect", "dspark_trace_entry", "dspark_logprobs",
+                     "dspark_logprobs_backward", "dspark_cache_fork", "dspark_cache_reserve",
+                     "dspark_cache_commit", "dspark_cache_release", "dspark_cache_compact",
+                     "dspark_cache_attend"):
             getattr(L, name).restype = _i
         _lib = L
     return _lib
@@ -182,6 +204,85 @@ def dspark_train_losses(R, gamma, V, r, dt, temp, U, W1, W2, P, x0, y, c, a_ce, 
     return library().dspark_train_losses(R, gamma, V, r, dt, temp, _p(U), _p(W1), _p(W2), _p(P),
                                          _p(x0), _p(y), _p(c), a_ce, a_tv, a_conf, _p(per_pos),
                                          _p(totals), _p(ws), ws_bytes, _s(stream))
+
+
+# ------------------------------------------------------------ dspark_serving.h
+def dspark_logprobs_workspace(n_rows, V, k, dt):
+    return library().dspark_logprobs_workspace(n_rows, V, k, dt)
+
+
+def dspark_logprobs(n_rows, V, row_stride, dt, temp, X, tokens, tok_stride, R, row_offset, k, logp,
+                    entropy, stats, top_ids, top_logp, ws, ws_bytes, stream):
+    return library().dspark_logprobs(n_rows, V, row_stride, dt, temp, _p(X), _p(tokens),
+                                     tok_stride, R, _p(row_offset), k, _p(logp), _p(entropy),
+                                     _p(stats), _p(top_ids), _p(top_logp), _p(ws), ws_bytes,
+                                     _s(stream))
+
+
+def dspark_logprobs_backward(n_rows, V, row_stride, dt, temp, X, tokens, tok_stride, R, row_offset,
+                             stats, entropy, g_logp, g_entropy, k, top_ids, g_top, dX, dx_stride,
+                             ws, ws_bytes, stream):
+    return library().dspark_logprobs_backward(n_rows, V, row_stride, dt, temp, _p(X), _p(tokens),
+                                              tok_stride, R, _p(row_offset), _p(stats),
+                                              _p(entropy), _p(g_logp), _p(g_entropy), k,
+                                              _p(top_ids), _p(g_top), _p(dX), dx_stride, _p(ws),
+                                              ws_bytes, _s(stream))
+
+
+def dspark_cache_workspace(R, n_pages):
+    return library().dspark_cache_workspace(R, n_pages)
+
+
+def dspark_cache_fork(R, page, max_pages, n_pages, n, src, dst, lens, table, refs, lens_out,
+                      table_out, refs_out, ws, ws_bytes, stream):
+    return library().dspark_cache_fork(R, page, max_pages, n_pages, n, _p(src), _p(dst), _p(lens),
+                                       _p(table), _p(refs), _p(lens_out), _p(table_out),
+                                       _p(refs_out), _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_cache_reserve(R, page, max_pages, n_pages, row_offset, lens, table, refs, lens_out,
+                         table_out, refs_out, k_pages, v_pages, page_bytes, missing, ws, ws_bytes,
+                         stream):
+    return library().dspark_cache_reserve(R, page, max_pages, n_pages, _p(row_offset), _p(lens),
+                                          _p(table), _p(refs), _p(lens_out), _p(table_out),
+                                          _p(refs_out), _p(k_pages), _p(v_pages), page_bytes,
+                                          _p(missing), _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_cache_commit(R, page, max_pages, n_pages, row_offset, n_acc, lens, table, refs, lens_out,
+                        table_out, refs_out, ws, ws_bytes, stream):
+    return library().dspark_cache_commit(R, page, max_pages, n_pages, _p(row_offset), _p(n_acc),
+                                         _p(lens), _p(table), _p(refs), _p(lens_out),
+                                         _p(table_out), _p(refs_out), _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_cache_release(R, page, max_pages, n_pages, n, which, lens, table, refs, lens_out,
+                         table_out, refs_out, ws, ws_bytes, stream):
+    return library().dspark_cache_release(R, page, max_pages, n_pages, n, _p(which), _p(lens),
+                                          _p(table), _p(refs), _p(lens_out), _p(table_out),
+                                          _p(refs_out), _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_cache_compact(R, page, max_pages, n_pages, lens, table, refs, lens_out, table_out,
+                         refs_out, k_pages, v_pages, page_bytes, n_live, ws, ws_bytes, stream):
+    return library().dspark_cache_compact(R, page, max_pages, n_pages, _p(lens), _p(table),
+                                          _p(refs), _p(lens_out), _p(table_out), _p(refs_out),
+                                          _p(k_pages), _p(v_pages), page_bytes, _p(n_live), _p(ws),
+                                          ws_bytes, _s(stream))
+
+
+def dspark_cache_attend_workspace(R, rows_capacity, Hq, Hkv, D, dt):
+    return library().dspark_cache_attend_workspace(R, rows_capacity, Hq, Hkv, D, dt)
+
+
+def dspark_cache_attend(R, rows_capacity, Hq, Hkv, D, page, max_pages, n_pages, dt, scale, window,
+                        q, q_stride, k_new, v_new, kv_stride, k_pages, v_pages, k_page_stride,
+                        v_page_stride, table, row_offset, kv_len, out, lse, ws, ws_bytes, stream):
+    return library().dspark_cache_attend(R, rows_capacity, Hq, Hkv, D, page, max_pages, n_pages, dt,
+                                         scale, window, _p(q), q_stride, _p(k_new), _p(v_new),
+                                         kv_stride, _p(k_pages), _p(v_pages), k_page_stride,
+                                         v_page_stride, _p(table), _p(row_offset), _p(kv_len),
+                                         _p(out), _p(lse), _p(ws), ws_bytes, _s(stream))
 
 
 def dspark_device_error(ws, stream):

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/dspark.h"
+#include "../../include/dspark_serving.h"
 #include "kernels.h"
 
 using namespace dspark;
@@ -343,6 +344,247 @@ dspark_status dspark_train_losses(int R, int gamma, int V, int r, dspark_dtype d
   T.per_pos = per_pos; T.totals = totals;
   T.req_sums = (double *)carve(ws, &off, (size_t)R * 3 * 8);
   return from_hip(launch_train(T, stream));
+}
+
+// ------------------------------------------------------- dspark_serving.h
+size_t dspark_logprobs_workspace(int n_rows, int V, int k, dspark_dtype dt) {
+  if (n_rows < 1 || V < 1 || k < 0 || (dt != DSPARK_F32 && dt != DSPARK_BF16)) return 0;
+  return logprobs_ws_bytes(n_rows, V, k, dt == DSPARK_BF16);
+}
+
+static dspark_status check_rows(int n_rows, int V, int64_t row_stride, dspark_dtype dt, float temp,
+                                const int32_t *tokens, int tok_stride, int R,
+                                const int32_t *row_offset, int k) {
+  if (dt != DSPARK_F32 && dt != DSPARK_BF16) return DSPARK_ERR_DTYPE;
+  if (n_rows < 1 || n_rows > (1 << 22) || V < 1 || V > 262144 || k < 0 || k > 64 || k > V)
+    return DSPARK_ERR_SHAPE;
+  if (row_stride < V || row_stride % (dt == DSPARK_BF16 ? 8 : 4) != 0) return DSPARK_ERR_SHAPE;
+  if (row_offset != nullptr && (R < 1 || R > n_rows)) return DSPARK_ERR_SHAPE;
+  if (row_offset != nullptr && tokens != nullptr && tok_stride < 1) return DSPARK_ERR_SHAPE;
+  if (bad_temp(temp)) return DSPARK_ERR_VALUE;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_logprobs(int n_rows, int V, int64_t row_stride, dspark_dtype dt, float temp,
+                              const void *X, const int32_t *tokens, int tok_stride, int R,
+                              const int32_t *row_offset, int k, float *logp, float *entropy,
+                              float *stats, int32_t *top_ids, float *top_logp, void *ws,
+                              size_t ws_bytes, hipStream_t stream) {
+  dspark_status s =
+      check_rows(n_rows, V, row_stride, dt, temp, tokens, tok_stride, R, row_offset, k);
+  if (s != DSPARK_OK) return s;
+  if (!X || !ws || (k > 0 && (!top_ids || !top_logp)) || (tokens == nullptr) != (logp == nullptr))
+    return DSPARK_ERR_NULL;
+  if (!aligned16(X) || !aligned16(ws)) return DSPARK_ERR_ALIGN;
+  if (ws_bytes < logprobs_ws_bytes(n_rows, V, k, dt == DSPARK_BF16)) return DSPARK_ERR_WORKSPACE;
+  size_t off = 0;
+  LogprobsLaunch L{};
+  L.err = (int32_t *)carve(ws, &off, kWsHeader);
+  L.scratch = (char *)ws + off;
+  L.n_rows = n_rows; L.V = V; L.R = R; L.k = k; L.tok_stride = tok_stride;
+  L.row_stride = row_stride; L.bf16 = dt == DSPARK_BF16; L.temp = temp; L.X = X;
+  L.tokens = tokens; L.row_offset = row_offset; L.logp = logp; L.entropy = entropy;
+  L.stats = stats; L.top_ids = k > 0 ? top_ids : nullptr; L.top_logp = k > 0 ? top_logp : nullptr;
+  return from_hip(launch_logprobs(L, stream));
+}
+
+dspark_status dspark_logprobs_backward(int n_rows, int V, int64_t row_stride, dspark_dtype dt,
+                                       float temp, const void *X, const int32_t *tokens,
+                                       int tok_stride, int R, const int32_t *row_offset,
+                                       const float *stats, const float *entropy,
+                                       const float *g_logp, const float *g_entropy, int k,
+                                       const int32_t *top_ids, const float *g_top, void *dX,
+                                       int64_t dx_stride, void *ws, size_t ws_bytes,
+                                       hipStream_t stream) {
+  dspark_status s =
+      check_rows(n_rows, V, row_stride, dt, temp, tokens, tok_stride, R, row_offset, k);
+  if (s != DSPARK_OK) return s;
+  if (dx_stride < V || dx_stride % (dt == DSPARK_BF16 ? 8 : 4) != 0) return DSPARK_ERR_SHAPE;
+  if (!X || !stats || !dX || !ws || (k > 0 && (!top_ids || !g_top)) ||
+      (g_logp != nullptr && !tokens) || (g_entropy != nullptr && !entropy))
+    return DSPARK_ERR_NULL;
+  if (dX == X && dx_stride != row_stride) return DSPARK_ERR_VALUE;
+  if (!aligned16(X) || !aligned16(dX) || !aligned16(ws)) return DSPARK_ERR_ALIGN;
+  if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  LogprobsGradLaunch L{};
+  L.err = (int32_t *)ws;
+  L.n_rows = n_rows; L.V = V; L.R = R; L.k = k; L.tok_stride = tok_stride;
+  L.row_stride = row_stride; L.dx_stride = dx_stride; L.bf16 = dt == DSPARK_BF16; L.temp = temp;
+  L.X = X; L.tokens = tokens; L.row_offset = row_offset; L.top_ids = top_ids; L.stats = stats;
+  L.entropy = entropy; L.g_logp = g_logp; L.g_entropy = g_entropy; L.g_top = g_top; L.dX = dX;
+  return from_hip(launch_logprobs_backward(L, stream));
+}
+
+static int shift_of(int page) {
+  int shift = 0;
+  while ((1 << shift) < page) ++shift;
+  return shift;
+}
+
+static bool bad_cache_shape(int R, int page, int max_pages, int n_pages) {
+  return R < 1 || R > 8192 || page < 16 || page > 256 || (page & (page - 1)) != 0 || n_pages < 1 ||
+         n_pages > (1 << 22) || max_pages < 1 || (int64_t)R * max_pages > (1 << 28) ||
+         (int64_t)page * max_pages > INT32_MAX;
+}
+
+// The shape, the state's arrays and the workspace of a page operation.
+static dspark_status cache_state(int R, int page, int max_pages, int n_pages, const int32_t *lens,
+                                 const int32_t *table, const int32_t *refs, int32_t *lens_out,
+                                 int32_t *table_out, int32_t *refs_out, void *ws, size_t ws_bytes,
+                                 CacheState *S) {
+  if (bad_cache_shape(R, page, max_pages, n_pages)) return DSPARK_ERR_SHAPE;
+  if (!lens || !table || !refs || !lens_out || !table_out || !refs_out || !ws)
+    return DSPARK_ERR_NULL;
+  if (!aligned16(refs) || !aligned16(refs_out) || !aligned16(ws)) return DSPARK_ERR_ALIGN;
+  const bool same = lens == lens_out;
+  if ((table == table_out) != same || (refs == refs_out) != same) return DSPARK_ERR_VALUE;
+  if (ws_bytes < cache_ws_bytes(R, n_pages)) return DSPARK_ERR_WORKSPACE;
+  S->R = R; S->page_shift = shift_of(page); S->max_pages = max_pages; S->n_pages = n_pages;
+  S->lens_in = lens; S->table_in = table; S->refs_in = refs;
+  S->lens = lens_out; S->table = table_out; S->refs = refs_out;
+  S->err = (int32_t *)ws;
+  S->plan = (int32_t *)((char *)ws + kWsHeader);
+  return DSPARK_OK;
+}
+
+static dspark_status cache_pools(void *k_pages, void *v_pages, size_t page_bytes, CachePools *P) {
+  if ((k_pages == nullptr) != (v_pages == nullptr)) return DSPARK_ERR_NULL;
+  if (k_pages != nullptr) {
+    if (page_bytes < 16 || page_bytes % 16 != 0) return DSPARK_ERR_SHAPE;
+    if (!aligned16(k_pages) || !aligned16(v_pages)) return DSPARK_ERR_ALIGN;
+  }
+  P->k = k_pages; P->v = v_pages; P->page_bytes = page_bytes;
+  return DSPARK_OK;
+}
+
+size_t dspark_cache_workspace(int R, int n_pages) {
+  if (R < 1 || n_pages < 1) return 0;
+  return cache_ws_bytes(R, n_pages);
+}
+
+dspark_status dspark_cache_fork(int R, int page, int max_pages, int n_pages, int n,
+                                const int32_t *src, const int32_t *dst, const int32_t *lens,
+                                const int32_t *table, const int32_t *refs, int32_t *lens_out,
+                                int32_t *table_out, int32_t *refs_out, void *ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  CacheState S{};
+  dspark_status s = cache_state(R, page, max_pages, n_pages, lens, table, refs, lens_out, table_out,
+                                refs_out, ws, ws_bytes, &S);
+  if (s != DSPARK_OK) return s;
+  if (n < 1 || n > R) return DSPARK_ERR_SHAPE;
+  if (!src || !dst) return DSPARK_ERR_NULL;
+  return from_hip(launch_cache_fork(S, n, src, dst, stream));
+}
+
+dspark_status dspark_cache_reserve(int R, int page, int max_pages, int n_pages,
+                                   const int32_t *row_offset, const int32_t *lens,
+                                   const int32_t *table, const int32_t *refs, int32_t *lens_out,
+                                   int32_t *table_out, int32_t *refs_out, void *k_pages,
+                                   void *v_pages, size_t page_bytes, int32_t *missing, void *ws,
+                                   size_t ws_bytes, hipStream_t stream) {
+  CacheState S{};
+  CachePools P{};
+  dspark_status s = cache_state(R, page, max_pages, n_pages, lens, table, refs, lens_out, table_out,
+                                refs_out, ws, ws_bytes, &S);
+  if (s == DSPARK_OK) s = cache_pools(k_pages, v_pages, page_bytes, &P);
+  if (s != DSPARK_OK) return s;
+  if (!row_offset || !missing) return DSPARK_ERR_NULL;
+  return from_hip(launch_cache_reserve(S, P, row_offset, missing, stream));
+}
+
+dspark_status dspark_cache_commit(int R, int page, int max_pages, int n_pages,
+                                  const int32_t *row_offset, const int32_t *n_acc,
+                                  const int32_t *lens, const int32_t *table, const int32_t *refs,
+                                  int32_t *lens_out, int32_t *table_out, int32_t *refs_out,
+                                  void *ws, size_t ws_bytes, hipStream_t stream) {
+  CacheState S{};
+  dspark_status s = cache_state(R, page, max_pages, n_pages, lens, table, refs, lens_out, table_out,
+                                refs_out, ws, ws_bytes, &S);
+  if (s != DSPARK_OK) return s;
+  if (!row_offset || !n_acc) return DSPARK_ERR_NULL;
+  return from_hip(launch_cache_commit(S, row_offset, n_acc, stream));
+}
+
+dspark_status dspark_cache_release(int R, int page, int max_pages, int n_pages, int n,
+                                   const int32_t *which, const int32_t *lens,
+                                   const int32_t *table, const int32_t *refs, int32_t *lens_out,
+                                   int32_t *table_out, int32_t *refs_out, void *ws,
+                                   size_t ws_bytes, hipStream_t stream) {
+  CacheState S{};
+  dspark_status s = cache_state(R, page, max_pages, n_pages, lens, table, refs, lens_out, table_out,
+                                refs_out, ws, ws_bytes, &S);
+  if (s != DSPARK_OK) return s;
+  if (n < 1 || n > R) return DSPARK_ERR_SHAPE;
+  if (!which) return DSPARK_ERR_NULL;
+  return from_hip(launch_cache_release(S, n, which, stream));
+}
+
+dspark_status dspark_cache_compact(int R, int page, int max_pages, int n_pages,
+                                   const int32_t *lens, const int32_t *table, const int32_t *refs,
+                                   int32_t *lens_out, int32_t *table_out, int32_t *refs_out,
+                                   void *k_pages, void *v_pages, size_t page_bytes,
+                                   int32_t *n_live, void *ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  CacheState S{};
+  CachePools P{};
+  dspark_status s = cache_state(R, page, max_pages, n_pages, lens, table, refs, lens_out, table_out,
+                                refs_out, ws, ws_bytes, &S);
+  if (s == DSPARK_OK) s = cache_pools(k_pages, v_pages, page_bytes, &P);
+  if (s != DSPARK_OK) return s;
+  if (!n_live) return DSPARK_ERR_NULL;
+  return from_hip(launch_cache_compact(S, P, n_live, stream));
+}
+
+static bool bad_attend_shape(int R, int rows_capacity, int Hq, int Hkv, int D) {
+  return R < 1 || R > 8192 || rows_capacity < 1 || rows_capacity > (1 << 20) || Hkv < 1 || Hq < Hkv ||
+         Hq > 1024 || Hq % Hkv != 0 || (D != 64 && D != 96 && D != 128 && D != 256);
+}
+
+size_t dspark_cache_attend_workspace(int R, int rows_capacity, int Hq, int Hkv, int D,
+                                     dspark_dtype dt) {
+  if (bad_attend_shape(R, rows_capacity, Hq, Hkv, D)) return 0;
+  return attend_ws_bytes(R, rows_capacity, Hq, Hkv, D, dt == DSPARK_BF16);
+}
+
+dspark_status dspark_cache_attend(int R, int rows_capacity, int Hq, int Hkv, int D, int page,
+                                  int max_pages, int n_pages, dspark_dtype dt, float scale,
+                                  int window, const void *q, int64_t q_stride, const void *k_new,
+                                  const void *v_new, int64_t kv_stride, void *k_pages,
+                                  void *v_pages, int64_t k_page_stride, int64_t v_page_stride,
+                                  const int32_t *table, const int32_t *row_offset,
+                                  const int32_t *kv_len, void *out, float *lse, void *ws,
+                                  size_t ws_bytes, hipStream_t stream) {
+  if (dt != DSPARK_F32 && dt != DSPARK_BF16) return DSPARK_ERR_DTYPE;
+  if (bad_attend_shape(R, rows_capacity, Hq, Hkv, D) || bad_cache_shape(R, page, max_pages, n_pages))
+    return DSPARK_ERR_SHAPE;
+  if (row_offset == nullptr && rows_capacity != R) return DSPARK_ERR_SHAPE;
+  if (!(scale > 0.0f) || !isfinite(scale) || window < 0) return DSPARK_ERR_VALUE;
+  if (!q || !k_pages || !v_pages || !table || !kv_len || !out || !ws ||
+      (k_new == nullptr) != (v_new == nullptr))
+    return DSPARK_ERR_NULL;
+  const int per = dt == DSPARK_BF16 ? 8 : 4;
+  const int64_t page_elems = (int64_t)Hkv * page * D;
+  if (q_stride < (int64_t)Hq * D || q_stride % per != 0 || k_page_stride < page_elems ||
+      v_page_stride < page_elems || k_page_stride % per != 0 || v_page_stride % per != 0)
+    return DSPARK_ERR_SHAPE;
+  if (k_new != nullptr && (kv_stride < (int64_t)Hkv * D || kv_stride % per != 0))
+    return DSPARK_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) ||
+      !aligned16(v_pages) || !aligned16(out) || !aligned16(ws))
+    return DSPARK_ERR_ALIGN;
+  if (ws_bytes < attend_ws_bytes(R, rows_capacity, Hq, Hkv, D, dt == DSPARK_BF16))
+    return DSPARK_ERR_WORKSPACE;
+  size_t off = 0;
+  AttendLaunch L{};
+  L.err = (int32_t *)carve(ws, &off, kWsHeader);
+  L.scratch = (char *)ws + off;
+  L.R = R; L.rows_capacity = rows_capacity; L.Hq = Hq; L.Hkv = Hkv; L.D = D;
+  L.page_shift = shift_of(page); L.max_pages = max_pages; L.n_pages = n_pages; L.window = window;
+  L.bf16 = dt == DSPARK_BF16; L.scale = scale; L.q = q; L.k_new = k_new; L.v_new = v_new;
+  L.q_stride = q_stride; L.kv_stride = kv_stride; L.k_page_stride = k_page_stride;
+  L.v_page_stride = v_page_stride; L.k_pages = k_pages; L.v_pages = v_pages; L.table = table;
+  L.row_offset = row_offset; L.kv_len = kv_len; L.out = out; L.lse = lse;
+  return from_hip(launch_attend(L, stream));
 }
 
 size_t dspark_tv_overlap_workspace(int n_rows, int V) {

@@ -24,7 +24,8 @@ constexpr int kMaxRank = 256;
 constexpr int kMaxGamma = 64;       // draft positions per request
 
 // sticky device error bits (mirrors dspark.h)
-constexpr int kErrToken = 1, kErrConfidence = 2, kErrLength = 4, kErrNonFinite = 8, kErrSync = 16;
+constexpr int kErrToken = 1, kErrConfidence = 2, kErrLength = 4, kErrNonFinite = 8, kErrSync = 16,
+              kErrPage = 32, kErrNoPages = 64;  // the last two: dspark_serving.h
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));

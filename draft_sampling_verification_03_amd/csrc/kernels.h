@@ -107,6 +107,73 @@ struct TrainLaunch {
   double *req_sums;  // [R][3]: each request's weighted (CE, L1, BCE) means
 };
 
+struct LogprobsLaunch {
+  int n_rows, V, R, k, tok_stride;
+  int64_t row_stride;
+  bool bf16;
+  double temp;
+  const void *X;
+  const int32_t *tokens, *row_offset;  // each or NULL
+  float *logp, *entropy, *stats, *top_logp;
+  int32_t *top_ids;
+  int32_t *err;
+  void *scratch;  // [n_rows][chunks] sums, then [n_rows][chunks][k] keys
+};
+
+struct LogprobsGradLaunch {
+  int n_rows, V, R, k, tok_stride;
+  int64_t row_stride, dx_stride;
+  bool bf16;
+  double temp;
+  const void *X;
+  const int32_t *tokens, *row_offset, *top_ids;
+  const float *stats, *entropy, *g_logp, *g_entropy, *g_top;
+  void *dX;
+  int32_t *err;
+};
+
+// State of a paged cache before (in) and after a page operation (the same
+// arrays when in place).
+struct CacheState {
+  int R, page_shift, max_pages, n_pages;
+  const int32_t *lens_in, *table_in, *refs_in;
+  int32_t *lens, *table, *refs;
+  int32_t *err;
+  int32_t *plan;  // scratch: cache_plan_ints(R, n_pages)
+  __host__ __device__ bool in_place() const { return lens == lens_in; }
+};
+
+struct CachePools {
+  void *k, *v;  // NULL both: numbers only
+  size_t page_bytes;
+};
+
+struct AttendLaunch {
+  int R, rows_capacity, Hq, Hkv, D, page_shift, max_pages, n_pages, window;
+  bool bf16;
+  float scale;
+  const void *q, *k_new, *v_new;
+  int64_t q_stride, kv_stride, k_page_stride, v_page_stride;
+  void *k_pages, *v_pages;
+  const int32_t *table, *row_offset, *kv_len;
+  void *out;
+  float *lse;
+  int32_t *err;
+  void *scratch;
+};
+
+hipError_t launch_logprobs(const LogprobsLaunch &L, hipStream_t stream);
+hipError_t launch_logprobs_backward(const LogprobsGradLaunch &L, hipStream_t stream);
+hipError_t launch_cache_fork(const CacheState &S, int n, const int32_t *src, const int32_t *dst,
+                             hipStream_t stream);
+hipError_t launch_cache_reserve(const CacheState &S, const CachePools &P, const int32_t *row_offset,
+                                int32_t *missing, hipStream_t stream);
+hipError_t launch_cache_commit(const CacheState &S, const int32_t *row_offset, const int32_t *n_acc,
+                               hipStream_t stream);
+hipError_t launch_cache_release(const CacheState &S, int n, const int32_t *which, hipStream_t stream);
+hipError_t launch_cache_compact(const CacheState &S, const CachePools &P, int32_t *n_live,
+                                hipStream_t stream);
+hipError_t launch_attend(const AttendLaunch &L, hipStream_t stream);
 hipError_t launch_draft(const DraftLaunch &L, hipStream_t stream);
 hipError_t launch_schedule(const ScheduleLaunch &L, hipStream_t stream);
 hipError_t launch_verify(const VerifyLaunch &L, hipStream_t stream);
@@ -139,6 +206,15 @@ inline size_t train_ws_bytes(int R, int gamma, int V) {
   return draft_ws_bytes(R, gamma, V) + verify_ws_bytes(R, gamma, V, R * (gamma + 1)) +
          4 * ws_align(n * 4) + ws_align(n * 8) + 3 * ws_align(((size_t)R + 1) * 4) +
          ws_align((size_t)R * (gamma + 1) * 4) + ws_align((size_t)R * 3 * 8);
+}
+size_t logprobs_ws_bytes(int n_rows, int V, int k, bool bf16);
+size_t attend_ws_bytes(int R, int rows_capacity, int Hq, int Hkv, int D, bool bf16);
+// page operations: a head of 64, three per request, three per page
+inline size_t cache_plan_ints(int R, int n_pages) {
+  return 64 + 3 * (size_t)R + 3 * (size_t)n_pages;
+}
+inline size_t cache_ws_bytes(int R, int n_pages) {
+  return kWsHeader + ws_align(cache_plan_ints(R, n_pages) * 4);
 }
 inline size_t overlap_ws_bytes(int n_rows, int V) {
   (void)V;

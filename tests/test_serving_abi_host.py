@@ -1,0 +1,207 @@
+"""Host-side checks of include/dspark_serving.h (no GPU needed): every declared
+function is exported, and every invalid argument is refused before any HIP
+call.  The pointers are fake aligned addresses that nothing dereferences."""
+import os
+import re
+
+import pytest
+import torch
+
+import draft_sampling_verification_03_amd as ds
+from draft_sampling_verification_03_amd import _abi as A
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, NULL, SHAPE, DTYPE, VALUE, WS, SPS, MODE, ALIGN = range(9)
+P, P2, P3, P4, P5, P6 = (0x10000 * i for i in range(1, 7))
+BIG = 1 << 40
+
+
+def test_library_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "dspark_serving.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\b(dspark_[a-z_0-9]+)\s*\(", text)))
+    assert len(names) == 11, names
+    for name in names:
+        assert hasattr(ds.library(), name)
+        assert callable(getattr(ds, name))
+
+
+def lp(**over):
+    a = dict(n_rows=8, V=1001, row_stride=1008, dt=A.DSPARK_BF16, temp=1.0, X=P, tokens=P,
+             tok_stride=4, R=2, row_offset=P, k=5, logp=P, entropy=P, stats=P, top_ids=P, top_logp=P,
+             ws=P, ws_bytes=BIG, stream=None)
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dt=2), DTYPE), (dict(n_rows=0), SHAPE), (dict(n_rows=(1 << 22) + 1), SHAPE),
+    (dict(V=0), SHAPE), (dict(V=262145, row_stride=262152), SHAPE), (dict(row_stride=1000), SHAPE),
+    (dict(row_stride=1012), SHAPE), (dict(dt=A.DSPARK_F32, row_stride=1002), SHAPE),
+    (dict(k=-1), SHAPE), (dict(k=65), SHAPE), (dict(V=4, k=5), SHAPE), (dict(R=0), SHAPE),
+    (dict(R=9), SHAPE), (dict(tok_stride=0), SHAPE), (dict(temp=0.0), VALUE),
+    (dict(temp=float("nan")), VALUE), (dict(X=None), NULL), (dict(ws=None), NULL),
+    (dict(tokens=None), NULL), (dict(logp=None), NULL), (dict(top_ids=None), NULL),
+    (dict(top_logp=None), NULL), (dict(X=P + 8), ALIGN), (dict(ws=P + 4), ALIGN),
+    (dict(ws_bytes=256), WS),
+])
+def test_logprobs_validation(over, expect):
+    assert A.dspark_logprobs(**lp(**over)) == expect
+
+
+def grad(**over):
+    a = dict(n_rows=8, V=1001, row_stride=1008, dt=A.DSPARK_BF16, temp=1.0, X=P, tokens=P,
+             tok_stride=4, R=2, row_offset=P, stats=P, entropy=P, g_logp=P, g_entropy=P, k=5,
+             top_ids=P, g_top=P, dX=P2, dx_stride=1008, ws=P, ws_bytes=256, stream=None)
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dt=-1), DTYPE), (dict(V=0), SHAPE), (dict(k=65), SHAPE), (dict(dx_stride=1000), SHAPE),
+    (dict(dx_stride=1009), SHAPE), (dict(temp=-1.0), VALUE), (dict(X=None), NULL),
+    (dict(stats=None), NULL), (dict(dX=None), NULL), (dict(top_ids=None), NULL),
+    (dict(g_top=None), NULL), (dict(tokens=None), NULL), (dict(entropy=None), NULL),
+    (dict(dX=P, dx_stride=1016), VALUE), (dict(dX=P2 + 2), ALIGN), (dict(ws_bytes=128), WS),
+])
+def test_logprobs_backward_validation(over, expect):
+    assert A.dspark_logprobs_backward(**grad(**over)) == expect
+
+
+def state(**over):
+    a = dict(R=4, page=16, max_pages=8, n_pages=64, lens=P, table=P2, refs=P3, lens_out=P4,
+             table_out=P5, refs_out=P6, ws=P, ws_bytes=BIG, stream=None)
+    a.update(over)
+    return a
+
+
+OPS = {
+    "fork": (A.dspark_cache_fork, dict(n=2, src=P, dst=P)),
+    "reserve": (A.dspark_cache_reserve, dict(row_offset=P, k_pages=P, v_pages=P, page_bytes=64,
+                                             missing=P)),
+    "commit": (A.dspark_cache_commit, dict(row_offset=P, n_acc=P)),
+    "release": (A.dspark_cache_release, dict(n=2, which=P)),
+    "compact": (A.dspark_cache_compact, dict(k_pages=P, v_pages=P, page_bytes=64, n_live=P)),
+}
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("over,expect", [
+    (dict(R=0), SHAPE), (dict(R=8193), SHAPE), (dict(page=8), SHAPE), (dict(page=24), SHAPE),
+    (dict(page=512), SHAPE), (dict(max_pages=0), SHAPE), (dict(max_pages=(1 << 27)), SHAPE),
+    (dict(R=1, page=256, max_pages=1 << 23), SHAPE), (dict(n_pages=0), SHAPE),
+    (dict(n_pages=(1 << 22) + 1), SHAPE), (dict(lens=None), NULL), (dict(table_out=None), NULL),
+    (dict(ws=None), NULL), (dict(refs=P3 + 4), ALIGN), (dict(ws_bytes=300), WS),
+    (dict(lens_out=P), VALUE), (dict(lens_out=P, table_out=P2), VALUE), (dict(refs_out=P3), VALUE),
+])
+def test_state_validation(op, over, expect):
+    f, more = OPS[op]
+    assert f(**state(**more, **over)) == expect
+
+
+@pytest.mark.parametrize("op,over,expect", [
+    ("fork", dict(n=0), SHAPE), ("fork", dict(n=5), SHAPE), ("fork", dict(src=None), NULL),
+    ("fork", dict(dst=None), NULL), ("release", dict(n=0), SHAPE), ("release", dict(n=5), SHAPE),
+    ("release", dict(which=None), NULL), ("commit", dict(n_acc=None), NULL),
+    ("commit", dict(row_offset=None), NULL), ("reserve", dict(row_offset=None), NULL),
+    ("reserve", dict(missing=None), NULL), ("reserve", dict(k_pages=None), NULL),
+    ("reserve", dict(page_bytes=40), SHAPE), ("reserve", dict(page_bytes=0), SHAPE),
+    ("reserve", dict(v_pages=P + 8), ALIGN), ("compact", dict(n_live=None), NULL),
+    ("compact", dict(v_pages=None), NULL), ("compact", dict(page_bytes=8), SHAPE),
+])
+def test_page_operation_validation(op, over, expect):
+    f, more = OPS[op]
+    assert f(**{**state(**more), **over}) == expect
+
+
+def attend(**over):
+    a = dict(R=4, rows_capacity=12, Hq=8, Hkv=2, D=64, page=16, max_pages=8, n_pages=64,
+             dt=A.DSPARK_BF16, scale=0.125, window=0, q=P, q_stride=512, k_new=P, v_new=P,
+             kv_stride=128, k_pages=P, v_pages=P, k_page_stride=2048, v_page_stride=2048, table=P,
+             row_offset=P, kv_len=P, out=P, lse=P, ws=P, ws_bytes=BIG, stream=None)
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dt=3), DTYPE), (dict(R=0), SHAPE), (dict(rows_capacity=0), SHAPE), (dict(Hq=9), SHAPE),
+    (dict(Hq=1), SHAPE), (dict(Hkv=0), SHAPE), (dict(Hq=2048), SHAPE), (dict(D=80), SHAPE),
+    (dict(D=512), SHAPE), (dict(page=12), SHAPE), (dict(n_pages=0), SHAPE),
+    (dict(row_offset=None), SHAPE), (dict(scale=0.0), VALUE), (dict(scale=float("inf")), VALUE),
+    (dict(window=-1), VALUE), (dict(q=None), NULL), (dict(k_pages=None), NULL),
+    (dict(v_pages=None), NULL), (dict(table=None), NULL), (dict(kv_len=None), NULL),
+    (dict(out=None), NULL), (dict(ws=None), NULL), (dict(k_new=None), NULL), (dict(v_new=None), NULL),
+    (dict(q_stride=504), SHAPE), (dict(q_stride=516), SHAPE), (dict(kv_stride=120), SHAPE),
+    (dict(kv_stride=132), SHAPE), (dict(k_page_stride=2040), SHAPE),
+    (dict(v_page_stride=2052), SHAPE), (dict(q=P + 8), ALIGN), (dict(k_new=P + 2), ALIGN),
+    (dict(v_pages=P + 4), ALIGN), (dict(out=P + 8), ALIGN), (dict(ws_bytes=1024), WS),
+])
+def test_attend_validation(over, expect):
+    assert A.dspark_cache_attend(**attend(**over)) == expect
+
+
+def test_workspace_sizes():
+    assert A.dspark_logprobs_workspace(0, 1000, 0, A.DSPARK_F32) == 0
+    assert A.dspark_logprobs_workspace(4, 151936, 20, 9) == 0
+    assert (A.dspark_logprobs_workspace(64, 151936, 20, A.DSPARK_BF16)
+            > A.dspark_logprobs_workspace(64, 151936, 0, A.DSPARK_BF16) >= 256)
+    assert A.dspark_cache_workspace(0, 5) == 0
+    assert A.dspark_cache_workspace(512, 40000) >= 256 + 4 * (3 * 512 + 3 * 40000)
+    assert A.dspark_cache_attend_workspace(4, 4, 8, 3, 64, 0) == 0
+    assert A.dspark_cache_attend_workspace(4, 4, 8, 2, 64, 0) > 0
+
+
+# ---------------------------------------------------------- the torch wrappers
+def host(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype)
+
+
+I32 = torch.int32
+
+
+@pytest.mark.parametrize("call,error,match", [
+    (lambda: ds.logprobs(host(4, 8, dtype=torch.float16)), TypeError, "bfloat16 or float32"),
+    (lambda: ds.logprobs(host(4)), ValueError, r"\[n_rows\]\[V\]"),
+    (lambda: ds.logprobs(host(4, 7)), ValueError, "16-byte pieces"),
+    (lambda: ds.logprobs(host(8, 4).t()), ValueError, "contiguous past"),
+    (lambda: ds.logprobs(host(4, 8), host(4)), TypeError, "tokens"),
+    (lambda: ds.logprobs(host(4, 8), host(3, dtype=I32)), ValueError, "tokens"),
+    (lambda: ds.logprobs(host(4, 8), host(3, 2, dtype=I32), row_offset=host(3, dtype=I32)),
+     ValueError, "tokens"),
+    (lambda: ds.logprobs(host(4, 8)), ValueError, "not a GPU tensor"),
+    (lambda: ds.logprobs_backward(host(4, 8), host(4, 2), g_logp=host(4)), ValueError, "needs tokens"),
+    (lambda: ds.logprobs_backward(host(4, 8), host(4, 2), g_entropy=host(4)), ValueError, "entropy"),
+    (lambda: ds.logprobs_backward(host(4, 8), host(4, 2), g_top=host(4, 3)), ValueError, "top_ids"),
+    (lambda: ds.cache_fork(host(2, dtype=I32), host(3, dtype=I32), host(4, dtype=I32),
+                           host(4, 8, dtype=I32), host(9, dtype=I32), page=16), ValueError, "dst"),
+    (lambda: ds.cache_commit(host(4, dtype=I32), host(4, dtype=I32), host(4, dtype=I32),
+                             host(4, 8, dtype=I32), host(9, dtype=I32), page=16), ValueError,
+     "row_offset"),
+    (lambda: ds.cache_reserve(host(5, dtype=I32), host(4, dtype=I32), host(4, 8, dtype=I32),
+                              host(9, dtype=I32), host(8, 4), host(9, 4), page=16), ValueError,
+     "k_pages"),
+    (lambda: ds.cache_compact(host(4, dtype=I32), host(4, 8, dtype=I32), host(9, dtype=I32),
+                              host(9, 4), host(9, 8), page=16), ValueError, "same size"),
+    (lambda: ds.cache_attend(host(4, 8, 64), host(9, 2, 16, 64), host(9, 2, 16, 64),
+                             host(4, 8, dtype=I32), host(4, dtype=I32)), ValueError, "v_pages"),
+    (lambda: ds.cache_attend(host(5, 8, 64), host(9, 2, 16, 64), host(9, 2, 64, 16),
+                             host(4, 8, dtype=I32), host(4, dtype=I32)), ValueError, "row_offset"),
+    (lambda: ds.cache_attend(host(4, 8, 64), host(9, 2, 16, 64), host(9, 2, 64, 16),
+                             host(4, 8, dtype=I32), host(4, dtype=I32), k_new=host(4, 2, 64)),
+     ValueError, "both k_new and v_new"),
+    (lambda: ds.cache_attend(host(4, 8, 64), host(9, 2, 16, 64, dtype=torch.bfloat16),
+                             host(9, 2, 64, 16), host(4, 8, dtype=I32), host(4, dtype=I32)),
+     TypeError, "k_pages"),
+])
+def test_wrapper_refusals(call, error, match):
+    with pytest.raises(error, match=match):
+        call()
+
+
+def test_cache_object_refuses_out_of_order():
+    cache = ds.PagedCache(2, 8, Hkv=2, D=64, device="cpu")
+    assert cache.k.shape == (8, 1, 2, 16, 64) and cache.v.shape == (8, 1, 2, 64, 16)
+    with pytest.raises(ValueError, match=r"reserve\(\) comes first"):
+        cache.commit(host(2, dtype=I32))
+    with pytest.raises(ValueError, match=r"reserve\(\) comes first"):
+        cache.attend(0, host(2, 8, 64), host(2, 2, 64), host(2, 2, 64))

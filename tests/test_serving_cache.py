@@ -1,0 +1,336 @@
+"""GPU tests of the page operations: every state, page and refusal against a
+plain model of the definitions in Python lists."""
+import numpy as np
+import pytest
+import torch
+
+import draft_sampling_verification_03_amd as ds
+
+pytestmark = pytest.mark.gpu
+
+LENGTH, PAGE, NO_PAGES = 4, 32, 64
+
+
+class Model:
+    """The definitions, one request and one page at a time."""
+
+    def __init__(self, R, page, width, n_pages, pool):
+        self.page, self.width, self.n = page, width, n_pages
+        self.lens, self.refs = [0] * R, [0] * n_pages
+        self.table = [[-1] * width for _ in range(R)]
+        self.k, self.v = pool[0].copy(), pool[1].copy()
+
+    def pages(self, n):
+        return -(-n // self.page)
+
+    def fork(self, src, dst):
+        lens = list(self.lens)
+        seen = set()
+        for s, d in zip(src, dst):
+            if not (0 <= s < len(lens) and 0 <= d < len(lens)) or lens[d] or d in seen:
+                continue
+            seen.add(d)
+            self.lens[d] = lens[s]
+            for i in range(self.pages(lens[s])):
+                self.table[d][i] = self.table[s][i]
+                self.refs[self.table[s][i]] += 1
+
+    def reserve(self, new):
+        """Pages missing (0: done)."""
+        tails = {}
+        for r, n in enumerate(new):
+            if self.lens[r] + n > self.page * self.width or n < 0:
+                return -1
+            if n and self.lens[r] % self.page:
+                tails.setdefault(self.table[r][self.lens[r] // self.page], []).append(r)
+        copies = [r for p, rs in tails.items() for r in rs
+                  if self.refs[p] > 1 and not (len(rs) == self.refs[p] and r == rs[0])]
+        need = len(copies) + sum(self.pages(self.lens[r] + n) - self.pages(self.lens[r])
+                                 for r, n in enumerate(new))
+        free = [p for p in range(self.n) if not self.refs[p]]
+        if need > len(free):
+            return need - len(free)
+        free = iter(free)
+        for r, n in enumerate(new):
+            if r in copies:
+                i = self.lens[r] // self.page
+                p, q = self.table[r][i], next(free)
+                self.k[q], self.v[q] = self.k[p], self.v[p]
+                self.refs[p] -= 1
+                self.refs[q], self.table[r][i] = 1, q
+            for i in range(self.pages(self.lens[r]), self.pages(self.lens[r] + n)):
+                q = self.table[r][i] = next(free)
+                self.refs[q] = 1
+            self.lens[r] += n
+        return 0
+
+    def cut(self, r, n):
+        for i in range(self.pages(n), self.pages(self.lens[r])):
+            self.refs[self.table[r][i]] -= 1
+            self.table[r][i] = -1
+        self.lens[r] = n
+
+    def compact(self):
+        live = sum(1 for c in self.refs if c)
+        holes = [p for p in range(live) if not self.refs[p]]
+        to = {}
+        for p in range(live, self.n):
+            if self.refs[p]:
+                to[p] = holes[len(to)]
+        for p, h in to.items():
+            self.k[h], self.v[h] = self.k[p], self.v[p]
+            self.refs[h], self.refs[p] = self.refs[p], 0
+        self.table = [[to.get(p, p) for p in row] for row in self.table]
+        return live
+
+
+def cu(a):
+    return torch.tensor(list(a), dtype=torch.int32, device="cuda")
+
+
+class Device:
+    """The same through the library; in place, or into new arrays every time."""
+
+    def __init__(self, R, page, width, n_pages, pool, in_place):
+        self.page, self.in_place = page, in_place
+        self.s = dict(lens=cu([0] * R), refs=cu([0] * n_pages),
+                      table=torch.full((R, width), -1, dtype=torch.int32, device="cuda"))
+        self.k, self.v = (torch.from_numpy(a).cuda() for a in pool)
+        self.ws = ds.Workspace()
+
+    def call(self, f, *args, pools=False):
+        s = self.s
+        pool = (self.k, self.v) if pools else ()
+        before = {k: t.clone() for k, t in s.items()}
+        o = f(*args, s["lens"], s["table"], s["refs"], *pool, page=self.page, ws=self.ws,
+              out=dict(s) if self.in_place else None)
+        if not self.in_place:
+            for name, t in s.items():
+                assert torch.equal(t, before[name]), name
+        self.s = {k: o[k] for k in s}
+        return o
+
+    def check(self, m, error=0):
+        assert self.s["lens"].tolist() == m.lens
+        assert self.s["refs"].tolist() == m.refs
+        assert self.s["table"].tolist() == m.table
+        assert np.array_equal(self.k.cpu().numpy(), m.k) and np.array_equal(self.v.cpu().numpy(), m.v)
+        assert self.ws.error_code() == error
+        if error:
+            self.ws.clear_error()
+
+
+def offsets(new, first=0):
+    return cu(np.concatenate(([first], first + np.cumsum(new))).astype(int))
+
+
+def both(R, page, width, n_pages, in_place, elems=(4, 12), seed=0):
+    """elems: int32 values of a page, in one or more dimensions."""
+    rng = np.random.default_rng(seed)
+    pool = [rng.integers(-2 ** 31, 2 ** 31, (n_pages, *elems)).astype(np.int32) for _ in range(2)]
+    return Model(R, page, width, n_pages, pool), Device(R, page, width, n_pages, pool, in_place), rng
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("R,page,width,n_pages,elems", [
+    (1, 16, 3, 1, (4,)), (5, 16, 9, 40, (4, 12)), (40, 32, 6, 131, (7, 100)), (70, 64, 3, 1000, (4,)),
+    (1500, 16, 4, 5003, (4,))])
+def test_rounds(R, page, width, n_pages, elems, in_place):
+    """Random rounds of forks, reservations, commits, releases and compactions."""
+    m, d, rng = both(R, page, width, n_pages, in_place, elems, seed=R)
+    for step in range(12 if R < 1000 else 4):
+        empty = [r for r in range(R) if not m.lens[r]]
+        full = [r for r in range(R) if m.lens[r]]
+        if empty and full and step % 2:
+            k = int(rng.integers(1, min(len(empty), 6) + 1))
+            dst, src = list(rng.permutation(empty)[:k]), list(rng.choice(full, k))
+            m.fork(src, dst)
+            d.call(ds.cache_fork, cu(src), cu(dst))
+            d.check(m)
+        room = [page * width - n for n in m.lens]
+        new = [int(min(rng.integers(0, 2 * page), q)) if rng.random() < 0.7 else 0 for q in room]
+        off = offsets(new)
+        missing = m.reserve(new)
+        o = d.call(ds.cache_reserve, off, pools=True)
+        assert o["missing"].item() == missing
+        d.check(m, NO_PAGES if missing else 0)
+        if not missing:
+            acc = [int(rng.integers(-1, n)) for n in new]
+            for r in range(R):
+                m.cut(r, m.lens[r] - new[r] + acc[r] + 1)
+            d.call(ds.cache_commit, off, cu(acc))
+            d.check(m)
+        if missing or step % 3 == 2:
+            leave = [int(r) for r in rng.permutation(R)[: max(1, R // 3)]]
+            for r in leave:
+                m.cut(r, 0)
+            d.call(ds.cache_release, cu(leave))
+            d.check(m)
+        if step % 4 == 3:
+            live = m.compact()
+            o = d.call(ds.cache_compact, pools=True)
+            assert o["n_live"].item() == live
+            d.check(m)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_shared_last_pages(in_place):
+    """A shared, partly filled page: copied by every writer when somebody else
+    keeps holding it, kept by the first when all write; a full page is never
+    copied, nor a page whose only writer appends nothing."""
+    m, d, _ = both(6, 16, 4, 30, in_place)
+    for args in ([20, 0, 0, 32, 0, 0],):
+        m.reserve(args)
+        d.call(ds.cache_reserve, offsets(args), pools=True)
+    m.fork([0, 0, 3, 0], [1, 2, 4, 5])
+    d.call(ds.cache_fork, cu([0, 0, 3, 0]), cu([1, 2, 4, 5]))
+    d.check(m)
+    for new in ([1, 0, 3, 1, 1, 0], [1, 1, 1, 1, 1, 1], [0, 5, 0, 0, 0, 5]):
+        assert m.reserve(new) == 0
+        d.call(ds.cache_reserve, offsets(new, first=7), pools=True)
+        d.check(m)
+    assert sorted(m.refs)[-2:] == [4, 2] or max(m.refs) >= 2
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_all_writers_of_a_page(in_place):
+    m, d, _ = both(3, 16, 2, 5, in_place)
+    m.reserve([3, 0, 0])
+    d.call(ds.cache_reserve, offsets([3, 0, 0]), pools=True)
+    m.fork([0, 0], [2, 1])
+    d.call(ds.cache_fork, cu([0, 0]), cu([2, 1]))
+    assert m.reserve([2, 2, 2]) == 0
+    o = d.call(ds.cache_reserve, offsets([2, 2, 2]), pools=True)
+    assert o["missing"].item() == 0 and m.table[0][0] == 0 and m.refs[:3] == [1, 1, 1]
+    d.check(m)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_forks_that_are_skipped(in_place):
+    m, d, _ = both(5, 16, 4, 30, in_place)
+    m.reserve([18, 5, 0, 0, 0])
+    d.call(ds.cache_reserve, offsets([18, 5, 0, 0, 0]), pools=True)
+    # the same destination twice (the first counts), itself, a full one, numbers out of range
+    src, dst = [0, 1, 2, 0, -1], [3, 3, 2, 1, 4]
+    m.fork(src, dst)
+    d.call(ds.cache_fork, cu(src), cu(dst))
+    assert m.lens == [18, 5, 0, 18, 0]
+    d.check(m, LENGTH)
+    # a source that is a destination too counts as it was: empty
+    src, dst = [0, 2], [2, 4]
+    m.fork(src, dst)
+    d.call(ds.cache_fork, cu(src), cu(dst))
+    assert m.lens == [18, 5, 18, 18, 0]
+    d.check(m)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_release_twice_and_out_of_range(in_place):
+    m, d, _ = both(4, 16, 4, 30, in_place)
+    m.reserve([18, 5, 16, 1])
+    d.call(ds.cache_reserve, offsets([18, 5, 16, 1]), pools=True)
+    for r in (2, 0):
+        m.cut(r, 0)
+    d.call(ds.cache_release, cu([2, 0, 2]))
+    d.check(m)
+    d.call(ds.cache_release, cu([9, -1, 2]))
+    d.check(m, LENGTH)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_lengths_out_of_bounds(in_place):
+    m, d, _ = both(3, 16, 2, 30, in_place)
+    m.reserve([18, 5, 0])
+    d.call(ds.cache_reserve, offsets([18, 5, 0]), pools=True)
+    # past max_pages; a decreasing row_offset; each leaves everything as it was
+    for off in ([0, 1, 30, 30], [0, 1, 0, 0]):
+        assert d.call(ds.cache_reserve, cu(off), pools=True)["missing"].item() == -1
+        d.check(m, LENGTH)
+    # commits that keep more than was reserved, less than none, or reserve more than there is
+    for new, acc in (([2, 0, 0], [2, -1, -1]), ([2, 0, 0], [-2, -1, -1]), ([19, 0, 0], [0, -1, -1])):
+        d.call(ds.cache_commit, offsets(new), cu(acc))
+        d.check(m, LENGTH)
+
+
+def test_bad_pages_are_not_followed():
+    m, d, _ = both(3, 16, 3, 8, True)
+    m.reserve([20, 20, 0])
+    d.call(ds.cache_reserve, offsets([20, 20, 0]), pools=True)
+    d.s["table"][0, 1] = 8
+    d.s["table"][1, 1] = -7
+    d.call(ds.cache_reserve, offsets([1, 1, 0]), pools=True)
+    assert d.ws.error_code() == PAGE
+    assert d.s["lens"].tolist() == [21, 21, 0]
+    d.ws.clear_error()
+    d.call(ds.cache_fork, cu([0]), cu([2]))
+    assert d.ws.error_code() == PAGE and d.s["refs"].tolist()[:4] == [2, 1, 1, 1]
+    d.ws.clear_error()
+    d.call(ds.cache_compact, pools=True)
+    assert d.ws.error_code() in (0, PAGE)
+    d.call(ds.cache_release, cu([0, 1, 2]))
+    assert d.ws.error_code() == PAGE
+    assert d.s["lens"].tolist() == [0, 0, 0] and (d.s["table"] == -1).all()
+
+
+def test_state_without_pools_and_compact_of_nothing():
+    m, d, _ = both(4, 16, 4, 9, True)
+    assert ds.cache_compact(d.s["lens"], d.s["table"], d.s["refs"], None, None, page=16,
+                            ws=d.ws)["n_live"].item() == 0
+    m.reserve([30, 2, 0, 9])
+    ds.cache_reserve(offsets([30, 2, 0, 9]), d.s["lens"], d.s["table"], d.s["refs"], None, None,
+                     page=16, ws=d.ws, out=dict(d.s))
+    d.check(m)
+
+
+def test_many_pages():
+    """A pool whose scan takes many steps, its free pages far up and odd ends."""
+    n, R = 300001, 3
+    refs = torch.ones(n, dtype=torch.int32, device="cuda")
+    free = torch.tensor([5, 4095, 4096, 150000, 299999, 300000], device="cuda")
+    refs[free] = 0
+    lens = cu([0, 0, 0])
+    table = torch.full((R, 4), -1, dtype=torch.int32, device="cuda")
+    o = ds.cache_reserve(offsets([17, 1, 33]), lens, table, refs, None, None, page=16)
+    assert o["table"].tolist() == [[5, 4095, -1, -1], [4096, -1, -1, -1], [150000, 299999, 300000, -1]]
+    assert o["missing"].item() == 0 and int(o["refs"].min()) == 1
+    ws = ds.Workspace()
+    o2 = ds.cache_reserve(offsets([0, 16, 0]), o["lens"], o["table"], o["refs"], None, None, page=16, ws=ws)
+    assert o2["missing"].item() == 1 and ws.error_code() == NO_PAGES
+    assert torch.equal(o2["table"], o["table"]) and torch.equal(o2["lens"], o["lens"])
+
+
+def test_captured_round_replays():
+    """One captured round, replayed with other counts and eager work in between."""
+    m, d, rng = both(6, 16, 8, 60, True)
+    off, acc = offsets([1] * 6), cu([0] * 6)
+
+    def go():
+        d.call_(ds.cache_reserve, off, pools=True)
+        d.call_(ds.cache_commit, off, acc)
+
+    def call_(f, *args, pools=False):
+        s = d.s
+        f(*args, s["lens"], s["table"], s["refs"], *((d.k, d.v) if pools else ()), page=16, ws=d.ws,
+          out=dict(s, missing=missing))
+
+    missing = cu([0])
+    d.call_ = call_
+    go()  # the workspace is made here
+    m.reserve([1] * 6)
+    d.check(m)
+    m.fork([0], [1]) if not m.lens[1] else None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for _ in range(5):
+        new = [int(rng.integers(0, 20)) for _ in range(6)]
+        off.copy_(offsets(new))
+        a = [int(rng.integers(-1, n)) for n in new]
+        acc.copy_(cu(a))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert m.reserve(new) == 0
+        for r in range(6):
+            m.cut(r, m.lens[r] - new[r] + a[r] + 1)
+        d.check(m)
