@@ -7,52 +7,101 @@ happens here.  Logit rows, queries, new keys and values and a layer's pages may
 be strided in their first dimension (a slice of a wider buffer); everything
 else is contiguous.
 """
-import contextlib
+import functools
 
 import torch
 
 from . import _abi as A
-from .api import F32, I32, Workspace, _Args, _check, _dt, _empty, _on_stream, _outputs
+from .api import F32, I32, Workspace, _Args, _check, _dt, _empty, _on_stream
 
 _PER = {torch.bfloat16: 8, torch.float32: 4}  # elements of 16 bytes
 
+# these calls take a few microseconds on the device, so the host's share counts:
+# the size queries are pure functions of their arguments and are asked once
+_logprobs_ws = functools.lru_cache(1024)(A.dspark_logprobs_workspace)
+_cache_ws = functools.lru_cache(1024)(A.dspark_cache_workspace)
+_attend_ws = functools.lru_cache(1024)(A.dspark_cache_attend_workspace)
+
 
 class _RowArgs(_Args):
+    """_Args with a short way for arguments that are right (what is not goes
+    through _Args.req, which says why), and for row strides."""
+
+    def req(self, t, name, dtype, shape, optional=False):
+        if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            self.tensors.append((name, t))
+            return t
+        return super().req(t, name, dtype, shape, optional)
+
     def rows(self, t, name, dtype, shape, optional=False):
         """As req, but the first dimension may have any stride of whole 16-byte
-        pieces that keeps its entries apart; returns (tensor, that stride)."""
+        pieces that keeps its entries apart; returns that stride."""
         if t is None and optional:
-            return None, 0
-        if not isinstance(t, torch.Tensor) or t.is_contiguous() and t.dim() == len(shape) > 1 \
-                and t[:1].numel() % _PER.get(t.dtype, 1) == 0:
+            return 0
+        if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape:
             self.req(t, name, dtype, shape)
-            return t, t.stride(0) if t.shape[0] > 1 else t[:1].numel()
-        if t.dtype != dtype or t.dim() != len(shape) or any(
-                s is not None and s != d for s, d in zip(shape, t.shape)):
-            self.req(t, name, dtype, shape)
-        one = t[0].numel() if t.shape[0] else 0
-        if t.shape[0] and not t[0].is_contiguous():
+        per = _PER[dtype]
+        one = 1
+        for n in shape[1:]:
+            one *= n
+        if shape[0] > 1:
+            stride = t.stride(0)
+            inner = t.is_contiguous() or t[0].is_contiguous()
+        else:
+            stride, inner = -(-one // per) * per, t.is_contiguous()
+        if not inner:
             raise ValueError(f"{self.where}: {name} must be contiguous past its first dimension")
-        stride = t.stride(0) if t.shape[0] > 1 else -(-one // _PER[dtype]) * _PER[dtype]
-        if stride < one or stride % _PER[dtype]:
+        if stride < one or stride % per:
             raise ValueError(f"{self.where}: {name} must have rows of whole 16-byte pieces "
                              f"(stride {stride} elements for rows of {one})")
         self.tensors.append((name, t))
-        return t, stride
+        return stride
+
+    def gpu(self):
+        """Index of the one GPU that every tensor checked so far is on."""
+        index = self.tensors[0][1].get_device()
+        for _, t in self.tensors:
+            if t.get_device() != index or index < 0:
+                self.device()
+        return index
 
 
-@contextlib.contextmanager
-def _guard(dev):
-    with torch.cuda.device(dev):
-        yield
+def _width(a, t, name):
+    """Last dimension of a tensor whose other sizes are checked afterwards."""
+    if not isinstance(t, torch.Tensor) or t.dim() == 0:
+        a.req(t, name, I32, (None,))
+        raise ValueError(f"{a.where}: {name} must have a dimension")
+    return t.shape[-1]
 
 
-def _run(dev, stream, call):
-    """call(stream) with the tensors' device current."""
-    if dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream() if stream is None else stream)
-    with _guard(dev):
-        return call(torch.cuda.current_stream() if stream is None else stream)
+def _outs(a, out, spec, dev):
+    """Outputs {name: (shape, dtype)}: new, or the caller's checked."""
+    if out is None:
+        return {n: _empty(s, t, dev) for n, (s, t) in spec.items()}
+    for n, (s, t) in spec.items():
+        a.req(out.get(n), f"out[{n!r}]", t, s)
+    return out
+
+
+def _workspace(ws, nbytes, dev, index, stream):
+    """(keeps alive, address, bytes) of the call's workspace."""
+    if ws is None:
+        ws = Workspace(dev)
+    buf = ws.buf
+    if stream is not None or buf is None or buf.get_device() != index or buf.numel() < nbytes:
+        buf = ws.get(nbytes, stream, dev)
+    return buf
+
+
+def _launch(name, index, stream, call):
+    """call(stream handle) with the tensors' device current."""
+    if index == torch.cuda.current_device():
+        st = call(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+    else:
+        with torch.cuda.device(index):
+            st = call(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+    if st:
+        _check(st, name)
 
 
 def _check_tokens(a, tokens, row_offset, n_rows):
@@ -60,43 +109,49 @@ def _check_tokens(a, tokens, row_offset, n_rows):
     if row_offset is None:
         a.req(tokens, "tokens", I32, (n_rows,), optional=True)
         return 0, 0
-    a.req(row_offset, "row_offset", I32, (None,))
-    R = row_offset.shape[0] - 1
+    R = _width(a, row_offset, "row_offset") - 1
+    a.req(row_offset, "row_offset", I32, (R + 1,))
     if R < 1:
         raise ValueError(f"{a.where}: row_offset must have shape [R + 1]")
     if tokens is None:
         return R, 0
-    a.req(tokens, "tokens", I32, (R, None))
-    return R, tokens.shape[1]
+    w = _width(a, tokens, "tokens")
+    a.req(tokens, "tokens", I32, (R, w))
+    return R, w
 
 
 def logprobs(X, tokens=None, *, k=0, row_offset=None, temp=1.0, ws=None, stream=None, out=None):
     """X [n_rows][V] logits (rows may be strided); tokens [n_rows] int32, or with
     row_offset [R + 1] the verified batch's layout [R][w] (y of verify()), -1
     for no token.  Returns logp (None without tokens), entropy and stats
-    [n_rows][2] = (m, S), and with k > 0 top_ids and top_logp [n_rows][k].
-    Rows from row_offset[R] on keep what `out` held (undefined without `out`)."""
+    [n_rows][2] = (m, S), top_ids and top_logp [n_rows][k] (None for k = 0).  Rows from
+    row_offset[R] on keep what `out` held (undefined without `out`)."""
     a = _RowArgs("logprobs")
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("logprobs: X must be a [n_rows][V] tensor")
     dt = _dt(X)
     n, V = X.shape
-    _, stride = a.rows(X, "X", X.dtype, (n, V))
-    R, w = _check_tokens(a, tokens, row_offset, n)
-    dev = a.device()
     k = int(k)
+    stride = a.rows(X, "X", X.dtype, (n, V))
+    R, w = _check_tokens(a, tokens, row_offset, n)
+    index, dev = a.gpu(), X.device
+    spec = {"entropy": ((n,), F32), "stats": ((n, 2), F32)}
+    if tokens is not None:
+        spec["logp"] = ((n,), F32)
+    if k > 0:
+        spec["top_ids"], spec["top_logp"] = ((n, k), I32), ((n, k), F32)
     with _on_stream(stream):
-        out = _outputs(a, out, dict(logp=((n,), F32) if tokens is not None else None,
-                                    entropy=((n,), F32), stats=((n, 2), F32),
-                                    top_ids=((n, k), I32) if k > 0 else None,
-                                    top_logp=((n, k), F32) if k > 0 else None), dev)
-        a.device()
-        ws = ws or Workspace(dev)
-        buf = ws.get(A.dspark_logprobs_workspace(n, V, k, dt), stream, dev)
-    st = _run(dev, stream, lambda s: A.dspark_logprobs(
-        n, V, stride, dt, float(temp), X, tokens, w, R, row_offset, k, out.get("logp"),
-        out["entropy"], out["stats"], out.get("top_ids"), out.get("top_logp"), buf, buf.numel(), s))
-    _check(st, "dspark_logprobs")
+        out = _outs(a, out, spec, dev)
+        for name in ("logp", "top_ids", "top_logp"):
+            if name not in spec:
+                out.setdefault(name, None)
+        a.gpu()
+        buf = _workspace(ws, _logprobs_ws(n, V, k, dt), dev, index, stream)
+    top = (out["top_ids"], out["top_logp"]) if k > 0 else (None, None)
+    _launch("dspark_logprobs", index, stream, lambda s: A.dspark_logprobs(
+        n, V, stride, dt, temp, X, tokens, w, R, row_offset, k,
+        out["logp"] if tokens is not None else None, out["entropy"], out["stats"], *top, buf,
+        buf.numel(), s))
     return out
 
 
@@ -111,7 +166,7 @@ def logprobs_backward(X, stats, entropy=None, *, tokens=None, g_logp=None, g_ent
         raise ValueError("logprobs_backward: X must be a [n_rows][V] tensor")
     dt = _dt(X)
     n, V = X.shape
-    _, stride = a.rows(X, "X", X.dtype, (n, V))
+    stride = a.rows(X, "X", X.dtype, (n, V))
     R, w = _check_tokens(a, tokens, row_offset, n)
     a.req(stats, "stats", F32, (n, 2))
     a.req(entropy, "entropy", F32, (n,), optional=g_entropy is None)
@@ -126,95 +181,98 @@ def logprobs_backward(X, stats, entropy=None, *, tokens=None, g_logp=None, g_ent
         a.req(top_ids, "top_ids", I32, (n, k))
     if g_logp is not None and tokens is None:
         raise ValueError("logprobs_backward: g_logp needs tokens")
-    dev = a.device()
+    index, dev = a.gpu(), X.device
     with _on_stream(stream):
         if out is None:
             per = _PER[X.dtype]
             out = _empty((n, -(-V // per) * per), X.dtype, dev)[:, :V]
-        _, dx_stride = a.rows(out, "out", X.dtype, (n, V))
-        a.device()
-        ws = ws or Workspace(dev)
-        buf = ws.get(256, stream, dev)
-    st = _run(dev, stream, lambda s: A.dspark_logprobs_backward(
-        n, V, stride, dt, float(temp), X, tokens if g_logp is not None else None, w, R, row_offset,
-        stats, entropy, g_logp, g_entropy, k, top_ids if k else None, g_top, out, dx_stride, buf,
-        buf.numel(), s))
-    _check(st, "dspark_logprobs_backward")
+        dx_stride = a.rows(out, "out", X.dtype, (n, V))
+        a.gpu()
+        buf = _workspace(ws, 256, dev, index, stream)
+    _launch("dspark_logprobs_backward", index, stream, lambda s: A.dspark_logprobs_backward(
+        n, V, stride, dt, temp, X, tokens if g_logp is not None else None, w, R, row_offset,
+        stats, entropy, g_logp, g_entropy, k, top_ids if k else None, g_top if k else None, out,
+        dx_stride, buf, buf.numel(), s))
     return out
 
 
 # -------------------------------------------------------------------- pages
-def _state(a, lens, table, refs):
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError(f"{a.where}: table must be a [R][max_pages] tensor")
-    R, width = table.shape
-    a.req(table, "table", I32, (R, width))
-    a.req(lens, "lens", I32, (R,))
-    a.req(refs, "refs", I32, (None,))
-    return R, width, refs.shape[0]
+class _State:
+    """The state of a page operation, checked, with its outputs and workspace:
+    in place when `out` names the inputs, else new or the caller's arrays."""
+
+    def __init__(self, where, lens, table, refs, others):
+        self.a = a = _RowArgs(where)
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError(f"{where}: table must be a [R][max_pages] tensor")
+        self.R, self.width = table.shape
+        self.n_pages = _width(a, refs, "refs")
+        self.ins = (lens, table, refs)
+        self.shapes = ((self.R,), (self.R, self.width), (self.n_pages,))
+        for t, name, shape in zip(self.ins, _NAMES, self.shapes):
+            a.req(t, name, I32, shape)
+        for t, name, shape in others(self):
+            a.req(t, name, I32, shape)
+
+    def pools(self, k_pages, v_pages):
+        """Bytes of a page in each pool (None both: numbers only)."""
+        if k_pages is None and v_pages is None:
+            return 0
+        size = []
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if not isinstance(t, torch.Tensor) or t.dim() < 2 or t.shape[0] != self.n_pages:
+                raise ValueError(f"{self.a.where}: {name} must be a [n_pages = {self.n_pages}][...] "
+                                 "tensor")
+            self.a.req(t, name, t.dtype, t.shape)
+            size.append(t.numel() // self.n_pages * t.element_size())
+        if size[0] != size[1]:
+            raise ValueError(f"{self.a.where}: k_pages and v_pages must have pages of the same size")
+        return size[0]
+
+    def run(self, name, page, ws, stream, out, before, after=(), extra=None):
+        """Calls dspark_<name>; `extra` is the one-element output beside the state."""
+        a = self.a
+        index, dev = a.gpu(), self.ins[1].device
+        with _on_stream(stream):
+            o = {}
+            if out is None:
+                for n, shape in zip(_NAMES, self.shapes):
+                    o[n] = _empty(shape, I32, dev)
+            else:
+                same = 0
+                for n, t, shape in zip(_NAMES, self.ins, self.shapes):
+                    o[n] = out.get(n)
+                    if o[n] is t:
+                        same += 1
+                    else:
+                        a.req(o[n], f"out[{n!r}]", I32, shape)
+                        same += o[n].data_ptr() == t.data_ptr()
+                if same not in (0, 3):
+                    raise ValueError(f"{a.where}: lens, table and refs change in place all three or "
+                                     "none")
+            if extra is not None:
+                t = None if out is None else out.get(extra)
+                o[extra] = _empty((1,), I32, dev) if t is None else a.req(t, f"out[{extra!r}]", I32, (1,))
+                after = (*after, o[extra])
+            a.gpu()
+            buf = _workspace(ws, _cache_ws(self.R, self.n_pages), dev, index, stream)
+        call = getattr(A, name)
+        _launch(name, index, stream, lambda s: call(
+            self.R, page, self.width, self.n_pages, *before, *self.ins, o["lens"], o["table"],
+            o["refs"], *after, buf, buf.numel(), s))
+        return o
 
 
-def _pools(a, k_pages, v_pages, n_pages):
-    """Bytes of a page in each pool (None both: numbers only)."""
-    if k_pages is None and v_pages is None:
-        return 0
-    size = []
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not isinstance(t, torch.Tensor) or t.dim() < 2 or t.shape[0] != n_pages:
-            raise ValueError(f"{a.where}: {name} must be a [n_pages = {n_pages}][...] tensor")
-        a.req(t, name, t.dtype, t.shape)
-        size.append(t[0].numel() * t.element_size())
-    if size[0] != size[1]:
-        raise ValueError(f"{a.where}: k_pages and v_pages must have pages of the same size")
-    return size[0]
-
-
-def _state_out(a, out, lens, table, refs):
-    spec = dict(lens=(lens.shape, I32), table=(table.shape, I32), refs=(refs.shape, I32))
-    out = dict(_outputs(a, out, spec, lens.device))
-    same = [out[n].data_ptr() == t.data_ptr()
-            for n, t in (("lens", lens), ("table", table), ("refs", refs))]
-    if any(same) and not all(same):
-        raise ValueError(f"{a.where}: lens, table and refs change in place all three or none")
-    return out
-
-
-def _cache_call(where, name, page, lens, table, refs, ws, stream, out, extra, args):
-    """Checks the state (after the caller's own arguments, given by `extra`),
-    makes the outputs and calls dspark_<name>; args(a, s, o, buf) gives the
-    arguments behind the sizes."""
-    a = _RowArgs(where)
-    R, width, n_pages = _state(a, lens, table, refs)
-    extra(a, R, n_pages)
-    dev = a.device()
-    with _on_stream(stream):
-        o = _state_out(a, out, lens, table, refs)
-        a.device()
-        ws = ws or Workspace(dev)
-        buf = ws.get(A.dspark_cache_workspace(R, n_pages), stream, dev)
-        tail = args(o, dev)
-    st = _run(dev, stream, lambda s: getattr(A, name)(R, int(page), width, n_pages, *tail[0], lens,
-                                                      table, refs, o["lens"], o["table"], o["refs"],
-                                                      *tail[1], buf, buf.numel(), s))
-    _check(st, name)
-    return o
-
-
-def _one(o, name, out, dev):
-    """A one-element result beside the state: the caller's or a new one."""
-    t = None if out is None else out.get(name)
-    o[name] = _empty((1,), I32, dev) if t is None else t
-    return o[name]
+_NAMES = ("lens", "table", "refs")
 
 
 def cache_fork(src, dst, lens, table, refs, *, page, ws=None, stream=None, out=None):
     """Requests dst[i] become copies of src[i] that share their pages.  Returns
     the state (lens, table, refs); `out` may name the inputs (in place)."""
-    def extra(a, R, n_pages):
-        a.req(src, "src", I32, (None,))
-        a.req(dst, "dst", I32, (src.shape[0],))
-    return _cache_call("cache_fork", "dspark_cache_fork", page, lens, table, refs, ws, stream, out,
-                       extra, lambda o, dev: ((src.shape[0], src, dst), ()))
+    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else None
+    s = _State("cache_fork", lens, table, refs,
+               lambda s: ((src, "src", (n,)), (dst, "dst", (n,))))
+    return s.run("dspark_cache_fork", page, ws, stream, out, (n, src, dst))
 
 
 def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=None,
@@ -222,50 +280,35 @@ def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=N
     """Pages for row_offset[r + 1] - row_offset[r] new tokens of every request.
     k_pages, v_pages: the whole pools, [n_pages][...] (None both: the state
     alone).  Returns the state and missing [1] (0: done)."""
-    size = [0]
-
-    def extra(a, R, n_pages):
-        a.req(row_offset, "row_offset", I32, (R + 1,))
-        size[0] = _pools(a, k_pages, v_pages, n_pages)
-        if out is not None and out.get("missing") is not None:
-            a.req(out["missing"], "out['missing']", I32, (1,))
-
-    return _cache_call("cache_reserve", "dspark_cache_reserve", page, lens, table, refs, ws, stream,
-                       out, extra, lambda o, dev: ((row_offset,), (k_pages, v_pages, size[0],
-                                                                   _one(o, "missing", out, dev))))
+    s = _State("cache_reserve", lens, table, refs,
+               lambda s: ((row_offset, "row_offset", (s.R + 1,)),))
+    size = s.pools(k_pages, v_pages)
+    return s.run("dspark_cache_reserve", page, ws, stream, out, (row_offset,),
+                 (k_pages, v_pages, size), "missing")
 
 
 def cache_commit(row_offset, n_acc, lens, table, refs, *, page, ws=None, stream=None, out=None):
     """After verify(): of the rows that cache_reserve made room for, the first
     n_acc + 1 stay.  Returns the state."""
-    def extra(a, R, n_pages):
-        a.req(row_offset, "row_offset", I32, (R + 1,))
-        a.req(n_acc, "n_acc", I32, (R,))
-    return _cache_call("cache_commit", "dspark_cache_commit", page, lens, table, refs, ws, stream,
-                       out, extra, lambda o, dev: ((row_offset, n_acc), ()))
+    s = _State("cache_commit", lens, table, refs,
+               lambda s: ((row_offset, "row_offset", (s.R + 1,)), (n_acc, "n_acc", (s.R,))))
+    return s.run("dspark_cache_commit", page, ws, stream, out, (row_offset, n_acc))
 
 
 def cache_release(which, lens, table, refs, *, page, ws=None, stream=None, out=None):
     """Requests `which` leave and give their pages back.  Returns the state."""
-    def extra(a, R, n_pages):
-        a.req(which, "which", I32, (None,))
-    return _cache_call("cache_release", "dspark_cache_release", page, lens, table, refs, ws, stream,
-                       out, extra, lambda o, dev: ((which.shape[0], which), ()))
+    n = which.shape[0] if isinstance(which, torch.Tensor) and which.dim() == 1 else None
+    s = _State("cache_release", lens, table, refs, lambda s: ((which, "which", (n,)),))
+    return s.run("dspark_cache_release", page, ws, stream, out, (n, which))
 
 
 def cache_compact(lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=None, out=None):
     """Moves the pages in use to the front of the pools.  Returns the state and
     n_live [1]."""
-    size = [0]
-
-    def extra(a, R, n_pages):
-        size[0] = _pools(a, k_pages, v_pages, n_pages)
-        if out is not None and out.get("n_live") is not None:
-            a.req(out["n_live"], "out['n_live']", I32, (1,))
-
-    return _cache_call("cache_compact", "dspark_cache_compact", page, lens, table, refs, ws, stream,
-                       out, extra, lambda o, dev: ((), (k_pages, v_pages, size[0],
-                                                        _one(o, "n_live", out, dev))))
+    s = _State("cache_compact", lens, table, refs, lambda s: ())
+    size = s.pools(k_pages, v_pages)
+    return s.run("dspark_cache_compact", page, ws, stream, out, (), (k_pages, v_pages, size),
+                 "n_live")
 
 
 # ---------------------------------------------------------------- attention
@@ -282,36 +325,36 @@ def cache_attend(q, k_pages, v_pages, table, kv_len, *, row_offset=None, k_new=N
         raise ValueError("cache_attend: q must be a [rows][Hq][D] tensor")
     dt = _dt(q)
     n, Hq, D = q.shape
-    _, q_stride = a.rows(q, "q", q.dtype, (n, Hq, D))
+    q_stride = a.rows(q, "q", q.dtype, (n, Hq, D))
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("cache_attend: k_pages must be a [n_pages][Hkv][page][D] tensor")
     n_pages, Hkv, page, _ = k_pages.shape
-    _, k_stride = a.rows(k_pages, "k_pages", q.dtype, (n_pages, Hkv, page, D))
-    _, v_stride = a.rows(v_pages, "v_pages", q.dtype, (n_pages, Hkv, D, page))
-    a.req(kv_len, "kv_len", I32, (None,))
-    R = kv_len.shape[0]
-    a.req(table, "table", I32, (R, None))
-    a.req(row_offset, "row_offset", I32, (R + 1,), optional=True)
-    if row_offset is None and n != R:
+    k_stride = a.rows(k_pages, "k_pages", q.dtype, (n_pages, Hkv, page, D))
+    v_stride = a.rows(v_pages, "v_pages", q.dtype, (n_pages, Hkv, D, page))
+    R, width = _width(a, kv_len, "kv_len"), _width(a, table, "table")
+    a.req(kv_len, "kv_len", I32, (R,))
+    a.req(table, "table", I32, (R, width))
+    if row_offset is not None:
+        a.req(row_offset, "row_offset", I32, (R + 1,))
+    elif n != R:
         raise ValueError(f"cache_attend: {n} rows for {R} requests need row_offset")
     if (k_new is None) != (v_new is None):
         raise ValueError("cache_attend: give both k_new and v_new, or neither")
-    _, kn = a.rows(k_new, "k_new", q.dtype, (n, Hkv, D), optional=True)
-    _, vn = a.rows(v_new, "v_new", q.dtype, (n, Hkv, D), optional=True)
+    kn = a.rows(k_new, "k_new", q.dtype, (n, Hkv, D), optional=True)
+    vn = a.rows(v_new, "v_new", q.dtype, (n, Hkv, D), optional=True)
     if kn != vn:
         raise ValueError("cache_attend: k_new and v_new must have the same row stride")
-    dev = a.device()
+    index, dev = a.gpu(), q.device
     with _on_stream(stream):
-        out = _outputs(a, out, dict(out=((n, Hq, D), q.dtype), lse=((n, Hq), F32)), dev)
-        a.device()
-        ws = ws or Workspace(dev)
-        buf = ws.get(A.dspark_cache_attend_workspace(R, n, Hq, Hkv, D, dt), stream, dev)
-    st = _run(dev, stream, lambda s: A.dspark_cache_attend(
-        R, n, Hq, Hkv, D, page, table.shape[1], n_pages, dt, float(D ** -0.5 if scale is None
-                                                                   else scale), int(window),
-        q, q_stride, k_new, v_new, kn, k_pages, v_pages, k_stride, v_stride, table, row_offset,
-        kv_len, out["out"], out["lse"], buf, buf.numel(), s))
-    _check(st, "dspark_cache_attend")
+        out = _outs(a, out, {"out": ((n, Hq, D), q.dtype), "lse": ((n, Hq), F32)}, dev)
+        a.gpu()
+        buf = _workspace(ws, _attend_ws(R, n, Hq, Hkv, D, dt), dev, index, stream)
+    if scale is None:
+        scale = D ** -0.5
+    _launch("dspark_cache_attend", index, stream, lambda s: A.dspark_cache_attend(
+        R, n, Hq, Hkv, D, page, width, n_pages, dt, scale, window, q, q_stride, k_new, v_new, kn,
+        k_pages, v_pages, k_stride, v_stride, table, row_offset, kv_len, out["out"], out["lse"], buf,
+        buf.numel(), s))
     return out
 
 
