@@ -3,21 +3,27 @@
 // Three launches:
 //  1. attend_prepare_kernel: the first workgroup lays out the work (below); the
 //     others write the new rows' keys and values into their pages.
-//  2. attend_kernel: one work item is a block of up to 16 MT rows (a row here is
-//     one query head of one new token; the Hq / Hkv heads of a group and the
-//     request's new tokens share their keys, so they share the block), one
-//     key-value head and a stretch of the request's tokens.  Its four waves take
-//     the stretch's steps in turn and are joined in LDS.  A request in one
-//     stretch writes its result, one in several leaves (max, sum, sum p v).
-//  3. attend_join_kernel joins the stretches.
+//  2. the product.  A unit of work is a block of rows (a row here is one query head
+//     of one new token; the Hq / Hkv heads of a group and the request's new tokens
+//     share their keys, so they share the block) over one request's tokens, for one
+//     key-value head.  All units in a line are cut into equal shares, one per
+//     workgroup and about as many as the chip holds at once, whatever the lengths.
+//     A unit within one share writes its result; of one that is cut, every share
+//     leaves (max, sum, sum p v).  Two kernels:
+//       attend_few_kernel   up to 16 rows a block (single tokens): its four waves
+//                           take the steps along the tokens in turn, each straight
+//                           from memory into its products, and are joined in LDS;
+//       attend_many_kernel  up to 64 rows: the waves take the rows, and each step's
+//                           keys and values pass through LDS once for all of them.
+//  3. attend_join_kernel joins what was cut.
 //
-// The product in registers alone.  Scores are formed transposed, S^T = K Q^T, and
+// The products need no shuffle.  Scores are formed transposed, S^T = K Q^T, and
 // the result too, O^T = V^T P^T: a lane then holds the same row of Q in S^T and in
 // O^T, so maxima, sums and rescaling factors never cross lanes, and P^T leaves the
 // first product in the register layout in which the second wants it.  For that the
 // 32 keys of a bf16 step are entered in an order that gives a lane 8 consecutive
 // ones, and values lie along the tokens in their pages, so that a lane's 8 are one
-// 16-byte load.  No LDS and no shuffle stand between the loads and the products.
+// 16-byte load.
 //
 // Bound: keys and values are read once from memory (2 Hkv D bytes a token for each
 // of K and V); the products are 4 Hq D n operations a token, far below the matrix
@@ -33,22 +39,23 @@ namespace dspark {
 namespace {
 
 constexpr int kWaves = kBlock / kWave;
-// Work items aimed at over all key-value heads (see lay_out).
-constexpr int kTarget = 4 * kComputeUnits;
-constexpr int kLeast = 128;       // tokens of a stretch, at least: one step of every wave
+constexpr int kShares = 2 * kComputeUnits;  // over all key-value heads: two workgroups a unit
+constexpr int kCut = 128;         // a unit is cut at multiples of this many tokens
+constexpr int kFixed = 64;        // a unit's fixed cost, in tokens
+constexpr int kWindow = 1024;     // page numbers of a stretch that wait in LDS at a time
 constexpr float kNone = -1e30f;   // running maximum of a row that has seen nothing
 constexpr float kSlack = 8.0f;    // see rescale below
 
 struct AttendParams {
   AttendLaunch L;
   int heads_per_group, block_rows;
-  int most_items, most_slots;
+  int most_shares;  // per key-value head
   // scratch
-  int32_t *head;    // [0] number of items, [1] split slots used
-  int4 *items;      // (request, first row of the block, first token, slot or -1)
-  int2 *stretches;  // [R]: (tokens of a stretch, first slot or -1)
-  float2 *part_ml;  // [slots][Hkv][block_rows]: (max in log2 units, sum)
-  float *part_o;    // [slots][Hkv][block_rows][D]
+  int64_t *head;    // work units per share (tokens), of all requests
+  int64_t *before;  // [R + 1] work units before each request
+  int32_t *first;   // [most_shares] the request in which each share begins
+  float2 *part_ml;  // [2 most_shares][Hkv][block_rows]: (max in log2 units, sum)
+  float *part_o;    // [2 most_shares][Hkv][block_rows][D]
 };
 
 struct Slice { int row0, n, len; };
@@ -79,94 +86,87 @@ __device__ __forceinline__ int first_token(const AttendLaunch &L, const Slice &s
   return max(0, s.len - s.n + 1 - L.window) & ~31;
 }
 
-__device__ __forceinline__ int2 scan2(int2 v, int2 *scratch, int2 *total) {
+// The units of a request: so many blocks of `size` work units each, over the tokens
+// [t0, len).
+struct Units { int blocks, size, t0; };
+__device__ __forceinline__ Units units_of(const AttendParams &p, const Slice &s) {
+  Units u;
+  u.blocks = (int)(((int64_t)s.n * p.heads_per_group + p.block_rows - 1) / p.block_rows);
+  u.t0 = first_token(p.L, s);
+  u.size = kFixed + (s.len - u.t0);
+  return u;
+}
+// Where a cut at `at` of a unit's `size` work units lies among its tokens.
+__device__ __forceinline__ int cut_at(int64_t at, int size) {
+  if (at >= size) return size - kFixed;
+  return at <= kFixed ? 0 : ((int)at - kFixed) & ~(kCut - 1);
+}
+
+// Exclusive prefix over the workgroup, and the total.
+__device__ __forceinline__ int64_t scan64(int64_t v, int64_t *scratch, int64_t *total) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  int2 inc = v;
+  int64_t inc = v;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
-    const int x = __shfl_up(inc.x, o), y = __shfl_up(inc.y, o);
-    if (lane >= o) { inc.x += x; inc.y += y; }
+    const int64_t x = __shfl_up((long long)inc, o);
+    if (lane >= o) inc += x;
   }
   __syncthreads();
   if (lane == kWave - 1) scratch[w] = inc;
   __syncthreads();
-  int2 before = {0, 0}, all = {0, 0};
+  int64_t before = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
-    if (i < w) { before.x += scratch[i].x; before.y += scratch[i].y; }
-    all.x += scratch[i].x; all.y += scratch[i].y;
+    if (i < w) before += scratch[i];
+    all += scratch[i];
   }
   *total = all;
-  return make_int2(before.x + inc.x - v.x, before.y + inc.y - v.y);
-}
-
-__device__ __forceinline__ double block_sum_f64(double v, double *scratch) {
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  __syncthreads();
-  if ((threadIdx.x & (kWave - 1)) == 0) scratch[threadIdx.x / kWave] = v;
-  __syncthreads();
-  return ((scratch[0] + scratch[1]) + scratch[2]) + scratch[3];
+  return before + inc - v;
 }
 
 }  // namespace
 
-// Stretches so long that all blocks' tokens together make about kTarget items
-// over all key-value heads (lengths may differ a lot: an item's work, not a
-// request's, is what has to be alike); a request within one stretch is not
-// split.  A split request has at least two stretches, each but the last full,
-// so split items number at most 2 kTarget / Hkv: the slots.
+// Equal shares of the units of all requests, of at least one cut.
 __device__ __forceinline__ void lay_out(const AttendParams &p) {
   const AttendLaunch &L = p.L;
-  __shared__ double sums[kWaves];
-  __shared__ int2 scratch[kWaves];
+  __shared__ int64_t scratch[kWaves], from[kBlock];
   const int tid = threadIdx.x;
   int bits = 0;
-  double work = 0.0;
-  for (int r = tid; r < L.R; r += kBlock) {
-    const Slice s = slice_of(L, r, &bits);
-    const int blocks = (s.n * p.heads_per_group + p.block_rows - 1) / p.block_rows;
-    work += (double)blocks * (s.len - first_token(L, s));
-  }
-  work = block_sum_f64(work, sums) * L.Hkv;
-  const int64_t even = (int64_t)(work / kTarget) + 1;
-  const int stretch = (int)min((int64_t)(even < kLeast ? kLeast : (even + 127) / 128 * 128),
-                               (int64_t)1 << 30);
-  int2 base = {0, 0};
+  auto work_of = [&](int r) __attribute__((always_inline)) {
+    if (r >= L.R) return (int64_t)0;
+    const Units u = units_of(p, slice_of(L, r, &bits));
+    return (int64_t)u.blocks * u.size;
+  };
+  int64_t all = 0, mine = 0;
+  for (int r = tid; r < L.R; r += kBlock) mine += work_of(r);
+  scan64(mine, scratch, &all);
+  const int64_t even = (all + p.most_shares - 1) / p.most_shares;
+  const int64_t share = even < kCut + kFixed ? kCut + kFixed : even;
+  int64_t base = 0;
   for (int r0 = 0; r0 < L.R; r0 += kBlock) {
     const int r = r0 + tid;
-    int2 count = {0, 0};
-    Slice s{};
-    int blocks = 0, splits = 1, t0 = 0;
-    if (r < L.R) {
-      s = slice_of(L, r, &bits);
-      t0 = first_token(L, s);
-      blocks = (s.n * p.heads_per_group + p.block_rows - 1) / p.block_rows;
-      splits = max(1, (int)(((int64_t)s.len - t0 + stretch - 1) / stretch));
-      count = make_int2(blocks * splits, splits > 1 ? blocks * splits : 0);
+    int64_t total;
+    const int64_t at = base + scan64(work_of(r), scratch, &total);
+    if (r < L.R) p.before[r] = at;
+    from[tid] = at;
+    __syncthreads();
+    // shares that begin among these requests, by all threads: in the last request
+    // that does not begin behind them
+    const int here = min(L.R - r0, kBlock);
+    for (int64_t i = (base + share - 1) / share + tid; i * share < base + total; i += kBlock) {
+      int lo = 0;
+#pragma unroll
+      for (int step = kBlock / 2; step > 0; step >>= 1)
+        if (lo + step < here && from[lo + step] <= i * share) lo += step;
+      p.first[i] = r0 + lo;
     }
-    int2 total;
-    const int2 at = scan2(count, scratch, &total);
-    if (r < L.R) {
-      const int item0 = base.x + at.x, slot0 = base.y + at.y;
-      p.stretches[r] = make_int2(stretch, splits > 1 ? slot0 : -1);
-      for (int i = 0; i < blocks * splits; ++i) {
-        // only slices that overlap (a row_offset that decreases) can pass the bounds
-        if (item0 + i >= p.most_items || (splits > 1 && slot0 + i >= p.most_slots)) {
-          bits |= kErrLength;
-          break;
-        }
-        const int b = i % blocks, k = i / blocks;
-        p.items[item0 + i] =
-            make_int4(r, b * p.block_rows, t0 + k * stretch, splits > 1 ? slot0 + i : -1);
-      }
-    }
-    base.x += total.x;
-    base.y += total.y;
+    __syncthreads();
+    base += total;
   }
   if (tid == 0) {
-    p.head[0] = min(base.x, p.most_items);
-    p.head[1] = base.y;
+    p.before[L.R] = all;
+    p.head[0] = share;
+    p.head[1] = all;
   }
   if (bits) flag_error(L.err, bits);
 }
@@ -214,6 +214,15 @@ __global__ __launch_bounds__(kBlock) void attend_prepare_kernel(AttendParams p) 
 
 namespace {
 
+// 16 bytes of keys or values.  A step reads 64 bytes of each of its rows of values.
+// Where that is the whole row of a page, the step's lines are its own and pass the
+// caches by (decoding 256 requests of up to 4000 tokens, pages of 16: 350 us, 381
+// through the caches); where rows are longer, another wave wants the line's other
+// half a moment later (pages of 64: 363 us through the caches, 414 past them).
+template <bool kPast> __device__ __forceinline__ u32x4 ld_cache(const void *p) {
+  if constexpr (kPast) return ld_stream4(p);
+  else return *reinterpret_cast<const u32x4 *>(p);
+}
 // The matrix products of one step.  Lane l: column c = l % 16 of a 16-row tile of
 // Q, group g = l / 16.  S^T tile: register i of the lane is key 4 g + i of the
 // tile.  bf16: two tiles of 16 keys, entered so that the lane's two quads are the
@@ -230,10 +239,10 @@ template <> struct Step<bf16_t> {
   template <int D> struct V { u32x4 v[D / 16]; };
   template <int D> struct Q { u32x4 v[D / 32]; };
   // key row `k` (this lane's), element order: contraction index 32 s + 8 g + e
-  template <int D>
+  template <bool kPast, int D>
   __device__ static __forceinline__ void load_k(const bf16_t *k, int t, int g, K<D> &o) {
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) o.v[t][s] = ld_stream4(k + 32 * s + 8 * g);
+    for (int s = 0; s < D / 32; ++s) o.v[t][s] = ld_cache<kPast>(k + 32 * s + 8 * g);
   }
   template <int D>
   __device__ static __forceinline__ void load_q(const bf16_t *q, int g, Q<D> &o) {
@@ -290,10 +299,10 @@ template <> struct Step<float> {
   template <int D> struct V { u32x4 v[D / 16]; };
   template <int D> struct Q { u32x4 v[D / 16]; };
   // element order: product 4 s + e takes contraction index 16 s + 4 g + e
-  template <int D>
+  template <bool kPast, int D>
   __device__ static __forceinline__ void load_k(const float *k, int t, int g, K<D> &o) {
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) o.v[t][s] = ld_stream4(k + 16 * s + 4 * g);
+    for (int s = 0; s < D / 16; ++s) o.v[t][s] = ld_cache<kPast>(k + 16 * s + 4 * g);
   }
   template <int D>
   __device__ static __forceinline__ void load_q(const float *q, int g, Q<D> &o) {
@@ -348,318 +357,576 @@ __device__ __forceinline__ void store4(bf16_t *p, const float *v) {
 
 }  // namespace
 
-template <typename T, int D, int MT>
-__global__ __launch_bounds__(kBlock) void attend_kernel(AttendParams p) {
+namespace {
+
+template <bool B> struct Flag { static constexpr bool value = B; };
+
+// The page numbers of tokens [begin, end) to LDS (-1 where there is no such page);
+// returns whether one is missing.  From LDS, because loads come back in order: a
+// number read from memory would be waited for behind every key in flight.
+__device__ __forceinline__ bool stage_ids(const AttendLaunch &L, const int32_t *table, int begin, int end,
+                                          int32_t *ids) {
+  bool bad = false;
+  const int first = begin >> L.page_shift, n = ((end - 1) >> L.page_shift) - first + 1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kBlock) {
+    const int id = table[first + i];
+    const bool there = (unsigned)id < (unsigned)L.n_pages;
+    ids[i] = there ? id : -1;
+    bad = bad || !there;
+  }
+  return __syncthreads_or(bad);
+}
+
+// A share's stretches, one after the other.
+struct Stretch {
+  Slice sl;
+  int r, block_row, rows, begin, end;
+  int slot;  // where its part goes, -1: the unit is whole
+};
+struct Share {
+  int64_t at, end;
+  int r, index;
+};
+__device__ __forceinline__ bool share_of(const AttendParams &p, int index, Share *s) {
+  s->index = index;
+  s->at = index * p.head[0];
+  s->end = min(s->at + p.head[0], p.head[1]);
+  if (s->at >= s->end) return false;
+  s->r = p.first[index];
+  return true;
+}
+__device__ __forceinline__ bool next_stretch(const AttendParams &p, Share *s, Stretch *o) {
+  if (s->at >= s->end) return false;
+  while (s->at >= p.before[s->r + 1]) ++s->r;  // requests without rows have no units
+  int bits = 0;
+  o->r = s->r;
+  o->sl = slice_of(p.L, s->r, &bits);
+  const Units u = units_of(p, o->sl);
+  const int64_t rel = s->at - p.before[s->r];
+  const int b = (int)(rel / u.size);
+  const int64_t x = rel - (int64_t)b * u.size, x1 = min((int64_t)u.size, x + (s->end - s->at));
+  o->block_row = b * p.block_rows;
+  o->rows = min(p.block_rows, o->sl.n * p.heads_per_group - o->block_row);
+  o->begin = u.t0 + cut_at(x, u.size);
+  o->end = u.t0 + cut_at(x1, u.size);
+  // a share has at most one part that begins within a unit and one that ends within
+  o->slot = x > 0 ? 2 * s->index : x1 < u.size ? 2 * s->index + 1 : -1;
+  s->at += x1 - x;
+  return true;
+}
+
+// One row (of Q) of a 16-row tile as a lane holds it: the tokens that it sees,
+// [low, high), the subtrahend m (log2 units) and its lane's share of the sum.
+struct RowState {
+  int low, high;
+  float m, l;
+};
+
+// Row `row` of the item's `rows` (block_row on): what it sees and its query.
+template <typename T, int D>
+__device__ __forceinline__ RowState row_state(const AttendParams &p, const Slice &sl, int block_row,
+                                              int row, int rows, int hk, int g,
+                                              typename Step<T>::template Q<D> &q) {
+  const AttendLaunch &L = p.L;
+  RowState s{0, 0, kNone, 0.0f};
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(q.v) / 16; ++i) q.v[i] = u32x4{0, 0, 0, 0};
+  if (row < rows) {
+    const int group = p.heads_per_group, j = (block_row + row) / group, h = (block_row + row) % group;
+    s.high = max(0, sl.len - sl.n + 1 + j);
+    s.low = L.window > 0 ? max(0, s.high - L.window) : 0;
+    Step<T>::template load_q<D>(reinterpret_cast<const T *>(L.q) + (int64_t)(sl.row0 + j) * L.q_stride +
+                                    (int64_t)(hk * group + h) * D,
+                                g, q);
+  }
+  return s;
+}
+
+// Masks a lane's scores of the tokens from t0 on.
+template <int kMine>
+__device__ __forceinline__ void mask_scores(float *s, const RowState &r, int t0, bool bad) {
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (bad || t0 + i < r.low || t0 + i >= r.high) s[i] = -INFINITY;
+}
+
+// Scores to probabilities against the row's subtrahend.  That follows the running
+// maximum only when it is kSlack (a factor 2^8) behind: below that the sums just
+// grow, and what is summed so far needs no rescaling.  The lanes of a row (16, 32
+// and 48 apart) agree on it.
+template <typename T, int kOut>
+__device__ __forceinline__ typename Step<T>::P weigh(float *s, float to_log2, RowState &r,
+                                                     floatx4 (&o)[kOut]) {
+  constexpr int kMine = Step<T>::kMine;
+  float top = s[0];
+#pragma unroll
+  for (int i = 1; i < kMine; ++i) top = fmaxf(top, s[i]);
+  top *= to_log2;
+  if (__ballot(top > r.m + kSlack) != 0) {
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float now = fmaxf(r.m, top), f = exp2_fast(r.m - now);
+    r.m = now;
+    r.l *= f;
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) o[d] *= f;
+  }
+  float e[kMine], sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    e[i] = exp2_fast(fmaf(s[i], to_log2, -r.m));
+    sum += e[i];
+  }
+  r.l += sum;
+  return Step<T>::pack(e);
+}
+
+// The product row by row, with the values that the row does not see zeroed:
+// where a value that some of the rows see is not finite.
+template <typename T>
+__device__ __forceinline__ floatx4 product_mixed(const u32x4 &v, const typename Step<T>::P &pr,
+                                                 const RowState &r, int t0, floatx4 o) {
+  const int col = threadIdx.x & 15;
+  for (int c = 0; c < 16; ++c) {
+    const int from = __shfl(r.low, c) - t0, to = __shfl(r.high, c) - t0;
+    const floatx4 a = Step<T>::product(Step<T>::keep(v, from, to), pr, o);
+    if (col == c) o = a;
+  }
+  return o;
+}
+
+// Four elements from d on of a row's result: the stretch's share, or the result.
+template <typename T>
+__device__ __forceinline__ void write_row(const AttendParams &p, const Slice &sl, int hk, int slot,
+                                          int block_row, int row, int d, float m, float sum,
+                                          const float *x) {
+  const AttendLaunch &L = p.L;
+  if (slot >= 0) {
+    const int64_t at = ((int64_t)slot * L.Hkv + hk) * p.block_rows + row;
+    store4(p.part_o + at * L.D + d, x);
+    if (d == 0) p.part_ml[at] = make_float2(m, sum);
+    return;
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : sum;  // nothing seen: 0; NaN stays
+  const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+  const int group = p.heads_per_group;
+  const int j = (block_row + row) / group, h = hk * group + (block_row + row) % group;
+  const int64_t out_row = (int64_t)(sl.row0 + j) * L.Hq + h;
+  store4(reinterpret_cast<T *>(L.out) + out_row * L.D + d, y);
+  if (d == 0 && L.lse != nullptr)
+    L.lse[out_row] = sum == 0.0f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(sum));
+}
+
+}  // namespace
+
+template <typename T, int D, bool kPast>
+__global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(AttendParams p) {
   using St = Step<T>;
   constexpr int kKeys = St::kKeys, kMine = St::kMine, kTiles = St::kTiles;
   constexpr int kOut = D / 16;      // 16-wide tiles of the result
   constexpr int kPitch = D + 4;     // of a row in LDS, floats
-  // registers: D / 2 for a step's keys and values, 3 D / 8 for a tile's result and queries
-  constexpr bool kAhead = D + MT * 3 * D / 8 <= 240;
+  // two steps' keys and values (D / 2 registers each) beside the result and queries
+  constexpr bool kAhead = D <= 128;
   __shared__ float lds_o[kWaves][16][kPitch];
   __shared__ float2 lds_ml[kWaves][16];
+  __shared__ int32_t ids[kWindow];
   const AttendLaunch &L = p.L;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int col = lane & 15, g = lane >> 4;
-  const int n_items = p.head[0];
   const int group = p.heads_per_group;
   const float to_log2 = L.scale * kLog2e;
+  const int page_mask = (1 << L.page_shift) - 1;
 
-  for (int64_t w = blockIdx.x; w < (int64_t)n_items * L.Hkv; w += gridDim.x) {
-    const int hk = (int)(w % L.Hkv);
-    const int4 item = p.items[w / L.Hkv];
-    const int r = item.x, block_row = item.y, begin = item.z, slot = item.w;
+  const int hk = blockIdx.x % L.Hkv;
+  Share share;
+  if (!share_of(p, blockIdx.x / L.Hkv, &share)) return;
+  Stretch st;
+  while (next_stretch(p, &share, &st)) {
+    const Slice &sl = st.sl;
+    const int block_row = st.block_row, rows = st.rows, begin = st.begin, end = st.end, slot = st.slot;
     int bits = 0;
-    const Slice sl = slice_of(L, r, &bits);
-    const int end = min(begin + p.stretches[r].x, sl.len);
-    const int rows = min(p.block_rows, sl.n * group - block_row);
-    const int32_t *table = L.table + (int64_t)r * L.max_pages;
-
-    // this lane's row of each tile: tokens it sees are [low, high)
-    typename St::template Q<D> q[MT];
-    int low[MT], high[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int i = mt * 16 + col, j = (block_row + i) / group, h = (block_row + i) % group;
-      low[mt] = high[mt] = 0;
-#pragma unroll
-      for (unsigned s = 0; s < sizeof(q[mt].v) / 16; ++s) q[mt].v[s] = u32x4{0, 0, 0, 0};
-      if (i < rows) {
-        high[mt] = max(0, sl.len - sl.n + 1 + j);
-        low[mt] = L.window > 0 ? max(0, high[mt] - L.window) : 0;
-        St::template load_q<D>(reinterpret_cast<const T *>(L.q) +
-                                   (int64_t)(sl.row0 + j) * L.q_stride + (hk * group + h) * D,
-                               g, q[mt]);
-      }
-    }
+    const int32_t *table = L.table + (int64_t)st.r * L.max_pages;
+    typename St::template Q<D> q;
+    RowState row = row_state<T, D>(p, sl, block_row, col, rows, hk, g, q);
+    // tokens before most_low or from least_high on are hidden from some row
     const int first_j = block_row / group, last_j = (block_row + rows - 1) / group;
     const int least_high = max(0, sl.len - sl.n + 1 + first_j);
     const int most_low = L.window > 0 ? sl.len - sl.n + 1 + last_j - L.window : 0;
-
-    floatx4 o[MT][kOut];
-    float m[MT], l[MT];
+    floatx4 o[kOut];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt] = kNone;
-      l[mt] = 0.0f;
-#pragma unroll
-      for (int d = 0; d < kOut; ++d) o[mt][d] = floatx4{0, 0, 0, 0};
-    }
+    for (int d = 0; d < kOut; ++d) o[d] = floatx4{0, 0, 0, 0};
 
     struct Data {
       typename St::template K<D> k;
       typename St::template V<D> v;
-      bool bad;  // this lane's keys lie in a page that does not exist
     };
     const T *kbase = reinterpret_cast<const T *>(L.k_pages) + ((int64_t)hk << L.page_shift) * D;
     const T *vbase = reinterpret_cast<const T *>(L.v_pages) + ((int64_t)hk * D << L.page_shift);
-    const int page_mask = (1 << L.page_shift) - 1;
-    // loads of the step at token t; tokens past the last read the last page again
-    auto load = [&](int t, Data &x) __attribute__((always_inline)) {
-      const int last = sl.len - 1;
-      const int tk = t + St::key_of_row(col, 0), tv = t + kMine * g;
-      const int ik = table[min(tk, last) >> L.page_shift];
-      const int iv = table[min(tv, last) >> L.page_shift];
-      x.bad = (unsigned)iv >= (unsigned)L.n_pages;
-      const T *k = kbase + (int64_t)((unsigned)ik < (unsigned)L.n_pages ? ik : 0) * L.k_page_stride;
-      const T *v = vbase + (int64_t)(x.bad ? 0 : iv) * L.v_page_stride + (tv & page_mask);
+    const int stride = kWaves * kKeys;
+    for (int w0 = begin; w0 < end; w0 += kWindow << L.page_shift) {
+      const int w1 = min(end, w0 + (kWindow << L.page_shift));
+      const bool any_bad = stage_ids(L, table, w0, w1, ids);
+      const int first_page = w0 >> L.page_shift;
+      // loads of the step at token t; tokens past the last read the last page again
+      auto load = [&](int t, Data &x) __attribute__((always_inline)) {
+        const int tk = t + St::key_of_row(col, 0), tv = t + kMine * g;
+        const int ik = max(0, ids[(min(tk, w1 - 1) >> L.page_shift) - first_page]);
+        const int iv = max(0, ids[(min(tv, w1 - 1) >> L.page_shift) - first_page]);
+        const T *k = kbase + (int64_t)ik * L.k_page_stride;
+        const T *v = vbase + (int64_t)iv * L.v_page_stride + (tv & page_mask) + (col << L.page_shift);
 #pragma unroll
-      for (int s = 0; s < kTiles; ++s)
-        St::template load_k<D>(k + (int64_t)((t + St::key_of_row(col, s)) & page_mask) * D, s, g, x.k);
+        for (int s = 0; s < kTiles; ++s)
+          St::template load_k<kPast, D>(k + ((t + St::key_of_row(col, s)) & page_mask) * D, s, g, x.k);
 #pragma unroll
-      for (int d = 0; d < kOut; ++d)
-        x.v.v[d] = ld_stream4(v + ((int64_t)(16 * d + col) << L.page_shift));
-    };
-    auto compute = [&](int t, Data &x) __attribute__((always_inline)) {
-      const int t0 = t + kMine * g;  // this lane's first token
-      const bool any_bad = __ballot(x.bad) != 0;
-      const bool edge = any_bad || t + kKeys > least_high || t < most_low;  // uniform
-      bool mixed = false;  // a value that is not finite, seen by some rows only
-      if (edge) {
-        if (x.bad) bits |= kErrPage;
-        bool odd = false;
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) {
-          x.v.v[d] = St::keep(x.v.v[d], 0, x.bad ? 0 : sl.len - t0);
-          odd = odd || St::not_finite(x.v.v[d]);
-        }
-        mixed = __ballot(odd) != 0;
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (mt * 16 >= rows) continue;  // uniform
+        for (int d = 0; d < kOut; ++d) x.v.v[d] = ld_cache<kPast>(v + (16 * d << L.page_shift));
+      };
+      auto compute = [&](int t, Data &x) __attribute__((always_inline)) {
+        const int t0 = t + kMine * g;  // this lane's first token
+        const bool edge = any_bad || t + kKeys > least_high || t < most_low;  // uniform
         float s[kMine];
 #pragma unroll
         for (int u = 0; u < kTiles; ++u) {
-          const floatx4 a = St::template scores<D>(x.k, u, q[mt]);
+          const floatx4 a = St::template scores<D>(x.k, u, q);
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[4 * u + i] = a[i];
         }
+        bool mixed = false;
         if (edge) {
+          const bool bad = any_bad && ids[(min(t0, w1 - 1) >> L.page_shift) - first_page] < 0;
+          if (bad) bits |= kErrPage;
+          mask_scores<kMine>(s, row, t0, bad);
+          bool odd = false;
 #pragma unroll
-          for (int i = 0; i < kMine; ++i)
-            if (x.bad || t0 + i < low[mt] || t0 + i >= high[mt]) s[i] = -INFINITY;
+          for (int d = 0; d < kOut; ++d) {
+            x.v.v[d] = St::keep(x.v.v[d], 0, bad ? 0 : sl.len - t0);
+            odd = odd || St::not_finite(x.v.v[d]);
+          }
+          mixed = __ballot(odd) != 0;
         }
-        // The subtrahend follows the running maximum only when that is kSlack
-        // (a factor 2^8) ahead; below that the sums just grow, and the sums and
-        // products need no rescaling.
-        float top = s[0];
-#pragma unroll
-        for (int i = 1; i < kMine; ++i) top = fmaxf(top, s[i]);
-        top *= to_log2;
-        if (__ballot(top > m[mt] + kSlack) != 0) {
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float now = fmaxf(m[mt], top), f = exp2_fast(m[mt] - now);
-          m[mt] = now;
-          l[mt] *= f;
-#pragma unroll
-          for (int d = 0; d < kOut; ++d) o[mt][d] *= f;
-        }
-        float e[kMine], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          e[i] = exp2_fast(fmaf(s[i], to_log2, -m[mt]));
-          sum += e[i];
-        }
-        l[mt] += sum;
-        const typename St::P pr = St::pack(e);
+        const typename St::P pr = weigh<T, kOut>(s, to_log2, row, o);
         if (!mixed) {
 #pragma unroll
-          for (int d = 0; d < kOut; ++d) o[mt][d] = St::product(x.v.v[d], pr, o[mt][d]);
+          for (int d = 0; d < kOut; ++d) o[d] = St::product(x.v.v[d], pr, o[d]);
         } else {
-          // row by row, with what the row does not see zeroed in V
-          for (int c = 0; c < 16; ++c) {
-            const int from = __shfl(low[mt], c) - t0, to = __shfl(high[mt], c) - t0;
 #pragma unroll
-            for (int d = 0; d < kOut; ++d) {
-              const floatx4 a = St::product(St::keep(x.v.v[d], from, to), pr, o[mt][d]);
-              if (col == c) o[mt][d] = a;
-            }
-          }
+          for (int d = 0; d < kOut; ++d) o[d] = product_mixed<T>(x.v.v[d], pr, row, t0, o[d]);
         }
-      }
-    };
+      };
 
-    // every wave its steps; where registers allow, the next one's loads are in
-    // flight during this one's products
-    const int stride = kWaves * kKeys;
-    int t = begin + wave * kKeys;
-    Data a;
-    if constexpr (!kAhead) {
-      for (; t < end; t += stride) {
+      // every wave its steps; where registers allow, the next one's loads are in
+      // flight during this one's products
+      int t = w0 + wave * kKeys;
+      Data a;
+      if constexpr (!kAhead) {
+        for (; t < w1; t += stride) {
+          load(t, a);
+          compute(t, a);
+        }
+      } else if (t < w1) {
+        Data b;
         load(t, a);
-        compute(t, a);
-      }
-    } else if (t < end) {
-      Data b;
-      load(t, a);
-      for (;;) {
-        const bool more = t + stride < end;
-        if (more) load(t + stride, b);
-        compute(t, a);
-        t += stride;
-        if (!more) break;
-        const bool again = t + stride < end;
-        if (again) load(t + stride, a);
-        compute(t, b);
-        t += stride;
-        if (!again) break;
+        for (;;) {
+          const bool more = t + stride < w1;
+          if (more) load(t + stride, b);
+          compute(t, a);
+          t += stride;
+          if (!more) break;
+          const bool again = t + stride < w1;
+          if (again) load(t + stride, a);
+          compute(t, b);
+          t += stride;
+          if (!again) break;
+        }
       }
     }
     if (bits) flag_error(L.err, bits);
 
-    // join the waves, one tile of rows at a time
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt * 16 >= rows) continue;
-      float sum = l[mt];
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      __syncthreads();
-      if (g == 0) lds_ml[wave][col] = make_float2(m[mt], sum);
-#pragma unroll
-      for (int d = 0; d < kOut; ++d)
-        *reinterpret_cast<floatx4 *>(&lds_o[wave][col][16 * d + 4 * g]) = o[mt][d];
-      __syncthreads();
-      // 4 elements a thread at a time
-      for (int i = threadIdx.x; i < 16 * D / 4; i += kBlock) {
-        const int c = i / (D / 4), d = i % (D / 4) * 4, row = mt * 16 + c;
-        if (row >= rows) continue;
-        float mx = kNone;
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) mx = fmaxf(mx, lds_ml[v][c].x);
-        float all = 0.0f, x[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-          const float f = exp2_fast(lds_ml[v][c].x - mx);
-          all += f * lds_ml[v][c].y;
-          const floatx4 y = *reinterpret_cast<const floatx4 *>(&lds_o[v][c][d]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] += f * y[k];
-        }
-        if (slot >= 0) {
-          const int64_t at = ((int64_t)slot * L.Hkv + hk) * p.block_rows + row;
-          store4(p.part_o + at * D + d, x);
-          if (d == 0) p.part_ml[at] = make_float2(mx, all);
-        } else {
-          const float inv = all > 0.0f ? 1.0f / all : (all == 0.0f ? 0.0f : all);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] *= inv;
-          const int j = (block_row + row) / group, h = hk * group + (block_row + row) % group;
-          const int64_t out_row = (int64_t)(sl.row0 + j) * L.Hq + h;
-          store4(reinterpret_cast<T *>(L.out) + out_row * D + d, x);
-          if (d == 0 && L.lse != nullptr)
-            L.lse[out_row] = all == 0.0f ? -INFINITY : fmaf(mx, 0.6931471805599453f, logf(all));
-        }
-      }
-    }
+    // join the waves
+    float sum = row.l;
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
     __syncthreads();
+    if (g == 0) lds_ml[wave][col] = make_float2(row.m, sum);
+#pragma unroll
+    for (int d = 0; d < kOut; ++d)
+      *reinterpret_cast<floatx4 *>(&lds_o[wave][col][16 * d + 4 * g]) = o[d];
+    __syncthreads();
+    // 4 elements a thread at a time
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kBlock) {
+      const int c = i / (D / 4), d = i % (D / 4) * 4;
+      float mx = kNone;
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) mx = fmaxf(mx, lds_ml[v][c].x);
+      float all = 0.0f, x[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) {
+        const float f = exp2_fast(lds_ml[v][c].x - mx);
+        all += f * lds_ml[v][c].y;
+        const floatx4 y = *reinterpret_cast<const floatx4 *>(&lds_o[v][c][d]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] += f * y[k];
+      }
+      write_row<T>(p, sl, hk, slot, block_row, c, d, mx, all, x);
+    }
   }
 }
 
-// One wave per (new token, query head) of the split requests.
-template <typename T>
-__global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
+// 16 rows a wave.  A step's keys and values are D / 8 pieces of 64 x 16 bytes, each
+// an operand of the matrix cores in lane order: waves 0 and 1 fetch the keys', 2 and
+// 3 the values', kDeep steps ahead in registers, and pass them on through two buffers
+// in LDS.  In lane order every LDS access is 1 KB in a row; one barrier a step.
+template <typename T, int D, bool kPast>
+__global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(AttendParams p) {
+  using St = Step<T>;
+  constexpr int kKeys = St::kKeys, kMine = St::kMine, kTiles = St::kTiles;
+  constexpr int kOut = D / 16;
+  constexpr int kPieces = D / 8, kFetch = kPieces / kWaves;  // of a step; of a wave
+  constexpr int kDeep = D <= 128 ? 4 : 2;
+  __shared__ u32x4 ring[2][kPieces][kWave];
+  __shared__ int32_t ids[kWindow];
   const AttendLaunch &L = p.L;
-  if (p.head[1] == 0) return;
-  const int lane = threadIdx.x & (kWave - 1);
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int col = lane & 15, g = lane >> 4;
+  const int group = p.heads_per_group;
+  const float to_log2 = L.scale * kLog2e;
+  const int page_mask = (1 << L.page_shift) - 1;
+  const bool keys = wave < 2;  // what this wave fetches
+
+  const int hk = blockIdx.x % L.Hkv;
+  Share share;
+  if (!share_of(p, blockIdx.x / L.Hkv, &share)) return;
+  Stretch st;
+  while (next_stretch(p, &share, &st)) {
+    const Slice &sl = st.sl;
+    const int block_row = st.block_row, rows = st.rows, begin = st.begin, end = st.end, slot = st.slot;
+    int bits = 0;
+    const int32_t *table = L.table + (int64_t)st.r * L.max_pages;
+    typename St::template Q<D> q;
+    RowState row = row_state<T, D>(p, sl, block_row, 16 * wave + col, rows, hk, g, q);
+    floatx4 o[kOut];
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) o[d] = floatx4{0, 0, 0, 0};
+    const int first_j = block_row / group, last_j = (block_row + rows - 1) / group;
+    const int least_high = max(0, sl.len - sl.n + 1 + first_j);
+    const int most_low = L.window > 0 ? sl.len - sl.n + 1 + last_j - L.window : 0;
+
+    // The lane's address within a page (element), and its token within a step:
+    // keys: pieces [wave kFetch, ..) of the step's kTiles key tiles.
+    const int tile = kTiles == 2 ? (wave & 1) : 0;
+    const int s0 = kTiles == 2 ? 0 : (wave & 1) * kFetch;  // first piece of the tile
+    const int my_token = keys ? St::key_of_row(col, tile) : kMine * g;
+    const T *base = keys ? reinterpret_cast<const T *>(L.k_pages) + ((int64_t)hk << L.page_shift) * D +
+                               4 * kMine * s0 + kMine * g
+                         : reinterpret_cast<const T *>(L.v_pages) +
+                               (((int64_t)hk * D + (wave - 2) * kFetch * 16 + col) << L.page_shift);
+    const int64_t page_stride = keys ? L.k_page_stride : L.v_page_stride;
+    const int piece_step = keys ? 4 * kMine : 16 << L.page_shift;  // elements from piece to piece
+    const int slot_step = keys ? D : 1;
+    for (int w0 = begin; w0 < end; w0 += kWindow << L.page_shift) {
+    const int w1 = min(end, w0 + (kWindow << L.page_shift));
+    const bool any_bad = stage_ids(L, table, w0, w1, ids);
+    const int first_page = w0 >> L.page_shift;
+    // tokens past the last read the last page again
+    auto fetch = [&](int t, u32x4 (&x)[kFetch]) __attribute__((always_inline)) {
+      const int id = max(0, ids[(min(t + my_token, w1 - 1) >> L.page_shift) - first_page]);
+      const T *at = base + (int64_t)id * page_stride + ((t + my_token) & page_mask) * slot_step;
+#pragma unroll
+      for (int i = 0; i < kFetch; ++i) x[i] = ld_cache<kPast>(at + i * piece_step);
+    };
+    u32x4 ahead[kDeep][kFetch];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (w0 + i * kKeys < w1) fetch(w0 + i * kKeys, ahead[i]);
+    int buf = 0;
+    for (int t1 = w0; t1 < w1; t1 += kDeep * kKeys) {
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const int t = t1 + i * kKeys;
+        if (t >= w1) break;  // uniform
+        u32x4(*to)[kWave] = ring[buf];
+#pragma unroll
+        for (int f = 0; f < kFetch; ++f) to[wave * kFetch + f][lane] = ahead[i][f];
+        if (t + kDeep * kKeys < w1) fetch(t + kDeep * kKeys, ahead[i]);
+        // the step's pieces are in LDS; the buffer written next was last read
+        // before this barrier
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        buf ^= 1;
+
+        if (16 * wave >= rows) continue;  // no rows of this wave
+        const bool edge = any_bad || t + kKeys > least_high || t < most_low;  // uniform
+        // two straight paths, so that the reads from LDS and the products overlap
+        auto step = [&](auto at_edge) __attribute__((always_inline)) {
+          constexpr bool kEdge = decltype(at_edge)::value;
+          const int t0 = t + kMine * g;
+          float s[kMine];
+          typename St::template K<D> k;
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+            for (int f = 0; f < kOut / kTiles; ++f) k.v[u][f] = to[u * (kOut / kTiles) + f][lane];
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u) {
+            const floatx4 a = St::template scores<D>(k, u, q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[4 * u + e] = a[e];
+          }
+          bool bad = false;
+          if (kEdge) {
+            if (any_bad) {
+              bad = ids[(min(t0, w1 - 1) >> L.page_shift) - first_page] < 0;
+              if (bad) bits |= kErrPage;
+            }
+            mask_scores<kMine>(s, row, t0, bad);
+          }
+          const typename St::P pr = weigh<T, kOut>(s, to_log2, row, o);
+#pragma unroll
+          for (int d = 0; d < kOut; ++d) {
+            u32x4 v = to[kOut + d][lane];
+            bool mixed = false;
+            if (kEdge) {
+              v = St::keep(v, 0, bad ? 0 : sl.len - t0);
+              mixed = __ballot(St::not_finite(v)) != 0;
+            }
+            o[d] = mixed ? product_mixed<T>(v, pr, row, t0, o[d]) : St::product(v, pr, o[d]);
+          }
+        };
+        if (edge) step(Flag<true>{});
+        else step(Flag<false>{});
+      }
+    }
+    }
+    if (bits) flag_error(L.err, bits);
+    const int c = 16 * wave + col;
+    float sum = row.l;
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (c < rows) {
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) {
+        const float x[4] = {o[d][0], o[d][1], o[d][2], o[d][3]};
+        write_row<T>(p, sl, hk, slot, block_row, c, 16 * d + 4 * g, row.m, sum, x);
+      }
+    }
+    __syncthreads();  // the ring is free for the next item
+  }
+}
+
+// The parts of one (new token, query head) of a unit that was cut: one wave where
+// they are few, the workgroup's four together where they may be many.  A part takes D / 4 lanes, so a wave reads 256 / D of them (two for D = 96) at a time.
+template <typename T, int D>
+__global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
+  constexpr int kLanes = D / 4, kSide = kWave / kLanes;
+  __shared__ float lds_x[kWaves][D];
+  __shared__ float lds_sum[kWaves];
+  const AttendLaunch &L = p.L;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int r = blockIdx.x;
-  const int2 st = p.stretches[r];
-  if (st.y < 0) return;
   int bits = 0;
   const Slice s = slice_of(L, r, &bits);
-  const int group = p.heads_per_group, D = L.D;
-  const int blocks = (s.n * group + p.block_rows - 1) / p.block_rows;
-  const int splits = (s.len - first_token(L, s) + st.x - 1) / st.x;
-  const int waves = gridDim.y * kWaves;
-  for (int i = blockIdx.y * kWaves + threadIdx.x / kWave; i < s.n * L.Hq; i += waves) {
-    const int j = i / L.Hq, h = i % L.Hq, hk = h / group, row = j * group + h % group;
-    const int b = row / p.block_rows;
-    // slot of stretch k: st.y + k blocks + b
-    const int64_t first = ((int64_t)(st.y + b) * L.Hkv + hk) * p.block_rows + row % p.block_rows;
-    const int64_t next = (int64_t)blocks * L.Hkv * p.block_rows;
+  const Units u = units_of(p, s);
+  const int64_t share = p.head[0], at0 = p.before[r];
+  if (u.blocks == 0 || at0 / share == (at0 + (int64_t)u.blocks * u.size - 1) / share) return;
+  const int group = p.heads_per_group;
+  // a unit has at most so many parts
+  const int most = (int)(u.size / share) + 2;
+  const int together = most > 8 ? kWaves : 1, at_once = kWaves / together;  // waves a row, rows
+  const int part = wave % together, side = lane / kLanes, d = lane % kLanes * 4;
+  int unit = -1, s0 = 0, splits = 0;
+  for (int i0 = blockIdx.y * at_once; i0 < s.n * L.Hq; i0 += gridDim.y * at_once) {
+    const int i = i0 + wave / together;
+    const bool there = i < s.n * L.Hq;
+    const int j = there ? i / L.Hq : 0, h = there ? i % L.Hq : 0, hk = h / group;
+    const int row = j * group + h % group, b = row / p.block_rows;
+    if (b != unit) {  // most rows follow one of the same unit
+      unit = b;
+      const int64_t at = at0 + (int64_t)b * u.size;
+      s0 = (int)(at / share);
+      splits = (int)((at + u.size - 1) / share) - s0 + 1;
+    }
+    // part k: what share s0 + k left, the first of them as its last
+    const int64_t slot_size = (int64_t)L.Hkv * p.block_rows;
+    const int64_t base = (int64_t)hk * p.block_rows + row % p.block_rows;
+    auto part_at = [&](int k) __attribute__((always_inline)) {
+      return base + (2 * (int64_t)(s0 + k) + (k == 0)) * slot_size;
+    };
     float mx = kNone;
-    for (int k = lane; k < splits; k += kWave) mx = fmaxf(mx, p.part_ml[first + k * next].x);
+    for (int k = lane; k < splits; k += kWave) mx = fmaxf(mx, p.part_ml[part_at(k)].x);
     mx = wave_max(mx);
     float all = 0.0f, x[4] = {0, 0, 0, 0};
-    const int d = lane * 4;
-    for (int k = 0; k < splits; ++k) {
-      const float2 ml = p.part_ml[first + k * next];
-      const float f = exp2_fast(ml.x - mx);
-      all += f * ml.y;
-      if (d < D) {
-        const floatx4 y = *reinterpret_cast<const floatx4 *>(p.part_o + (first + k * next) * D + d);
+    if (side < kSide) {
+#pragma unroll 4
+      for (int k = part * kSide + side; k < splits; k += together * kSide) {
+        const float2 ml = p.part_ml[part_at(k)];
+        const floatx4 y = *reinterpret_cast<const floatx4 *>(p.part_o + part_at(k) * D + d);
+        const float f = exp2_fast(ml.x - mx);
+        all += f * ml.y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += f * y[e];
       }
     }
-    const float inv = all > 0.0f ? 1.0f / all : (all == 0.0f ? 0.0f : all);
+    // over the sides of the wave, in order
+    float sum = 0.0f, y[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] *= inv;
-    const int64_t out_row = (int64_t)(s.row0 + j) * L.Hq + h;
-    if (d < D) store4(reinterpret_cast<T *>(L.out) + out_row * D + d, x);
-    if (lane == 0 && L.lse != nullptr)
-      L.lse[out_row] = all == 0.0f ? -INFINITY : fmaf(mx, 0.6931471805599453f, logf(all));
+    for (int v = 0; v < kSide; ++v) {
+      const int from = v * kLanes + lane % kLanes;
+      sum += __shfl(all, from);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] += __shfl(x[e], from);
+    }
+    if (together > 1) {
+      __syncthreads();
+      if (lane < kLanes) store4(&lds_x[wave][d], y);
+      if (lane == 0) lds_sum[wave] = sum;
+      __syncthreads();
+      sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = 0.0f;
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) {
+        sum += lds_sum[v];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += lds_x[v][d + e];
+      }
+    }
+    if (there && splits > 1 && part == 0 && lane < kLanes) {
+      const int rr = row % p.block_rows;
+      write_row<T>(p, s, hk, -1, row - rr, rr, d, mx, sum, y);
+    }
   }
 }
 
 // ------------------------------------------------------------------- launch
 namespace {
 
-// Row tiles of a block: enough for the mean request's rows, so that the keys are
-// read once for all of them (a request with more takes several blocks, which read
-// them again from the caches); registers allow 4 tiles up to D = 128, 1 beyond.
-int row_tiles(int R, int rows_capacity, int group, int D) {
-  const int rows = (int)(((int64_t)rows_capacity * group + R - 1) / R);
-  if (D > 128 || rows <= 16) return 1;
-  return rows <= 32 ? 2 : 4;
+// Rows of a block.  Up to 16 rows a request on the mean (single tokens): 16, and
+// the waves share the tokens.  Beyond: 64, 16 a wave.
+int rows_of_block(int R, int rows_capacity, int group) {
+  return (int64_t)rows_capacity * group <= (int64_t)16 * R ? 16 : 64;
 }
 
 struct Sizes {
-  int tiles, block_rows;
-  int64_t items, slots;
+  int block_rows, shares;
 };
 Sizes sizes_of(int R, int rows_capacity, int Hq, int Hkv, int D) {
-  Sizes z;
-  const int group = Hq / Hkv;
-  z.tiles = row_tiles(R, rows_capacity, group, D);
-  z.block_rows = 16 * z.tiles;
-  z.slots = 2 * kTarget / Hkv + 2;
-  z.items = R + ((int64_t)rows_capacity * group) / z.block_rows + z.slots;
-  return z;
+  return {rows_of_block(R, rows_capacity, Hq / Hkv), (kShares + Hkv - 1) / Hkv};
 }
 
-template <typename T, int D, int MT> void launch_one(const AttendParams &p, int grid, hipStream_t stream) {
-  DSPARK_LAUNCH("attend", stream, (attend_kernel<T, D, MT>), grid, kBlock, p);
+template <typename T, int D, bool kPast>
+void launch_rows(const AttendParams &p, int grid, hipStream_t stream) {
+  if (p.block_rows == 16)
+    DSPARK_LAUNCH("attend_few", stream, (attend_few_kernel<T, D, kPast>), grid, kBlock, p);
+  else
+    DSPARK_LAUNCH("attend_many", stream, (attend_many_kernel<T, D, kPast>), grid, kBlock, p);
 }
 template <typename T, int D>
-void launch_tiles(const AttendParams &p, int tiles, int grid, hipStream_t stream) {
-  if constexpr (D <= 128) {
-    if (tiles == 4) return launch_one<T, D, 4>(p, grid, stream);
-    if (tiles == 2) return launch_one<T, D, 2>(p, grid, stream);
-  }
-  launch_one<T, D, 1>(p, grid, stream);
+void launch_product(const AttendParams &p, int grid, dim3 join_grid, hipStream_t stream) {
+  // whether a step's 64 bytes are a page's whole row of values (see ld_cache)
+  if ((sizeof(T) << p.L.page_shift) <= 64) launch_rows<T, D, true>(p, grid, stream);
+  else launch_rows<T, D, false>(p, grid, stream);
+  DSPARK_LAUNCH("attend_join", stream, (attend_join_kernel<T, D>), join_grid, kBlock, p);
 }
 
 template <typename T> hipError_t launch_attend_t(const AttendLaunch &L, hipStream_t stream) {
@@ -668,30 +935,28 @@ template <typename T> hipError_t launch_attend_t(const AttendLaunch &L, hipStrea
   p.L = L;
   p.heads_per_group = L.Hq / L.Hkv;
   p.block_rows = z.block_rows;
-  p.most_items = (int)z.items;
-  p.most_slots = (int)z.slots;
+  p.most_shares = z.shares;
   char *at = (char *)L.scratch;
   auto take = [&](size_t bytes) { char *c = at; at += ws_align(bytes); return c; };
-  p.head = (int32_t *)take(256);
-  p.items = (int4 *)take((size_t)z.items * 16);
-  p.stretches = (int2 *)take((size_t)L.R * 8);
-  p.part_ml = (float2 *)take((size_t)z.slots * L.Hkv * z.block_rows * 8);
-  p.part_o = (float *)take((size_t)z.slots * L.Hkv * z.block_rows * L.D * 4);
-  // appenders: a workgroup for every 4 rows of a request or so
+  const size_t parts = (size_t)2 * z.shares * L.Hkv * z.block_rows;
+  p.head = (int64_t *)take(256);
+  p.before = (int64_t *)take(((size_t)L.R + 1) * 8);
+  p.first = (int32_t *)take((size_t)z.shares * 4);
+  p.part_ml = (float2 *)take(parts * 8);
+  p.part_o = (float *)take(parts * L.D * 4);
+  // a workgroup for every row of a request or so
   const int64_t mean = (L.rows_capacity + L.R - 1) / L.R;
-  const int parts = L.k_new == nullptr ? 0 : (int)(mean < 4 ? 1 : mean < 256 ? (mean + 3) / 4 : 64);
-  DSPARK_LAUNCH("attend_prepare", stream, attend_prepare_kernel<T>, 1 + L.R * parts, kBlock, p);
-  const int64_t most = z.items * L.Hkv;
-  const int grid = (int)(most < 8 * kComputeUnits ? most : 8 * kComputeUnits);
-  switch (L.D) {
-    case 64: launch_tiles<T, 64>(p, z.tiles, grid, stream); break;
-    case 96: launch_tiles<T, 96>(p, z.tiles, grid, stream); break;
-    case 128: launch_tiles<T, 128>(p, z.tiles, grid, stream); break;
-    default: launch_tiles<T, 256>(p, z.tiles, grid, stream); break;
-  }
+  const int appenders = L.k_new == nullptr ? 0 : (int)(mean < 64 ? mean : 64);
+  DSPARK_LAUNCH("attend_prepare", stream, attend_prepare_kernel<T>, 1 + L.R * appenders, kBlock, p);
+  const int grid = z.shares * L.Hkv;
   const int64_t heads = mean * L.Hq;
-  const int gy = (int)(heads < 4 * 64 ? (heads + 3) / 4 : 64);
-  DSPARK_LAUNCH("attend_join", stream, attend_join_kernel<T>, dim3(L.R, gy), kBlock, p);
+  const dim3 join(L.R, (unsigned)(heads < 64 ? heads : 64));
+  switch (L.D) {
+    case 64: launch_product<T, 64>(p, grid, join, stream); break;
+    case 96: launch_product<T, 96>(p, grid, join, stream); break;
+    case 128: launch_product<T, 128>(p, grid, join, stream); break;
+    default: launch_product<T, 256>(p, grid, join, stream); break;
+  }
   return hipGetLastError();
 }
 
@@ -700,8 +965,8 @@ template <typename T> hipError_t launch_attend_t(const AttendLaunch &L, hipStrea
 size_t attend_ws_bytes(int R, int rows_capacity, int Hq, int Hkv, int D, bool bf16) {
   (void)bf16;
   const Sizes z = sizes_of(R, rows_capacity, Hq, Hkv, D);
-  const size_t parts = (size_t)z.slots * Hkv * z.block_rows;
-  return kWsHeader + 256 + ws_align((size_t)z.items * 16) + ws_align((size_t)R * 8) +
+  const size_t parts = (size_t)2 * z.shares * Hkv * z.block_rows;
+  return kWsHeader + 256 + ws_align(((size_t)R + 1) * 8) + ws_align((size_t)z.shares * 4) +
          ws_align(parts * 8) + ws_align(parts * D * 4);
 }
 
