@@ -117,7 +117,7 @@ struct LogprobsLaunch {
   float *logp, *entropy, *stats, *top_logp;
   int32_t *top_ids;
   int32_t *err;
-  void *scratch;  // [n_rows][chunks] sums, then [n_rows][chunks][k] keys
+  void *scratch;  // [n_rows][chunks] sums, then with k > 0 the maximum of every line
 };
 
 struct LogprobsGradLaunch {

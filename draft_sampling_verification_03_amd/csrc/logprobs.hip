@@ -5,15 +5,14 @@
 // one row and keeps it in registers (every load in flight at once), so the row
 // is read from memory once; from the registers come the chunk's maximum, then
 //   S = sum 2^u, E = sum 2^u u, u = (x - max) log2(e) / T   (no running rescale)
-// and the chunk's k largest elements.  logprob_join_kernel: one workgroup a row
-// joins the chunks by their maxima, and
-//   log S, entropy = log S - E ln 2 / S, logp = (x_t - max) / T - log S.
-//
-// Top k of a chunk without sorting it: every wave finds the ceil(k / 4)-th
-// largest of its lanes' maxima (the lanes hold different elements, so at least
-// ceil(k / 4) elements of the wave reach it); the least of the four is a
-// threshold that at least k elements of the chunk reach, and hardly more than
-// that.  Those are collected and ranked by counting.
+// and the maximum of every 128 bytes.  logprob_join_kernel: one workgroup a row
+// joins the chunks by their maxima,
+//   log S, entropy = log S - E ln 2 / S, logp = (x_t - max) / T - log S,
+// and finds the alternatives among the 128-byte lines: a threshold that at least k
+// of the lines' maxima reach (and hardly more), those lines read again, and their
+// elements that reach it ranked by counting.  So the alternatives cost the pass
+// over the row one comparison of maxima, and no element is looked at twice but
+// those of some 40 lines.
 #include <limits.h>
 
 #include "common.h"
@@ -24,7 +23,10 @@ namespace dspark {
 
 namespace {
 
-constexpr int kMaxCand = 1024;  // collected elements of a chunk or a row
+constexpr int kMaxCand = 1024;  // elements of a row that are ranked
+constexpr int kLine = 8;        // pieces of 16 bytes in a line
+constexpr int kMaxLines = 128;  // lines of a row that are read again
+constexpr int kHeld = 32;       // lines' maxima a thread: V = 262144 fp32 has 8192 lines
 
 // Order of the alternatives: larger value first, then smaller index.  A key
 // holds the value's bits as an ordered integer above the index's complement;
@@ -45,6 +47,44 @@ __device__ __forceinline__ uint64_t wave_max_key(uint64_t v) {
   for (int o = 32; o >= 1; o >>= 1) {
     const uint64_t w = __shfl_xor((unsigned long long)v, o);
     v = w > v ? w : v;
+  }
+  return v;
+}
+
+// Maximum of three; the instruction takes any values, where fmaxf spends one more
+// on each operand that might be a signalling NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+// Maximum of a 16-byte piece.
+__device__ __forceinline__ float piece_max(const u32x4 &v, bf16_t *) {
+  float x[8];
+  unpack16(v, (bf16_t *)nullptr, x);
+  return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], -INFINITY));
+}
+__device__ __forceinline__ float piece_max(const u32x4 &v, float *) {
+  return max3(__uint_as_float(v[0]), __uint_as_float(v[1]),
+              max3(__uint_as_float(v[2]), __uint_as_float(v[3]), -INFINITY));
+}
+// Maximum over the eight lanes of a line.
+__device__ __forceinline__ float eight_max(float v) {
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true)));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true)));
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true)));
+}
+// Two bf16 or one fp32 minus infinity.
+__device__ __forceinline__ uint32_t masked_word(bf16_t *) { return 0xFF80FF80u; }
+__device__ __forceinline__ uint32_t masked_word(float *) { return 0xFF800000u; }
+// A piece whose elements from n on are masked.
+template <typename T> __device__ __forceinline__ u32x4 keep_first(u32x4 v, int n) {
+  constexpr int kIn = 4 / (int)sizeof(T);  // elements of a word
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int left = n - i * kIn;
+    if (left <= 0) v[i] = masked_word((T *)nullptr);
+    else if (left < kIn) v[i] = (v[i] & 0xFFFFu) | 0xFF800000u;
   }
   return v;
 }
@@ -82,6 +122,7 @@ __device__ __forceinline__ void rank_keys(const uint64_t *buf, int n, int k, F w
   for (int i = threadIdx.x; i < n; i += kBlock) {
     const uint64_t mine = buf[i];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) rank += buf[j] > mine;
     if (rank < k) write(rank, mine);
   }
@@ -93,8 +134,8 @@ struct ChunkParams {
   float scale;  // log2(e) / T
   const void *X;
   const int32_t *row_offset;
-  float4 *sums;    // [n_rows][n_chunks]: (max x, S, E, unused)
-  uint64_t *keys;  // [n_rows][n_chunks][k], descending, 0 behind the last
+  float4 *sums;   // [n_rows][n_chunks]: (max x, S, E, unused)
+  float *lines;   // [n_rows][n_chunks][kBlock / kLine][VPT]: maximum of each line
 };
 
 }  // namespace
@@ -103,8 +144,6 @@ template <typename T, int VPT>
 __global__ __launch_bounds__(kBlock) void logprob_chunk_kernel(ChunkParams p) {
   constexpr int kPer = Elem<T>::kPerVec;
   __shared__ float red[8];
-  __shared__ uint64_t cand[kMaxCand];
-  __shared__ int n_cand;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int row = blockIdx.x / p.n_chunks, c = blockIdx.x % p.n_chunks;
   if (row >= rows_in_use(p.row_offset, p.R, p.n_rows)) return;
@@ -117,44 +156,36 @@ __global__ __launch_bounds__(kBlock) void logprob_chunk_kernel(ChunkParams p) {
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
     raw[j] = ld_stream4(X + (int64_t)min(p0 + j * kBlock + tid, p1 - 1) * kPer);
-  if (tid == 0) n_cand = 0;
 
-  // element q of piece j; past the chunk or the vocabulary: -infinity
-  auto value = [&](int j, int q, const float *x) __attribute__((always_inline)) {
-    const int piece = p0 + j * kBlock + tid;
-    return piece < p1 && piece * kPer + q < p.V ? x[q] : -INFINITY;
-  };
-  float pm[VPT], tm = -INFINITY;
+  // past the chunk or the vocabulary: masked
+  if (p1 - p0 < VPT * kBlock) {  // uniform
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      raw[j] = p0 + j * kBlock + tid < p1 ? raw[j] : u32x4(masked_word((T *)nullptr));
+  }
+  if (p1 == n_pieces && p.V % kPer != 0) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (p0 + j * kBlock + tid == p1 - 1) raw[j] = keep_first<T>(raw[j], p.V % kPer);
+  }
+  // maxima: of the pieces, of the lines (8 lanes), of the chunk
+  float tm = -INFINITY, line = -INFINITY;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    float x[kPer];
-    unpack16(raw[j], (T *)nullptr, x);
-    pm[j] = -INFINITY;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) pm[j] = fmaxf(pm[j], value(j, q, x));
-    tm = fmaxf(tm, pm[j]);
-  }
-
-  // threshold of the k largest
-  const int kw = (p.k + 3) / 4;
-  float thr = tm;
-  if (kw > 0) {
-    float left = tm;
-    uint64_t out = 0;  // lanes taken
-    for (int i = 0; i < kw; ++i) {
-      thr = wave_max(left);
-      const uint64_t at = __ballot(left == thr) & ~out;
-      if (at == 0) { thr = -INFINITY; break; }  // NaN lanes
-      const uint64_t one = at & (~at + 1);
-      out |= one;
-      if (one >> lane & 1) left = -INFINITY;
+    float m = piece_max(raw[j], (T *)nullptr);
+    tm = fmaxf(tm, m);
+    if (p.k > 0) {
+      m = eight_max(m);
+      if ((lane & (kLine - 1)) == j) line = m;  // lane j of the eight writes line j
     }
   }
+  if (p.k > 0 && (lane & (kLine - 1)) < VPT)
+    p.lines[((int64_t)row * p.n_chunks + c) * (kBlock / kLine * VPT) + tid / kLine * VPT +
+            (lane & (kLine - 1))] = line;
   const float wm = wave_max(tm);
-  if (lane == 0) { red[wave] = wm; red[4 + wave] = thr; }
+  if (lane == 0) red[wave] = wm;
   __syncthreads();
   const float mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  thr = fminf(fminf(red[4], red[5]), fminf(red[6], red[7]));
 
   float S = 0.0f, E = 0.0f;
   if (mx != -INFINITY) {
@@ -164,8 +195,7 @@ __global__ __launch_bounds__(kBlock) void logprob_chunk_kernel(ChunkParams p) {
       unpack16(raw[j], (T *)nullptr, x);
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        const float u = (value(j, q, x) - mx) * p.scale;
-        const float e = exp2_fast(u);
+        const float u = (x[q] - mx) * p.scale, e = exp2_fast(u);
         S += e;
         E = fmaf(e, fmaxf(u, -1e4f), E);  // a masked logit has e = 0: its u only has to be finite
       }
@@ -176,67 +206,13 @@ __global__ __launch_bounds__(kBlock) void logprob_chunk_kernel(ChunkParams p) {
       float x[kPer];
       unpack16(raw[j], (T *)nullptr, x);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const float v = value(j, q, x);
-        if (v != v) S = v;
-      }
+      for (int q = 0; q < kPer; ++q)
+        if (x[q] != x[q]) S = x[q];
     }
   }
   const float Sw = wave_sum(S), Ew = wave_sum(E);
-  if (p.k > 0) {
-    // the finite elements that reach the threshold (masked ones are filled in by the join)
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (pm[j] >= thr && pm[j] != -INFINITY) {
-        float x[kPer];
-        unpack16(raw[j], (T *)nullptr, x);
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          const float v = value(j, q, x);
-          if (v >= thr && v != -INFINITY) {
-            const int at = atomicAdd(&n_cand, 1);
-            if (at < kMaxCand) cand[at] = alt_key(v, (p0 + j * kBlock + tid) * kPer + q);
-          }
-        }
-      }
-    }
-  }
-  __syncthreads();
+  __syncthreads();  // every wave has read the maxima
   if (lane == 0) { red[wave] = Sw; red[4 + wave] = Ew; }
-  uint64_t *keys = p.keys + ((int64_t)row * p.n_chunks + c) * p.k;
-  const int n = n_cand;
-  if (p.k > 0 && n <= kMaxCand) {
-    rank_keys(cand, n, p.k, [&](int rank, uint64_t key) { keys[rank] = key; });
-    for (int i = n + tid; i < p.k; i += kBlock) keys[i] = 0;
-  } else if (p.k > 0) {
-    // more equal or unevenly spread elements than fit: k rounds, each the
-    // largest element of the registers below the one before
-    uint64_t before = ~0ull;
-    __syncthreads();
-    for (int i = 0; i < p.k; ++i) {
-      uint64_t best = 0;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        float x[kPer];
-        unpack16(raw[j], (T *)nullptr, x);
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          const float v = value(j, q, x);
-          if (v == -INFINITY) continue;
-          const uint64_t key = alt_key(v, (p0 + j * kBlock + tid) * kPer + q);
-          if (key < before && key > best) best = key;
-        }
-      }
-      best = wave_max_key(best);
-      if (lane == 0) cand[wave] = best;
-      __syncthreads();
-      best = cand[0];
-      for (int w = 1; w < kBlock / kWave; ++w) best = cand[w] > best ? cand[w] : best;
-      before = best;
-      if (tid == 0) keys[i] = best;
-      __syncthreads();
-    }
-  }
   __syncthreads();
   if (tid == 0)
     p.sums[(int64_t)row * p.n_chunks + c] =
@@ -246,17 +222,32 @@ __global__ __launch_bounds__(kBlock) void logprob_chunk_kernel(ChunkParams p) {
 
 namespace {
 struct JoinParams {
-  int n_rows, V, R, k, n_chunks, tok_stride;
+  int n_rows, V, R, k, n_chunks, pieces_per_chunk, vpt, tok_stride;
   int64_t row_stride;
   float invT, invT_low, scale;  // 1 / T and what its rounding left; log2(e) / T
   const void *X;
   const int32_t *tokens, *row_offset;
   const float4 *sums;
-  const uint64_t *keys;
+  const float *lines;
   float *logp, *entropy, *stats, *top_logp;
   int32_t *top_ids;
   int32_t *err;
 };
+
+// Sum of a count over the workgroup.
+__device__ __forceinline__ int block_count(int v, int *scratch) {
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if ((threadIdx.x & (kWave - 1)) == 0) scratch[threadIdx.x / kWave] = v;
+  __syncthreads();
+  return scratch[0] + scratch[1] + scratch[2] + scratch[3];
+}
+
+// Floats as unsigned integers in the same order, and back.
+__device__ __forceinline__ uint32_t ordered(float x) { return (uint32_t)(alt_key(x, 0) >> 32); }
+__device__ __forceinline__ float from_ordered(uint32_t o) { return key_value((uint64_t)o << 32); }
+
 }  // namespace
 
 template <typename T>
@@ -264,92 +255,172 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
   __shared__ float red[8];
   __shared__ uint64_t cand[kMaxCand];
   __shared__ uint64_t picked[64];
-  __shared__ int n_cand;
+  __shared__ int list[kMaxLines];
+  __shared__ int n_cand, n_list;
+  __shared__ int counts[4];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int row = blockIdx.x;
   const int used = rows_in_use(p.row_offset, p.R, p.n_rows);
   if (row == 0 && tid == 0 && p.row_offset != nullptr && p.row_offset[p.R] > p.n_rows)
     flag_error(p.err, kErrLength);
   if (row >= used) return;
-  if (tid == 0) n_cand = 0;
-  const float4 *sums = p.sums + (int64_t)row * p.n_chunks;
-  float mx = -INFINITY;
-  for (int c = tid; c < p.n_chunks; c += kBlock) mx = fmaxf(mx, sums[c].x);
-  mx = block_max(mx, red);
-  float S = 0.0f, E = 0.0f;
-  for (int c = tid; c < p.n_chunks; c += kBlock) {
-    const float4 s = sums[c];
-    // a chunk of the type's lowest values: f is 0, and d only has to be finite
-    const float d = fmaxf((s.x - mx) * p.scale, -1e4f), f = exp2_fast(d);
-    if (s.y != 0.0f) {  // a chunk that is all masked has no sum
-      S += s.y * f;
-      E += f * (s.z + s.y * d);
+  if (tid == 0) n_cand = n_list = 0;
+  const T *X = reinterpret_cast<const T *>(p.X) + (int64_t)row * p.row_stride;
+  // everything that the row needs is asked for at once: a chunk's sums a thread,
+  // the lines' maxima, the token and its logit
+  constexpr int kPer = Elem<T>::kPerVec;
+  const int n_pieces = (p.V + kPer - 1) / kPer;
+  const int per_chunk = kBlock / kLine * p.vpt, n_lines = p.k > 0 ? p.n_chunks * per_chunk : 0;
+  const float4 sum = tid < p.n_chunks ? p.sums[(int64_t)row * p.n_chunks + tid]
+                                      : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  float held[kHeld];
+  const float *lines = p.lines + (int64_t)row * n_lines;
+#pragma unroll
+  for (int b = 0; b < kHeld; b += 8) {
+#pragma unroll
+    for (int i = b; i < b + 8; ++i) held[i] = -INFINITY;
+    if (b * kBlock < n_lines) {  // uniform
+#pragma unroll
+      for (int i = b; i < b + 8; ++i) {
+        const float m = lines[min(i * kBlock + tid, n_lines - 1)];
+        held[i] = i * kBlock + tid < n_lines ? m : -INFINITY;
+      }
     }
   }
-  S = block_sum(S, red);
-  E = block_sum(E, red);
+  int tok = -1;
+  float x_tok = 0.0f;
+  if (wave == 0) {
+    tok = token_of_row(p.tokens, p.row_offset, p.R, p.tok_stride, row);
+    if (tok >= 0 && tok < p.V) x_tok = Elem<T>::at(X, tok);
+  }
+  const float mx = block_max(sum.x, red);
+  float S = 0.0f, E = 0.0f;
+  {
+    // a chunk of the type's lowest values: f is 0, and d only has to be finite
+    const float d = fmaxf((sum.x - mx) * p.scale, -1e4f), f = exp2_fast(d);
+    if (sum.y != 0.0f) {  // a chunk that is all masked has no sum
+      S = sum.y * f;
+      E = f * (sum.z + sum.y * d);
+    }
+  }
+  S = wave_sum(S);
+  E = wave_sum(E);
+  if (lane == 0) { red[wave] = S; red[4 + wave] = E; }
+  __syncthreads();
+  S = ((red[0] + red[1]) + red[2]) + red[3];
+  E = ((red[4] + red[5]) + red[6]) + red[7];
   const bool ok = isfinite(mx) && isfinite(S) && S > 0.0f;
   const float logS = logf(S);
-  const T *X = reinterpret_cast<const T *>(p.X) + (int64_t)row * p.row_stride;
-  if (wave == 0) {
-    const int tok = token_of_row(p.tokens, p.row_offset, p.R, p.tok_stride, row);
-    if (lane == 0) {
-      int bits = ok ? 0 : kErrNonFinite;
-      if (p.logp != nullptr) {
-        float lp = 0.0f;
-        if (tok < -1 || tok >= p.V) {
-          bits |= kErrToken;
-          lp = NAN;
-        } else if (tok >= 0) {
-          const float d = Elem<T>::at(X, tok) - mx;
-          lp = fmaf(d, p.invT, -logS);
-        }
-        p.logp[row] = ok ? lp : NAN;
+  if (tid == 0) {
+    int bits = ok ? 0 : kErrNonFinite;
+    if (p.logp != nullptr) {
+      float lp = 0.0f;
+      if (tok < -1 || tok >= p.V) {
+        bits |= kErrToken;
+        lp = NAN;
+      } else if (tok >= 0) {
+        lp = fmaf(x_tok - mx, p.invT, -logS);
       }
-      if (p.entropy != nullptr) p.entropy[row] = ok ? logS - E * 0.6931471805599453f / S : NAN;
-      if (p.stats != nullptr) {
-        // S belongs to the exact max / T; the stored m is that rounded
-        const float m = mx * p.invT;
-        const float off = fmaf(mx, p.invT_low, fmaf(mx, p.invT, -m));
-        p.stats[2 * (int64_t)row] = ok ? m : NAN;
-        p.stats[2 * (int64_t)row + 1] = ok ? S + S * off : NAN;
-      }
-      if (bits) flag_error(p.err, bits);
+      p.logp[row] = ok ? lp : NAN;
     }
+    if (p.entropy != nullptr) p.entropy[row] = ok ? logS - E * 0.6931471805599453f / S : NAN;
+    if (p.stats != nullptr) {
+      // S belongs to the exact max / T; the stored m is that rounded
+      const float m = mx * p.invT;
+      const float off = fmaf(mx, p.invT_low, fmaf(mx, p.invT, -m));
+      p.stats[2 * (int64_t)row] = ok ? m : NAN;
+      p.stats[2 * (int64_t)row + 1] = ok ? S + S * off : NAN;
+    }
+    if (bits) flag_error(p.err, bits);
   }
   if (p.k == 0) return;
 
-  // Threshold: the k-th largest of the chunks' q-th elements, q the least with
-  // n_chunks q >= k ... for q = 1 the k-th largest head, else the least q-th one.
-  const uint64_t *keys = p.keys + (int64_t)row * p.n_chunks * p.k;
-  const int q = (p.k + p.n_chunks - 1) / p.n_chunks;
-  uint64_t thr = 0;
-  if (q > 1) {
-    uint64_t low = ~0ull;
-    for (int c = lane; c < p.n_chunks; c += kWave) {
-      const uint64_t v = keys[(int64_t)c * p.k + q - 1];
-      low = v < low ? v : low;
-    }
-    thr = ~wave_max_key(~low);
-  } else {
-    for (int c = tid; c < p.n_chunks && c < kMaxCand; c += kBlock) cand[c] = keys[(int64_t)c * p.k];
-    if (tid == 0) picked[0] = 0;
-    __syncthreads();
-    // heads of all-masked chunks are 0 and equal: they leave picked[0] at 0
-    rank_keys(cand, min(p.n_chunks, kMaxCand), p.k, [&](int rank, uint64_t key) {
-      if (rank == p.k - 1) picked[0] = key;
-    });
-    __syncthreads();
-    thr = picked[0];
+  // Threshold.  The lanes hold different lines, so with the ceil(k / 4)-th largest
+  // of each wave's lanes at least k lines reach the least of the four.
+  float left = -INFINITY, thr = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) left = fmaxf(left, held[i]);
+  uint64_t out = 0;  // lanes taken
+  for (int i = 0; i < (p.k + 3) / 4; ++i) {
+    thr = wave_max(left);
+    const uint64_t at = __ballot(left == thr) & ~out;
+    if (at == 0) { thr = -INFINITY; break; }  // the row has a NaN
+    const uint64_t one = at & (~at + 1);
+    out |= one;
+    if (one >> lane & 1) left = -INFINITY;
   }
+  __syncthreads();  // the sums are read
+  if (lane == 0) red[wave] = thr;
   __syncthreads();
-  const int total = p.n_chunks * p.k;
-  for (int i = tid; i < total; i += kBlock) {
-    const uint64_t v = keys[i];
-    if (v != 0 && v >= thr) {
-      const int at = atomicAdd(&n_cand, 1);
-      if (at < kMaxCand) cand[at] = v;
+  thr = fminf(fminf(red[0], red[1]), fminf(red[2], red[3]));
+  // the lines that reach it (masked elements are filled in at the end)
+  auto gather = [&](bool strictly) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const float m = held[i];
+      if (m != -INFINITY && (strictly ? m > thr : m >= thr)) {
+        const int at = atomicAdd(&n_list, 1);
+        if (at < kMaxLines) list[at] = i * kBlock + tid;
+      }
     }
+    __syncthreads();
+  };
+  gather(false);
+  bool tied = false;  // more lines share the threshold than are read again
+  if (n_list > kMaxLines) {
+    // uneven rows: the k-th largest maximum itself, by halving the range of values
+    uint32_t lo = ordered(thr), hi = ordered(mx);
+    while (lo < hi) {  // at least k lines reach lo, fewer than k pass hi
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      const float t = from_ordered(mid);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) n += held[i] >= t;
+      if (block_count(n, counts) >= p.k) lo = mid;
+      else hi = mid - 1;
+    }
+    thr = from_ordered(lo);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) n += held[i] >= thr;
+    tied = block_count(n, counts) > kMaxLines;
+    if (tid == 0) n_list = 0;
+    __syncthreads();
+    gather(tied);  // strictly: fewer than k
+  }
+  // their elements: eight threads a line, at most four pieces a thread
+  const int n_here = n_list;
+  constexpr int kRounds = kMaxLines * kLine / kBlock;
+  u32x4 raw[kRounds];
+  int first[kRounds];  // index of the piece's first element, V: none
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    const int i = (j * kBlock + tid) / kLine;
+    first[j] = p.V;
+    raw[j] = u32x4(masked_word((T *)nullptr));
+    if (i < n_here) {
+      const int id = list[i], c = id / per_chunk, in = id % per_chunk;
+      const int local = in % p.vpt * kBlock + in / p.vpt * kLine + (tid & (kLine - 1));
+      const int piece = c * p.pieces_per_chunk + local;
+      if (local < p.pieces_per_chunk && piece < n_pieces) {
+        first[j] = piece * kPer;
+        raw[j] = *reinterpret_cast<const u32x4 *>(X + (int64_t)piece * kPer);
+      }
+    }
+  }
+  auto wanted = [&](float v, int at) __attribute__((always_inline)) {
+    return at < p.V && v != -INFINITY && (tied ? v > thr : v >= thr);
+  };
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    float x[kPer];
+    unpack16(raw[j], (T *)nullptr, x);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      if (wanted(x[q], first[j] + q)) {
+        const int at = atomicAdd(&n_cand, 1);
+        if (at < kMaxCand) cand[at] = alt_key(x[q], first[j] + q);
+      }
   }
   __syncthreads();
   int n = n_cand;
@@ -357,15 +428,21 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
     rank_keys(cand, n, p.k, [&](int rank, uint64_t key) { picked[rank] = key; });
     n = min(n, p.k);
   } else {
-    // unevenly spread chunks: k rounds over all keys
+    // too many to rank: k rounds, each the largest of the registers below the last
     uint64_t before = ~0ull;
     n = p.k;
     __syncthreads();
     for (int r = 0; r < p.k; ++r) {
       uint64_t best = 0;
-      for (int i = tid; i < total; i += kBlock) {
-        const uint64_t v = keys[i];
-        if (v < before && v > best) best = v;
+#pragma unroll
+      for (int j = 0; j < kRounds; ++j) {
+        float x[kPer];
+        unpack16(raw[j], (T *)nullptr, x);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const uint64_t key = alt_key(x[q], first[j] + q);
+          if (wanted(x[q], first[j] + q) && key < before && key > best) best = key;
+        }
       }
       best = wave_max_key(best);
       if (lane == 0) cand[wave] = best;
@@ -385,21 +462,41 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
     ids[tid] = ok ? key_index(key) : -1;
     tlp[tid] = ok ? fmaf(key_value(key) - mx, p.invT, -logS) : NAN;
   }
-  // fewer than k unmasked: the lowest indices that are not among them follow.
-  // n of the first k + n indices at most are taken, so k of them are not.
-  if (n < p.k && wave == 0) {
-    int at = n;
-    for (int i0 = 0; i0 < p.k + n && at < p.k; i0 += kWave) {
-      const int i = i0 + lane;
-      bool is_free = i < p.V;
-      for (int j = 0; j < n; ++j) is_free = is_free && key_index(picked[j]) != i;
-      const uint64_t m = __ballot(is_free);
-      const int mine = at + __popcll(m & ((1ull << lane) - 1));
-      if (is_free && mine < p.k) {
-        ids[mine] = ok ? i : -1;
-        tlp[mine] = ok ? -INFINITY : NAN;
+  // Too few: elements of the value that so many lines share follow by index, then
+  // masked ones; the row is read in order until there are enough.
+  for (int pass = tied ? 0 : 1; pass < 2; ++pass) {
+    const float fill = pass == 0 ? thr : -INFINITY;
+    const float lp = ok ? fmaf(fill - mx, p.invT, -logS) : NAN;
+    for (int t = 0; t < n_pieces && n < p.k; t += kBlock) {
+      const int piece = t + tid;
+      float x[kPer];
+      int mine = 0;
+      if (piece < n_pieces) {
+        unpack16(*reinterpret_cast<const u32x4 *>(X + (int64_t)piece * kPer), (T *)nullptr, x);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) mine += piece * kPer + q < p.V && x[q] == fill;
       }
-      at += __popcll(m);
+      float total;
+      int at = n + (int)block_exclusive_scan((float)mine, red, &total);
+      if (mine > 0) {
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+          if (piece * kPer + q < p.V && x[q] == fill) {
+            if (at < p.k) {
+              ids[at] = ok ? piece * kPer + q : -1;
+              tlp[at] = lp;
+            }
+            ++at;
+          }
+      }
+      n += (int)total;
+    }
+  }
+  // a row without statistics may have neither
+  if (!ok) {
+    for (int i = n + tid; i < p.k; i += kBlock) {
+      ids[i] = -1;
+      tlp[i] = NAN;
     }
   }
 }
@@ -567,10 +664,12 @@ Split split_of(int n_rows, int V, bool bf16) {
 
 }  // namespace
 
+static size_t lines_of(const Split &s) { return (size_t)s.n_chunks * (kBlock / kLine) * s.vpt; }
+
 size_t logprobs_ws_bytes(int n_rows, int V, int k, bool bf16) {
   const Split s = split_of(n_rows, V, bf16);
-  const size_t n = (size_t)n_rows * s.n_chunks;
-  return kWsHeader + ws_align(n * 16) + ws_align(n * k * 8);
+  return kWsHeader + ws_align((size_t)n_rows * s.n_chunks * 16) +
+         (k > 0 ? ws_align((size_t)n_rows * lines_of(s) * 4) : 0);
 }
 
 template <typename T, int VPT>
@@ -586,7 +685,7 @@ template <typename T> static hipError_t launch_logprobs_t(const LogprobsLaunch &
   c.pieces_per_chunk = s.pieces_per_chunk; c.row_stride = L.row_stride;
   c.scale = (float)(1.4426950408889634 / L.temp); c.X = L.X; c.row_offset = L.row_offset;
   c.sums = (float4 *)L.scratch;
-  c.keys = (uint64_t *)((char *)L.scratch + ws_align(n * 16));
+  c.lines = (float *)((char *)L.scratch + ws_align(n * 16));
   switch (s.vpt) {
     case 8: launch_chunk<T, 8>(c, stream); break;
     case 4: launch_chunk<T, 4>(c, stream); break;
@@ -597,7 +696,8 @@ template <typename T> static hipError_t launch_logprobs_t(const LogprobsLaunch &
   j.n_rows = L.n_rows; j.V = L.V; j.R = L.R; j.k = L.k; j.n_chunks = s.n_chunks;
   j.tok_stride = L.tok_stride; j.row_stride = L.row_stride; j.invT = (float)(1.0 / L.temp);
   j.invT_low = (float)(1.0 / L.temp - (double)j.invT); j.scale = c.scale; j.X = L.X;
-  j.tokens = L.tokens; j.row_offset = L.row_offset; j.sums = c.sums; j.keys = c.keys;
+  j.tokens = L.tokens; j.row_offset = L.row_offset; j.sums = c.sums; j.lines = c.lines;
+  j.pieces_per_chunk = s.pieces_per_chunk; j.vpt = s.vpt;
   j.logp = L.logp; j.entropy = L.entropy; j.stats = L.stats; j.top_logp = L.top_logp;
   j.top_ids = L.top_ids; j.err = L.err;
   DSPARK_LAUNCH("logprob_join", stream, logprob_join_kernel<T>, L.n_rows, kBlock, j);

@@ -124,6 +124,22 @@ def test_masked(n, V, dt, k, masked):
     assert out["logp"][1] == 0 and out["entropy"][1] == 0
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("end", [1, -1])
+def test_rows_at_the_end_of_the_range(dt, end):
+    """Rows of the type's lowest (or largest) value alone: every entry alike; and
+    with one entry a step of the type apart, far enough to be 0 or 1."""
+    V = 5003
+    X, _ = make(2, V, dt, 1)
+    X.fill_(end * torch.finfo(dt).max)
+    X[1, 77] = end * torch.finfo(dt).max * (1 - torch.finfo(dt).eps)
+    tok = torch.tensor([5, 77], dtype=torch.int32, device="cuda")
+    ws = ds.Workspace()
+    out = ds.logprobs(X, tok, k=3, ws=ws)
+    assert ws.error_code() == 0
+    check(X, tok, 3, 1.0, out)
+
+
 def test_rows_without_a_distribution_and_bad_tokens():
     X, _ = make(6, 9000, BF, 3)
     X[1] = float("-inf")
