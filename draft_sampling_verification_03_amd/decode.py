@@ -19,12 +19,17 @@ alpha / (alpha + beta).  Round t schedules with the estimate from rounds
 before t, and the asynchronous top-K mode reads the estimate as it stood at
 round t - 2 (Blog, "Async scheduler in practice").  The estimate is formed
 from integer counts in float64 and rounded once to float32.
+
+With a paged cache (serving.PagedCache) the loop keeps the target's keys and
+values in step: before the target rows it reserves pages for every scheduled
+row, and after the verification it gives back what the rejected rows held.
+With `logprobs` it returns what a server sends along with the tokens.
 """
 import numpy as np
 import torch
 
 from . import _abi as A
-from . import api
+from . import api, serving
 
 
 class AcceptanceHistory:
@@ -54,8 +59,22 @@ class AcceptanceHistory:
             return np.where(t > 0, self.passed.sum(axis=0) / np.maximum(t, 1), np.nan)
 
 
+def _record_logprobs(rec, lp, row_offset, n_acc, gamma):
+    """The rows of emitted tokens (n_acc + 1 of each request's) as [R][gamma + 1] arrays."""
+    R = len(n_acc)
+    keep = np.arange(gamma + 1)[None, :] <= n_acc[:, None]
+    rows = (row_offset[:-1, None] + np.arange(gamma + 1)[None, :])[keep]
+    for name in ("logp", "entropy", "top_ids", "top_logp"):
+        if name in rec:
+            a = lp[name].cpu().numpy()
+            full = np.full((R, gamma + 1) + a.shape[1:], -1 if name == "top_ids" else np.nan, a.dtype)
+            full[keep] = a[rows]
+            rec[name].append(full)
+
+
 def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, threshold=0.0,
-           conf_of_round=None, history=None, temp=1.0, seed=0, first_round=0, stream=None):
+           conf_of_round=None, history=None, temp=1.0, seed=0, first_round=0, stream=None,
+           cache=None, logprobs=None):
     """Run `rounds` rounds for R requests.
 
     x0            [R] int32 anchors of the first round (host or device)
@@ -68,19 +87,33 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
                   are the confidences instead (conf_of_round is then ignored)
     mode          scheduler mode (ASYNC_TOPK reads the confidences of round t - 2;
                   THRESHOLD keeps each request's leading drafts with c >= threshold)
+    cache         serving.PagedCache of the R requests, holding every token before
+                  the anchors: target_rows is then called as target_rows(prev,
+                  cache) with the round's rows reserved, row i of prev being row
+                  i of cache.attend(layer, q, k, v).  The rejected rows leave the
+                  cache before the next round.  Too few pages raise RuntimeError.
+    logprobs      number of alternatives (0: none) to report beside the log
+                  probability and entropy of every emitted token
 
     Returns a dict of per-round host arrays (x, ell, n_acc, y, theta,
     n_admitted; with confidences also c and a, the predicted tokens
     tau_pred = sum_r (1 + sum_{k <= ell_r} a_rk) and the realized tau_real =
     sum_r (n_acc_r + 1)), the emitted token stream of every request (anchors
-    excluded) and, with a history, its conditional acceptance curve."""
-    ws_d, ws_s, ws_v = api.Workspace(), api.Workspace(), api.Workspace()
+    excluded) and, with a history, its conditional acceptance curve.  With
+    `logprobs` also lists of [R][gamma + 1] arrays beside y (NaN, and -1 for
+    tokens, past the emitted ones): logp, entropy and, for alternatives,
+    top_ids and top_logp with a last dimension of that number."""
+    ws_d, ws_s, ws_v, ws_l = api.Workspace(), api.Workspace(), api.Workspace(), api.Workspace()
     anchors = torch.as_tensor(np.asarray(x0, dtype=np.int32) if not torch.is_tensor(x0) else x0)
     anchors = anchors.to(W1.device, dtype=torch.int32).contiguous()
     R = anchors.numel()
     streams = [[] for _ in range(R)]
     rec = dict(ell=[], n_acc=[], y=[], theta=[], n_admitted=[], x=[], c=[], a=[], tau_pred=[],
                tau_real=[])
+    if logprobs is not None:
+        rec.update(logp=[], entropy=[])
+        if logprobs > 0:
+            rec.update(top_ids=[], top_logp=[])
     hist, past = None, []
     for i in range(rounds):
         t = first_round + i
@@ -108,11 +141,29 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
         # target row of (rho, k), k = 1..ell+1, is the target after x_{k-1} (x_0 = anchor)
         prev = np.concatenate([np.concatenate(([a[rho]], x[rho, : ell[rho]]))
                                for rho in range(R)]).astype(np.int64)
-        P = target_rows(prev)
+        if cache is not None:
+            missing = cache.reserve(s["row_offset"], stream=stream)
+            if isinstance(stream, torch.cuda.Stream):
+                stream.synchronize()
+            short = int(missing)
+            if short:
+                raise RuntimeError(f"decode: round {t} needs {short} more pages than the cache has free"
+                                   if short > 0 else f"decode: round {t} passes the cache's max_pages")
+            P = target_rows(prev, cache)
+        else:
+            P = target_rows(prev)
         v = api.verify(s["ell"], s["row_offset"], P, U, W1, W2, anchors, d["x"], d["q_stats"],
                        d["q_x"], temp=temp, seed=seed, round=t, ws=ws_v, stream=stream)
+        if cache is not None:
+            cache.commit(v["n_acc"], stream=stream)
+        lp = None
+        if logprobs is not None:
+            lp = serving.logprobs(P, v["y"], k=logprobs, row_offset=s["row_offset"], temp=temp,
+                                  ws=ws_l, stream=stream)
         n = v["n_acc"].cpu().numpy()
         y = v["y"].cpu().numpy()
+        if lp is not None:
+            _record_logprobs(rec, lp, s["row_offset"].cpu().numpy(), n, gamma)
         for rho in range(R):
             streams[rho].extend(int(tok) for tok in y[rho, : n[rho] + 1])
         anchors = torch.as_tensor(y[np.arange(R), n]).to(W1.device, dtype=torch.int32)
@@ -138,5 +189,9 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
         out["cond_accept"] = hist.curve()
         out["history"] = hist
     errs = (ws_d.error_code(stream), ws_s.error_code(stream), ws_v.error_code(stream))
+    if cache is not None:
+        errs += (cache.error_code(stream),)
+    if logprobs is not None:
+        errs += (ws_l.error_code(stream),)
     out["device_errors"] = errs
     return out

@@ -27,11 +27,26 @@ class _RowArgs(_Args):
     """_Args with a short way for arguments that are right (what is not goes
     through _Args.req, which says why), and for row strides."""
 
+    def __init__(self, where):
+        super().__init__(where)
+        self.index = None  # the GPU of the tensors so far
+
+    def add(self, t, name):
+        self.tensors.append((name, t))
+        index = t.get_device()
+        if index != self.index:
+            if self.index is not None:
+                self.device()
+            self.index = index
+        return t
+
     def req(self, t, name, dtype, shape, optional=False):
         if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            self.tensors.append((name, t))
-            return t
-        return super().req(t, name, dtype, shape, optional)
+            return self.add(t, name)
+        if super().req(t, name, dtype, shape, optional) is not None:
+            self.tensors.pop()
+            self.add(t, name)
+        return t
 
     def rows(self, t, name, dtype, shape, optional=False):
         """As req, but the first dimension may have any stride of whole 16-byte
@@ -54,16 +69,18 @@ class _RowArgs(_Args):
         if stride < one or stride % per:
             raise ValueError(f"{self.where}: {name} must have rows of whole 16-byte pieces "
                              f"(stride {stride} elements for rows of {one})")
-        self.tensors.append((name, t))
+        self.add(t, name)
         return stride
 
     def gpu(self):
-        """Index of the one GPU that every tensor checked so far is on."""
-        index = self.tensors[0][1].get_device()
-        for _, t in self.tensors:
-            if t.get_device() != index or index < 0:
-                self.device()
-        return index
+        """Index of the one GPU that every tensor is on."""
+        if self.index < 0:
+            self.device()
+        return self.index
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _width(a, t, name):
@@ -93,13 +110,16 @@ def _workspace(ws, nbytes, dev, index, stream):
     return buf
 
 
-def _launch(name, index, stream, call):
-    """call(stream handle) with the tensors' device current."""
+def _launch(name, index, stream, *args):
+    """The C function `name` with the tensors' device current; the stream comes last."""
+    call = getattr(A.library(), name)
     if index == torch.cuda.current_device():
-        st = call(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+        st = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None
+                  else A._s(stream))
     else:
         with torch.cuda.device(index):
-            st = call(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+            st = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None
+                      else A._s(stream))
     if st:
         _check(st, name)
 
@@ -145,13 +165,11 @@ def logprobs(X, tokens=None, *, k=0, row_offset=None, temp=1.0, ws=None, stream=
         for name in ("logp", "top_ids", "top_logp"):
             if name not in spec:
                 out.setdefault(name, None)
-        a.gpu()
         buf = _workspace(ws, _logprobs_ws(n, V, k, dt), dev, index, stream)
-    top = (out["top_ids"], out["top_logp"]) if k > 0 else (None, None)
-    _launch("dspark_logprobs", index, stream, lambda s: A.dspark_logprobs(
-        n, V, stride, dt, temp, X, tokens, w, R, row_offset, k,
-        out["logp"] if tokens is not None else None, out["entropy"], out["stats"], *top, buf,
-        buf.numel(), s))
+    top = (out["top_ids"].data_ptr(), out["top_logp"].data_ptr()) if k > 0 else (None, None)
+    _launch("dspark_logprobs", index, stream, n, V, stride, dt, temp, X.data_ptr(), _ptr(tokens), w,
+            R, _ptr(row_offset), k, out["logp"].data_ptr() if tokens is not None else None,
+            out["entropy"].data_ptr(), out["stats"].data_ptr(), *top, buf.data_ptr(), buf.numel())
     return out
 
 
@@ -187,12 +205,12 @@ def logprobs_backward(X, stats, entropy=None, *, tokens=None, g_logp=None, g_ent
             per = _PER[X.dtype]
             out = _empty((n, -(-V // per) * per), X.dtype, dev)[:, :V]
         dx_stride = a.rows(out, "out", X.dtype, (n, V))
-        a.gpu()
         buf = _workspace(ws, 256, dev, index, stream)
-    _launch("dspark_logprobs_backward", index, stream, lambda s: A.dspark_logprobs_backward(
-        n, V, stride, dt, temp, X, tokens if g_logp is not None else None, w, R, row_offset,
-        stats, entropy, g_logp, g_entropy, k, top_ids if k else None, g_top if k else None, out,
-        dx_stride, buf, buf.numel(), s))
+    _launch("dspark_logprobs_backward", index, stream, n, V, stride, dt, temp, X.data_ptr(),
+            None if g_logp is None else tokens.data_ptr(), w, R, _ptr(row_offset),
+            stats.data_ptr(), _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), k,
+            top_ids.data_ptr() if k else None, g_top.data_ptr() if k else None, out.data_ptr(),
+            dx_stride, buf.data_ptr(), buf.numel())
     return out
 
 
@@ -253,13 +271,12 @@ class _State:
             if extra is not None:
                 t = None if out is None else out.get(extra)
                 o[extra] = _empty((1,), I32, dev) if t is None else a.req(t, f"out[{extra!r}]", I32, (1,))
-                after = (*after, o[extra])
-            a.gpu()
+                after = (*after, o[extra].data_ptr())
             buf = _workspace(ws, _cache_ws(self.R, self.n_pages), dev, index, stream)
-        call = getattr(A, name)
-        _launch(name, index, stream, lambda s: call(
-            self.R, page, self.width, self.n_pages, *before, *self.ins, o["lens"], o["table"],
-            o["refs"], *after, buf, buf.numel(), s))
+        lens, table, refs = self.ins
+        _launch(name, index, stream, self.R, page, self.width, self.n_pages, *before,
+                lens.data_ptr(), table.data_ptr(), refs.data_ptr(), o["lens"].data_ptr(),
+                o["table"].data_ptr(), o["refs"].data_ptr(), *after, buf.data_ptr(), buf.numel())
         return o
 
 
@@ -272,7 +289,8 @@ def cache_fork(src, dst, lens, table, refs, *, page, ws=None, stream=None, out=N
     n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else None
     s = _State("cache_fork", lens, table, refs,
                lambda s: ((src, "src", (n,)), (dst, "dst", (n,))))
-    return s.run("dspark_cache_fork", page, ws, stream, out, (n, src, dst))
+    return s.run("dspark_cache_fork", page, ws, stream, out,
+                 (n, src.data_ptr(), dst.data_ptr()))
 
 
 def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=None,
@@ -283,8 +301,8 @@ def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=N
     s = _State("cache_reserve", lens, table, refs,
                lambda s: ((row_offset, "row_offset", (s.R + 1,)),))
     size = s.pools(k_pages, v_pages)
-    return s.run("dspark_cache_reserve", page, ws, stream, out, (row_offset,),
-                 (k_pages, v_pages, size), "missing")
+    return s.run("dspark_cache_reserve", page, ws, stream, out, (row_offset.data_ptr(),),
+                 (_ptr(k_pages), _ptr(v_pages), size), "missing")
 
 
 def cache_commit(row_offset, n_acc, lens, table, refs, *, page, ws=None, stream=None, out=None):
@@ -292,14 +310,15 @@ def cache_commit(row_offset, n_acc, lens, table, refs, *, page, ws=None, stream=
     n_acc + 1 stay.  Returns the state."""
     s = _State("cache_commit", lens, table, refs,
                lambda s: ((row_offset, "row_offset", (s.R + 1,)), (n_acc, "n_acc", (s.R,))))
-    return s.run("dspark_cache_commit", page, ws, stream, out, (row_offset, n_acc))
+    return s.run("dspark_cache_commit", page, ws, stream, out,
+                 (row_offset.data_ptr(), n_acc.data_ptr()))
 
 
 def cache_release(which, lens, table, refs, *, page, ws=None, stream=None, out=None):
     """Requests `which` leave and give their pages back.  Returns the state."""
     n = which.shape[0] if isinstance(which, torch.Tensor) and which.dim() == 1 else None
     s = _State("cache_release", lens, table, refs, lambda s: ((which, "which", (n,)),))
-    return s.run("dspark_cache_release", page, ws, stream, out, (n, which))
+    return s.run("dspark_cache_release", page, ws, stream, out, (n, which.data_ptr()))
 
 
 def cache_compact(lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=None, out=None):
@@ -307,8 +326,8 @@ def cache_compact(lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=
     n_live [1]."""
     s = _State("cache_compact", lens, table, refs, lambda s: ())
     size = s.pools(k_pages, v_pages)
-    return s.run("dspark_cache_compact", page, ws, stream, out, (), (k_pages, v_pages, size),
-                 "n_live")
+    return s.run("dspark_cache_compact", page, ws, stream, out, (),
+                 (_ptr(k_pages), _ptr(v_pages), size), "n_live")
 
 
 # ---------------------------------------------------------------- attention
@@ -347,14 +366,12 @@ def cache_attend(q, k_pages, v_pages, table, kv_len, *, row_offset=None, k_new=N
     index, dev = a.gpu(), q.device
     with _on_stream(stream):
         out = _outs(a, out, {"out": ((n, Hq, D), q.dtype), "lse": ((n, Hq), F32)}, dev)
-        a.gpu()
         buf = _workspace(ws, _attend_ws(R, n, Hq, Hkv, D, dt), dev, index, stream)
-    if scale is None:
-        scale = D ** -0.5
-    _launch("dspark_cache_attend", index, stream, lambda s: A.dspark_cache_attend(
-        R, n, Hq, Hkv, D, page, width, n_pages, dt, scale, window, q, q_stride, k_new, v_new, kn,
-        k_pages, v_pages, k_stride, v_stride, table, row_offset, kv_len, out["out"], out["lse"], buf,
-        buf.numel(), s))
+    _launch("dspark_cache_attend", index, stream, R, n, Hq, Hkv, D, page, width, n_pages, dt,
+            D ** -0.5 if scale is None else scale, window, q.data_ptr(), q_stride, _ptr(k_new),
+            _ptr(v_new), kn, k_pages.data_ptr(), v_pages.data_ptr(), k_stride, v_stride,
+            table.data_ptr(), _ptr(row_offset), kv_len.data_ptr(), out["out"].data_ptr(),
+            out["lse"].data_ptr(), buf.data_ptr(), buf.numel())
     return out
 
 

@@ -1,0 +1,189 @@
+"""The decode loop with a paged cache and log probabilities: an attention model
+whose logits come through PagedCache is compared, at every row of every round,
+with the same model over the whole history in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import draft_sampling_verification_03_amd as ds
+from draft_sampling_verification_03_amd import decode
+
+pytestmark = pytest.mark.gpu
+
+V, RANK, D, HQ, HKV, LAYERS = 64, 16, 64, 4, 2, 2
+I32 = torch.int32
+
+
+class Model:
+    """Two attention layers with residuals over token and position embeddings;
+    fp32 through the cache, and in 64 bits over a request's whole history."""
+
+    def __init__(self, seed, R, prompts):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+        self.emb, self.pos = r(V, D), 0.3 * r(400, D)
+        self.w = [(r(D, HQ * D) / 8, r(D, HKV * D) / 8, r(D, HKV * D) / 8, r(HQ * D, D) / 16)
+                  for _ in range(LAYERS)]
+        self.out = r(D, V) / 4
+        self.history = [list(p) for p in prompts]  # tokens in the cache, then this round's
+        self.rounds = 0
+        self.worst = 0.0
+
+    def layer(self, l, h, attend):
+        q, k, v, o = (w.to(h.dtype) for w in self.w[l])
+        n = h.shape[0]
+        a = attend((h @ q).view(n, HQ, D), (h @ k).view(n, HKV, D), (h @ v).view(n, HKV, D))
+        return h + a.reshape(n, HQ * D) @ o
+
+    def whole(self, tokens):
+        """Logits after every token of one history."""
+        t = torch.tensor(tokens, device="cuda")
+        h = (self.emb[t] + self.pos[: len(tokens)]).double()
+        mask = torch.ones(len(tokens), len(tokens), device="cuda").triu(1).bool()
+
+        def attend(q, k, v):
+            k, v = (x.repeat_interleave(HQ // HKV, 1) for x in (k, v))
+            s = torch.einsum("ihd,jhd->hij", q, k) * D ** -0.5
+            return torch.einsum("hij,jhd->ihd", torch.softmax(s.masked_fill(mask, -1e300), 2), v)
+
+        for l in range(LAYERS):
+            h = self.layer(l, h, attend)
+        return h @ self.out.double()
+
+    def rows(self, prev, cache):
+        """target_rows of the decode loop."""
+        off, lens = cache.row_offset.tolist(), cache.lens.tolist()
+        prev = torch.as_tensor(np.asarray(prev)).cuda()
+        at = torch.cat([torch.arange(lens[r] - off[r + 1] + off[r], lens[r])
+                        for r in range(len(lens))]).cuda()
+        h = self.emb[prev] + self.pos[at]
+        for l in range(LAYERS):
+            h = self.layer(l, h, lambda q, k, v, l=l: cache.attend(l, q, k, v)["out"])
+        P = (h @ self.out).contiguous()
+        for r in range(len(lens)):
+            n = off[r + 1] - off[r]
+            if n == 0:
+                continue
+            # what the loop rejected is gone from the cache, and from the history
+            self.history[r] = self.history[r][: lens[r] - n] + prev[off[r]:off[r + 1]].tolist()
+            want = self.whole(self.history[r])[-n:]
+            self.worst = max(self.worst, (P[off[r]:off[r + 1]].double() - want).abs().max().item())
+        self.rounds += 1
+        return P
+
+
+def offsets(rows):
+    return torch.tensor([0, *np.cumsum(rows).tolist()], dtype=I32, device="cuda")
+
+
+def head(seed, R, gamma):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    W1, W2 = (0.3 * torch.randn((V, RANK), generator=g, device="cuda") for _ in range(2))
+    return W1, W2, lambda t: torch.randn((R, gamma, V), device="cuda",
+                                         generator=torch.Generator(device="cuda").manual_seed(100 + t))
+
+
+def prefill(model, cache, prompts):
+    """Prompts enter at once; the last token of each is the first anchor."""
+    keep = [p[:-1] for p in prompts]
+    cache.reserve(offsets([len(p) for p in keep]))
+    model.history = [[] for _ in prompts]
+    model.rows(np.concatenate(keep), cache)
+    cache.commit(torch.tensor([len(p) - 1 for p in keep], dtype=I32, device="cuda"))
+    return np.array([p[-1] for p in prompts], np.int32)
+
+
+@pytest.mark.parametrize("logprobs", [0, 3])
+def test_decode_with_cache_and_logprobs(logprobs):
+    R, gamma = 5, 4
+    rng = np.random.default_rng(3)
+    prompts = [rng.integers(0, V, n).tolist() for n in (2, 17, 33, 5, 48)]
+    cache = ds.PagedCache(R, 60, Hkv=HKV, D=D, layers=LAYERS, page=16, dtype=torch.float32)
+    cache.k.fill_(float("nan"))
+    cache.v.fill_(float("nan"))
+    model = Model(1, R, prompts)
+    x0 = prefill(model, cache, prompts)
+    W1, W2, U = head(2, R, gamma)
+    rows = {}
+
+    def target_rows(prev, c):
+        P = model.rows(prev, c)
+        rows[len(rows)] = P
+        return P
+
+    res = decode.decode(8, x0, W1, W2, U, target_rows, cache=cache, logprobs=logprobs, temp=0.9)
+    assert res["device_errors"] == (0,) * 5
+    # fp32 layers of unit scale against 64 bits: D-term sums, two layers, 1e-5 is far above
+    # their 2^-24 * 64 * 2 and far below what a wrong or stale key would do
+    assert model.worst < 1e-4, model.worst
+    assert res["n_acc"].min() < gamma  # something was rejected
+    for r in range(R):
+        seen = prompts[r] + res["streams"][r]
+        # the cache holds every token but the last emitted one
+        n = int(cache.lens[r])
+        assert n == len(seen) - 1
+        assert model.history[r][:n] == seen[:n]
+    for i, P in rows.items():
+        lp = torch.log_softmax(P.double() / 0.9, 1).cpu().numpy()
+        at = 0
+        for r in range(R):
+            m = res["n_acc"][i][r] + 1
+            y = res["y"][i][r, :m]
+            got = lp[at + np.arange(m), y]
+            assert np.allclose(res["logp"][i][r, :m], got, atol=2e-5)
+            assert np.isnan(res["logp"][i][r, m:]).all() and np.isnan(res["entropy"][i][r, m:]).all()
+            p = np.exp(lp[at:at + m])
+            assert np.allclose(res["entropy"][i][r, :m], -(p * lp[at:at + m]).sum(1), atol=2e-4)
+            if logprobs:
+                order = np.argsort(-P[at:at + m].cpu().numpy(), axis=1, kind="stable")[:, :logprobs]
+                assert (res["top_ids"][i][r, :m] == order).all()
+                assert np.allclose(res["top_logp"][i][r, :m],
+                                   np.take_along_axis(lp[at:at + m], order, 1), atol=2e-5)
+            at += res["ell"][i][r] + 1
+    assert ("top_ids" in res) == (logprobs > 0)
+
+
+def test_decode_of_forked_requests_after_compaction():
+    """A prompt is forked, its branches go their own ways, one leaves, the cache is
+    compacted and the rest goes on."""
+    R, gamma = 4, 3
+    rng = np.random.default_rng(5)
+    prompts = [rng.integers(0, V, 21).tolist(), rng.integers(0, V, 9).tolist()]
+    cache = ds.PagedCache(R, 40, Hkv=HKV, D=D, layers=LAYERS, page=16, dtype=torch.float32)
+    cache.v.fill_(float("inf"))
+    model = Model(4, R, prompts)
+    model.history = [[] for _ in range(R)]
+    cache.reserve(offsets([20, 8, 0, 0]))
+    model.rows(np.concatenate([p[:-1] for p in prompts]), cache)
+    cache.commit(torch.tensor([19, 7, -1, -1], dtype=I32, device="cuda"))
+    cache.fork(torch.tensor([0, 0], dtype=I32, device="cuda"), torch.tensor([2, 3], dtype=I32, device="cuda"))
+    model.history[2], model.history[3] = list(model.history[0]), list(model.history[0])
+    x0 = np.array([prompts[0][-1], prompts[1][-1], prompts[0][-1], prompts[0][-1]], np.int32)
+    W1, W2, U = head(6, R, gamma)
+    a = decode.decode(5, x0, W1, W2, U, model.rows, cache=cache)
+    assert model.worst < 1e-4
+    streams = [list(s) for s in a["streams"]]
+    assert streams[0] != streams[2] or streams[2] != streams[3]  # drawn apart
+    # request 1 leaves, its place is taken by another branch of request 2
+    cache.release(torch.tensor([1], dtype=I32, device="cuda"))
+    cache.fork(torch.tensor([2], dtype=I32, device="cuda"), torch.tensor([1], dtype=I32, device="cuda"))
+    live = int(cache.compact())
+    assert live == int((cache.refs > 0).sum()) and int((cache.refs[live:] != 0).sum()) == 0
+    model.history[1] = list(model.history[2])
+    anchors = a["y"][-1][np.arange(R), a["n_acc"][-1]]
+    anchors[1] = anchors[2]
+    b = decode.decode(5, anchors, W1, W2, U, model.rows, cache=cache, first_round=5)
+    assert model.worst < 1e-4 and b["device_errors"] == (0,) * 4
+    for r in (0, 2, 3):
+        seen = prompts[0] + streams[r] + b["streams"][r]
+        assert int(cache.lens[r]) == len(seen) - 1 and model.history[r][: len(seen) - 1] == seen[:-1]
+
+
+def test_decode_stops_when_pages_run_out():
+    R, gamma = 2, 4
+    cache = ds.PagedCache(R, 2, Hkv=HKV, D=D, layers=LAYERS, page=16, dtype=torch.float32)
+    model = Model(7, R, [[], []])
+    W1, W2, U = head(8, R, gamma)
+    with pytest.raises(RuntimeError, match="more pages than the cache has free"):
+        decode.decode(40, np.array([1, 2], np.int32), W1, W2, U, model.rows, cache=cache)
+    assert cache.error_code() & 64
