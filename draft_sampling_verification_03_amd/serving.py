@@ -40,9 +40,15 @@ class _RowArgs(_Args):
             self.index = index
         return t
 
+    def right(self, t, dtype, shape):
+        """Whether t is such a contiguous tensor on the GPU of the others."""
+        return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous() and t.get_device() == self.index)
+
     def req(self, t, name, dtype, shape, optional=False):
-        if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            return self.add(t, name)
+        if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous() and t.get_device() == self.index):
+            return t
         if super().req(t, name, dtype, shape, optional) is not None:
             self.tensors.pop()
             self.add(t, name)
@@ -55,21 +61,17 @@ class _RowArgs(_Args):
             return 0
         if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape:
             self.req(t, name, dtype, shape)
-        per = _PER[dtype]
-        one = 1
-        for n in shape[1:]:
-            one *= n
-        if shape[0] > 1:
-            stride = t.stride(0)
-            inner = t.is_contiguous() or t[0].is_contiguous()
-        else:
-            stride, inner = -(-one // per) * per, t.is_contiguous()
-        if not inner:
-            raise ValueError(f"{self.where}: {name} must be contiguous past its first dimension")
+        per, one, strides = _PER[dtype], 1, t.stride()
+        for i in range(len(shape) - 1, 0, -1):
+            if strides[i] != one and shape[i] != 1:
+                raise ValueError(f"{self.where}: {name} must be contiguous past its first dimension")
+            one *= shape[i]
+        stride = strides[0] if shape[0] > 1 else -(-one // per) * per
         if stride < one or stride % per:
             raise ValueError(f"{self.where}: {name} must have rows of whole 16-byte pieces "
                              f"(stride {stride} elements for rows of {one})")
-        self.add(t, name)
+        if t.get_device() != self.index:
+            self.add(t, name)
         return stride
 
     def gpu(self):
@@ -96,7 +98,8 @@ def _outs(a, out, spec, dev):
     if out is None:
         return {n: _empty(s, t, dev) for n, (s, t) in spec.items()}
     for n, (s, t) in spec.items():
-        a.req(out.get(n), f"out[{n!r}]", t, s)
+        if not a.right(out.get(n), t, s):
+            a.req(out.get(n), f"out[{n!r}]", t, s)
     return out
 
 
@@ -223,6 +226,7 @@ class _State:
         self.a = a = _RowArgs(where)
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError(f"{where}: table must be a [R][max_pages] tensor")
+        a.add(table, "table")
         self.R, self.width = table.shape
         self.n_pages = _width(a, refs, "refs")
         self.ins = (lens, table, refs)
@@ -263,14 +267,19 @@ class _State:
                     if o[n] is t:
                         same += 1
                     else:
-                        a.req(o[n], f"out[{n!r}]", I32, shape)
+                        if not a.right(o[n], I32, shape):
+                            a.req(o[n], f"out[{n!r}]", I32, shape)
                         same += o[n].data_ptr() == t.data_ptr()
                 if same not in (0, 3):
                     raise ValueError(f"{a.where}: lens, table and refs change in place all three or "
                                      "none")
             if extra is not None:
                 t = None if out is None else out.get(extra)
-                o[extra] = _empty((1,), I32, dev) if t is None else a.req(t, f"out[{extra!r}]", I32, (1,))
+                if t is None:
+                    t = _empty((1,), I32, dev)
+                elif not a.right(t, I32, (1,)):
+                    a.req(t, f"out[{extra!r}]", I32, (1,))
+                o[extra] = t
                 after = (*after, o[extra].data_ptr())
             buf = _workspace(ws, _cache_ws(self.R, self.n_pages), dev, index, stream)
         lens, table, refs = self.ins
