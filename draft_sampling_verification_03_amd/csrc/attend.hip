@@ -42,6 +42,7 @@ constexpr int kWaves = kBlock / kWave;
 constexpr int kShares = 2 * kComputeUnits;  // over all key-value heads: two workgroups a unit
 constexpr int kCut = 128;         // a unit is cut at multiples of this many tokens
 constexpr int kFixed = 64;        // a unit's fixed cost, in tokens
+constexpr int kJoiners = 32;      // workgroups that join a request's rows, at most
 constexpr int kWindow = 1024;     // page numbers of a stretch that wait in LDS at a time
 constexpr float kNone = -1e30f;   // running maximum of a row that has seen nothing
 constexpr float kSlack = 8.0f;    // see rescale below
@@ -814,13 +815,15 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
   }
 }
 
-// The parts of one (new token, query head) of a unit that was cut: one wave where
-// they are few, the workgroup's four together where they may be many.  A part takes D / 4 lanes, so a wave reads 256 / D of them (two for D = 96) at a time.
+// The parts of the rows of units that were cut.  A row's part takes D / 4 lanes, so a
+// wave has 256 / D sides (two for D = 96), each with up to four parts in flight.
+// Where a row has few parts every side takes a row of its own; where it may have
+// many, the workgroup's sides share one and are joined at the end.
 template <typename T, int D>
 __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
-  constexpr int kLanes = D / 4, kSide = kWave / kLanes;
-  __shared__ float lds_x[kWaves][D];
-  __shared__ float lds_sum[kWaves];
+  constexpr int kLanes = D / 4, kSide = kWave / kLanes, kSides = kWaves * kSide;
+  __shared__ float lds_x[kSides][D];
+  __shared__ float2 lds_ml[kSides];
   const AttendLaunch &L = p.L;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int r = blockIdx.x;
@@ -830,14 +833,15 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
   const int64_t share = p.head[0], at0 = p.before[r];
   if (u.blocks == 0 || at0 / share == (at0 + (int64_t)u.blocks * u.size - 1) / share) return;
   const int group = p.heads_per_group;
-  // a unit has at most so many parts
-  const int most = (int)(u.size / share) + 2;
-  const int together = most > 8 ? kWaves : 1, at_once = kWaves / together;  // waves a row, rows
-  const int part = wave % together, side = lane / kLanes, d = lane % kLanes * 4;
+  const bool many = u.size / share + 2 > 8;  // parts of a unit, at most
+  const int at_once = many ? 1 : kSides;     // rows
+  const bool idle = lane / kLanes >= kSide;  // the last 16 lanes for D = 96
+  const int side = wave * kSide + (idle ? 0 : lane / kLanes), d = lane % kLanes * 4;
+  const int first = many ? side : 0, stride = many ? kSides : 1;
   int unit = -1, s0 = 0, splits = 0;
   for (int i0 = blockIdx.y * at_once; i0 < s.n * L.Hq; i0 += gridDim.y * at_once) {
-    const int i = i0 + wave / together;
-    const bool there = i < s.n * L.Hq;
+    const int i = i0 + (many ? 0 : side);
+    const bool there = i < s.n * L.Hq && !idle;
     const int j = there ? i / L.Hq : 0, h = there ? i % L.Hq : 0, hk = h / group;
     const int row = j * group + h % group, b = row / p.block_rows;
     if (b != unit) {  // most rows follow one of the same unit
@@ -849,51 +853,57 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
     // part k: what share s0 + k left, the first of them as its last
     const int64_t slot_size = (int64_t)L.Hkv * p.block_rows;
     const int64_t base = (int64_t)hk * p.block_rows + row % p.block_rows;
-    auto part_at = [&](int k) __attribute__((always_inline)) {
-      return base + (2 * (int64_t)(s0 + k) + (k == 0)) * slot_size;
-    };
-    float mx = kNone;
-    for (int k = lane; k < splits; k += kWave) mx = fmaxf(mx, p.part_ml[part_at(k)].x);
-    mx = wave_max(mx);
-    float all = 0.0f, x[4] = {0, 0, 0, 0};
-    if (side < kSide) {
-#pragma unroll 4
-      for (int k = part * kSide + side; k < splits; k += together * kSide) {
-        const float2 ml = p.part_ml[part_at(k)];
-        const floatx4 y = *reinterpret_cast<const floatx4 *>(p.part_o + part_at(k) * D + d);
-        const float f = exp2_fast(ml.x - mx);
-        all += f * ml.y;
+    float m = kNone, all = 0.0f, x[4] = {0, 0, 0, 0};
+    for (int k0 = first; k0 < splits && there && splits > 1; k0 += 4 * stride) {
+      float2 ml[4];
+      floatx4 y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] += f * y[e];
+      for (int v = 0; v < 4; ++v) {
+        const int k = min(k0 + v * stride, splits - 1);
+        const int64_t at = base + (2 * (int64_t)(s0 + k) + (k == 0)) * slot_size;
+        ml[v] = p.part_ml[at];
+        y[v] = *reinterpret_cast<const floatx4 *>(p.part_o + at * D + d);
+      }
+      float now = m;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) now = fmaxf(now, ml[v].x);  // a part twice does no harm here
+      const float old = exp2_fast(m - now);
+      m = now;
+      all *= old;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= old;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (k0 + v * stride < splits) {
+          const float f = exp2_fast(ml[v].x - m);
+          all += f * ml[v].y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] += f * y[v][e];
+        }
       }
     }
-    // over the sides of the wave, in order
-    float sum = 0.0f, y[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int v = 0; v < kSide; ++v) {
-      const int from = v * kLanes + lane % kLanes;
-      sum += __shfl(all, from);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] += __shfl(x[e], from);
-    }
-    if (together > 1) {
+    if (many) {  // uniform
       __syncthreads();
-      if (lane < kLanes) store4(&lds_x[wave][d], y);
-      if (lane == 0) lds_sum[wave] = sum;
+      if (!idle) store4(&lds_x[side][d], x);
+      if (!idle && d == 0) lds_ml[side] = make_float2(m, all);
       __syncthreads();
-      sum = 0.0f;
+      m = kNone;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = 0.0f;
+      for (int v = 0; v < kSides; ++v) m = fmaxf(m, lds_ml[v].x);
+      all = 0.0f;
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) {
-        sum += lds_sum[v];
+      for (int e = 0; e < 4; ++e) x[e] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += lds_x[v][d + e];
+      for (int v = 0; v < kSides; ++v) {
+        const float f = exp2_fast(lds_ml[v].x - m);
+        all += f * lds_ml[v].y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += f * lds_x[v][d + e];
       }
     }
-    if (there && splits > 1 && part == 0 && lane < kLanes) {
+    if (there && splits > 1 && (!many || side == 0)) {
       const int rr = row % p.block_rows;
-      write_row<T>(p, s, hk, -1, row - rr, rr, d, mx, sum, y);
+      write_row<T>(p, s, hk, -1, row - rr, rr, d, m, all, x);
     }
   }
 }
@@ -950,7 +960,12 @@ template <typename T> hipError_t launch_attend_t(const AttendLaunch &L, hipStrea
   DSPARK_LAUNCH("attend_prepare", stream, attend_prepare_kernel<T>, 1 + L.R * appenders, kBlock, p);
   const int grid = z.shares * L.Hkv;
   const int64_t heads = mean * L.Hq;
-  const dim3 join(L.R, (unsigned)(heads < 64 ? heads : 64));
+  // joiners of a request: its rows by the sides of a workgroup, but where requests are
+  // few (and may be in many parts) a workgroup a row
+  const int64_t spread = (kComputeUnits + L.R - 1) / L.R, sides = kWaves * (256 / L.D);
+  int64_t gy = (heads + sides - 1) / sides;
+  if (gy < spread) gy = heads < spread ? heads : spread;
+  const dim3 join(L.R, (unsigned)(gy < kJoiners ? gy : kJoiners));
   switch (L.D) {
     case 64: launch_product<T, 64>(p, grid, join, stream); break;
     case 96: launch_product<T, 96>(p, grid, join, stream); break;
