@@ -43,6 +43,7 @@ constexpr int kShares = 2 * kComputeUnits;  // over all key-value heads: two wor
 constexpr int kCut = 128;         // a unit is cut at multiples of this many tokens
 constexpr int kFixed = 64;        // a unit's fixed cost, in tokens
 constexpr int kJoiners = 32;      // workgroups that join a request's rows, at most
+constexpr int kAppend = 8;        // rows whose values a workgroup writes at a time
 constexpr int kWindow = 1024;     // page numbers of a stretch that wait in LDS at a time
 constexpr float kNone = -1e30f;   // running maximum of a row that has seen nothing
 constexpr float kSlack = 8.0f;    // see rescale below
@@ -172,7 +173,9 @@ __device__ __forceinline__ void lay_out(const AttendParams &p) {
   if (bits) flag_error(L.err, bits);
 }
 
-// Workgroups from 1 on: request (b - 1) % R, every n-th of its rows.
+// Workgroups from 1 on: a quarter of the elements of up to kAppend rows of request
+// (b - 1) % R at a time.  Values lie along the tokens, so neighbouring lanes take
+// neighbouring rows: a store reaches 8 pieces of a page and not 64.
 template <typename T>
 __global__ __launch_bounds__(kBlock) void attend_prepare_kernel(AttendParams p) {
   if (blockIdx.x == 0) {
@@ -182,35 +185,48 @@ __global__ __launch_bounds__(kBlock) void attend_prepare_kernel(AttendParams p) 
   const AttendLaunch &L = p.L;
   constexpr int kPer = Elem<T>::kPerVec;
   int bits = 0;
-  const int b = blockIdx.x - 1, r = b % L.R, part = b / L.R, parts = (gridDim.x - 1) / L.R;
+  const int b = blockIdx.x - 1, r = b % L.R, part = b / L.R / 4, parts = (gridDim.x - 1) / L.R / 4;
   const Slice s = slice_of(L, r, &bits);
   const int page_mask = (1 << L.page_shift) - 1;
-  const int pieces = L.Hkv * L.D / kPer;
+  const int elems = L.Hkv * L.D / 4, e0 = b / L.R % 4 * elems;  // a multiple of 16
   bits = 0;  // the layout reports the slices
-  for (int j = part; j < s.n; j += parts) {
+  // the page of row j, null where it is not to be written
+  auto page_of = [&](int j, void *pages, int64_t stride) __attribute__((always_inline)) {
     const int t = s.len - s.n + j;
-    if (t < 0) {
-      bits |= kErrLength;
-      continue;
+    const int id = t < 0 ? -1 : L.table[(int64_t)r * L.max_pages + (t >> L.page_shift)];
+    if (t < 0) bits |= kErrLength;
+    else if ((unsigned)id >= (unsigned)L.n_pages) bits |= kErrPage;
+    return (unsigned)id < (unsigned)L.n_pages ? reinterpret_cast<T *>(pages) + (int64_t)id * stride
+                                              : (T *)nullptr;
+  };
+  for (int j0 = part * kAppend; j0 < s.n; j0 += parts * kAppend) {
+    const int rows = min(kAppend, s.n - j0);
+    // keys: rows of D elements
+    const int pieces = elems / kPer;
+    for (int i = threadIdx.x; i < rows * pieces; i += kBlock) {
+      const int j = j0 + i / pieces, e = e0 + i % pieces * kPer, h = e / L.D;
+      T *page = page_of(j, L.k_pages, L.k_page_stride);
+      if (page == nullptr) continue;
+      const int slot = (s.len - s.n + j) & page_mask;
+      const T *from = reinterpret_cast<const T *>(L.k_new) + (int64_t)(s.row0 + j) * L.kv_stride + e;
+      *reinterpret_cast<u32x4 *>(page + (((int64_t)h << L.page_shift) + slot) * L.D + e - h * L.D) =
+          *reinterpret_cast<const u32x4 *>(from);
     }
-    const int id = L.table[(int64_t)r * L.max_pages + (t >> L.page_shift)], slot = t & page_mask;
-    if ((unsigned)id >= (unsigned)L.n_pages) {
-      bits |= kErrPage;
-      continue;
+    // values: `lanes` neighbours take as many rows
+    const int shift = rows > 4 ? 3 : rows > 2 ? 2 : rows > 1 ? 1 : 0;
+    const int mine = threadIdx.x & ((1 << shift) - 1);
+    if (mine < rows) {
+      const int j = j0 + mine, slot = (s.len - s.n + j) & page_mask;
+      T *page = page_of(j, L.v_pages, L.v_page_stride);
+      const T *from = reinterpret_cast<const T *>(L.v_new) + (int64_t)(s.row0 + j) * L.kv_stride;
+      if (page != nullptr) {
+#pragma unroll 8
+        for (int e = e0 + (threadIdx.x >> shift); e < e0 + elems; e += kBlock >> shift)
+          page[((int64_t)e << L.page_shift) + slot] = from[e];
+      }
     }
-    const T *kn = reinterpret_cast<const T *>(L.k_new) + (int64_t)(s.row0 + j) * L.kv_stride;
-    const T *vn = reinterpret_cast<const T *>(L.v_new) + (int64_t)(s.row0 + j) * L.kv_stride;
-    T *kp = reinterpret_cast<T *>(L.k_pages) + (int64_t)id * L.k_page_stride;
-    T *vp = reinterpret_cast<T *>(L.v_pages) + (int64_t)id * L.v_page_stride;
-    for (int i = threadIdx.x; i < pieces; i += kBlock) {
-      const int h = i * kPer / L.D, d = i * kPer - h * L.D;
-      const u32x4 k = *reinterpret_cast<const u32x4 *>(kn + i * kPer);
-      *reinterpret_cast<u32x4 *>(kp + (((int64_t)h << L.page_shift) + slot) * L.D + d) = k;
-    }
-    for (int i = threadIdx.x; i < L.Hkv * L.D; i += kBlock)
-      vp[((int64_t)i << L.page_shift) + slot] = vn[i];
   }
-  if (bits && threadIdx.x == 0) flag_error(L.err, bits);
+  if (bits) flag_error(L.err, bits);
 }
 
 namespace {
@@ -954,9 +970,9 @@ template <typename T> hipError_t launch_attend_t(const AttendLaunch &L, hipStrea
   p.first = (int32_t *)take((size_t)z.shares * 4);
   p.part_ml = (float2 *)take(parts * 8);
   p.part_o = (float *)take(parts * L.D * 4);
-  // a workgroup for every row of a request or so
-  const int64_t mean = (L.rows_capacity + L.R - 1) / L.R;
-  const int appenders = L.k_new == nullptr ? 0 : (int)(mean < 64 ? mean : 64);
+  // four workgroups for every kAppend rows of the mean request
+  const int64_t mean = (L.rows_capacity + L.R - 1) / L.R, sets = (mean + kAppend - 1) / kAppend;
+  const int appenders = L.k_new == nullptr ? 0 : 4 * (int)(sets < 64 ? sets : 64);
   DSPARK_LAUNCH("attend_prepare", stream, attend_prepare_kernel<T>, 1 + L.R * appenders, kBlock, p);
   const int grid = z.shares * L.Hkv;
   const int64_t heads = mean * L.Hq;
