@@ -424,7 +424,7 @@ static int shift_of(int page) {
 static bool bad_cache_shape(int R, int page, int max_pages, int n_pages) {
   return R < 1 || R > 8192 || page < 16 || page > 256 || (page & (page - 1)) != 0 || n_pages < 1 ||
          n_pages > (1 << 22) || max_pages < 1 || (int64_t)R * max_pages > (1 << 28) ||
-         (int64_t)page * max_pages > INT32_MAX;
+         (int64_t)page * max_pages > (1 << 30);
 }
 
 // The shape, the state's arrays and the workspace of a page operation.
@@ -579,7 +579,8 @@ dspark_status dspark_cache_attend(int R, int rows_capacity, int Hq, int Hkv, int
   L.err = (int32_t *)carve(ws, &off, kWsHeader);
   L.scratch = (char *)ws + off;
   L.R = R; L.rows_capacity = rows_capacity; L.Hq = Hq; L.Hkv = Hkv; L.D = D;
-  L.page_shift = shift_of(page); L.max_pages = max_pages; L.n_pages = n_pages; L.window = window;
+  L.page_shift = shift_of(page); L.max_pages = max_pages; L.n_pages = n_pages;
+  L.window = window > (1 << 30) ? 0 : window;  // wider than any request: none
   L.bf16 = dt == DSPARK_BF16; L.scale = scale; L.q = q; L.k_new = k_new; L.v_new = v_new;
   L.q_stride = q_stride; L.kv_stride = kv_stride; L.k_page_stride = k_page_stride;
   L.v_page_stride = v_page_stride; L.k_pages = k_pages; L.v_pages = v_pages; L.table = table;

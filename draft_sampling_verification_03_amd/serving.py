@@ -222,19 +222,19 @@ class _State:
     """The state of a page operation, checked, with its outputs and workspace:
     in place when `out` names the inputs, else new or the caller's arrays."""
 
-    def __init__(self, where, lens, table, refs, others):
+    __slots__ = ("a", "R", "width", "n_pages", "lens", "table", "refs")
+
+    def __init__(self, where, lens, table, refs):
         self.a = a = _RowArgs(where)
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError(f"{where}: table must be a [R][max_pages] tensor")
         a.add(table, "table")
-        self.R, self.width = table.shape
-        self.n_pages = _width(a, refs, "refs")
-        self.ins = (lens, table, refs)
-        self.shapes = ((self.R,), (self.R, self.width), (self.n_pages,))
-        for t, name, shape in zip(self.ins, _NAMES, self.shapes):
-            a.req(t, name, I32, shape)
-        for t, name, shape in others(self):
-            a.req(t, name, I32, shape)
+        self.R, self.width = R, width = table.shape
+        self.n_pages = n = _width(a, refs, "refs")
+        self.lens, self.table, self.refs = lens, table, refs
+        a.req(table, "table", I32, (R, width))
+        a.req(lens, "lens", I32, (R,))
+        a.req(refs, "refs", I32, (n,))
 
     def pools(self, k_pages, v_pages):
         """Bytes of a page in each pool (None both: numbers only)."""
@@ -251,55 +251,47 @@ class _State:
             raise ValueError(f"{self.a.where}: k_pages and v_pages must have pages of the same size")
         return size[0]
 
+    def outputs(self, out, dev):
+        if out is None:
+            return {"lens": _empty((self.R,), I32, dev), "refs": _empty((self.n_pages,), I32, dev),
+                    "table": _empty((self.R, self.width), I32, dev)}
+        lens, table, refs = out.get("lens"), out.get("table"), out.get("refs")
+        if lens is not self.lens or table is not self.table or refs is not self.refs:
+            a = self.a
+            a.req(lens, "out['lens']", I32, (self.R,))
+            a.req(table, "out['table']", I32, (self.R, self.width))
+            a.req(refs, "out['refs']", I32, (self.n_pages,))
+            if 0 < ((lens.data_ptr() == self.lens.data_ptr()) + (table.data_ptr() == self.table.data_ptr())
+                    + (refs.data_ptr() == self.refs.data_ptr())) < 3:
+                raise ValueError(f"{a.where}: lens, table and refs change in place all three or none")
+        return {"lens": lens, "table": table, "refs": refs}
+
     def run(self, name, page, ws, stream, out, before, after=(), extra=None):
         """Calls dspark_<name>; `extra` is the one-element output beside the state."""
-        a = self.a
-        index, dev = a.gpu(), self.ins[1].device
+        a, dev = self.a, self.table.device
+        index = a.gpu()
         with _on_stream(stream):
-            o = {}
-            if out is None:
-                for n, shape in zip(_NAMES, self.shapes):
-                    o[n] = _empty(shape, I32, dev)
-            else:
-                same = 0
-                for n, t, shape in zip(_NAMES, self.ins, self.shapes):
-                    o[n] = out.get(n)
-                    if o[n] is t:
-                        same += 1
-                    else:
-                        if not a.right(o[n], I32, shape):
-                            a.req(o[n], f"out[{n!r}]", I32, shape)
-                        same += o[n].data_ptr() == t.data_ptr()
-                if same not in (0, 3):
-                    raise ValueError(f"{a.where}: lens, table and refs change in place all three or "
-                                     "none")
+            o = self.outputs(out, dev)
             if extra is not None:
                 t = None if out is None else out.get(extra)
-                if t is None:
-                    t = _empty((1,), I32, dev)
-                elif not a.right(t, I32, (1,)):
-                    a.req(t, f"out[{extra!r}]", I32, (1,))
-                o[extra] = t
+                o[extra] = _empty((1,), I32, dev) if t is None else a.req(t, extra, I32, (1,))
                 after = (*after, o[extra].data_ptr())
             buf = _workspace(ws, _cache_ws(self.R, self.n_pages), dev, index, stream)
-        lens, table, refs = self.ins
         _launch(name, index, stream, self.R, page, self.width, self.n_pages, *before,
-                lens.data_ptr(), table.data_ptr(), refs.data_ptr(), o["lens"].data_ptr(),
-                o["table"].data_ptr(), o["refs"].data_ptr(), *after, buf.data_ptr(), buf.numel())
+                self.lens.data_ptr(), self.table.data_ptr(), self.refs.data_ptr(),
+                o["lens"].data_ptr(), o["table"].data_ptr(), o["refs"].data_ptr(), *after,
+                buf.data_ptr(), buf.numel())
         return o
-
-
-_NAMES = ("lens", "table", "refs")
 
 
 def cache_fork(src, dst, lens, table, refs, *, page, ws=None, stream=None, out=None):
     """Requests dst[i] become copies of src[i] that share their pages.  Returns
     the state (lens, table, refs); `out` may name the inputs (in place)."""
-    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else None
-    s = _State("cache_fork", lens, table, refs,
-               lambda s: ((src, "src", (n,)), (dst, "dst", (n,))))
-    return s.run("dspark_cache_fork", page, ws, stream, out,
-                 (n, src.data_ptr(), dst.data_ptr()))
+    s = _State("cache_fork", lens, table, refs)
+    n = _width(s.a, src, "src")
+    s.a.req(src, "src", I32, (n,))
+    s.a.req(dst, "dst", I32, (n,))
+    return s.run("dspark_cache_fork", page, ws, stream, out, (n, src.data_ptr(), dst.data_ptr()))
 
 
 def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=None,
@@ -307,8 +299,8 @@ def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=N
     """Pages for row_offset[r + 1] - row_offset[r] new tokens of every request.
     k_pages, v_pages: the whole pools, [n_pages][...] (None both: the state
     alone).  Returns the state and missing [1] (0: done)."""
-    s = _State("cache_reserve", lens, table, refs,
-               lambda s: ((row_offset, "row_offset", (s.R + 1,)),))
+    s = _State("cache_reserve", lens, table, refs)
+    s.a.req(row_offset, "row_offset", I32, (s.R + 1,))
     size = s.pools(k_pages, v_pages)
     return s.run("dspark_cache_reserve", page, ws, stream, out, (row_offset.data_ptr(),),
                  (_ptr(k_pages), _ptr(v_pages), size), "missing")
@@ -317,23 +309,25 @@ def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=N
 def cache_commit(row_offset, n_acc, lens, table, refs, *, page, ws=None, stream=None, out=None):
     """After verify(): of the rows that cache_reserve made room for, the first
     n_acc + 1 stay.  Returns the state."""
-    s = _State("cache_commit", lens, table, refs,
-               lambda s: ((row_offset, "row_offset", (s.R + 1,)), (n_acc, "n_acc", (s.R,))))
+    s = _State("cache_commit", lens, table, refs)
+    s.a.req(row_offset, "row_offset", I32, (s.R + 1,))
+    s.a.req(n_acc, "n_acc", I32, (s.R,))
     return s.run("dspark_cache_commit", page, ws, stream, out,
                  (row_offset.data_ptr(), n_acc.data_ptr()))
 
 
 def cache_release(which, lens, table, refs, *, page, ws=None, stream=None, out=None):
     """Requests `which` leave and give their pages back.  Returns the state."""
-    n = which.shape[0] if isinstance(which, torch.Tensor) and which.dim() == 1 else None
-    s = _State("cache_release", lens, table, refs, lambda s: ((which, "which", (n,)),))
+    s = _State("cache_release", lens, table, refs)
+    n = _width(s.a, which, "which")
+    s.a.req(which, "which", I32, (n,))
     return s.run("dspark_cache_release", page, ws, stream, out, (n, which.data_ptr()))
 
 
 def cache_compact(lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=None, out=None):
     """Moves the pages in use to the front of the pools.  Returns the state and
     n_live [1]."""
-    s = _State("cache_compact", lens, table, refs, lambda s: ())
+    s = _State("cache_compact", lens, table, refs)
     size = s.pools(k_pages, v_pages)
     return s.run("dspark_cache_compact", page, ws, stream, out, (),
                  (_ptr(k_pages), _ptr(v_pages), size), "n_live")

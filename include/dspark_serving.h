@@ -49,7 +49,7 @@ extern "C" {
  * counts as an alternative (log probability -infinity) only behind every other.
  * Inputs
  *   X [n_rows][row_stride] logits (dt), V of each row used; row_stride >= V and
- *     a multiple of 16 bytes; 1 <= V <= 262144, any V
+ *     a multiple of 16 bytes; 1 <= V <= 262144, any V; 1 <= n_rows <= 4194304
  *   tokens  [n_rows] int32, or with row_offset [R][tok_stride]: row
  *     row_offset[rho] + j takes tokens[rho * tok_stride + j] (the layout of
  *     dspark_verify's y, tok_stride = gamma + 1).  -1, and a j past tok_stride:
@@ -111,7 +111,7 @@ dspark_status dspark_logprobs_backward(int n_rows, int V, int64_t row_stride, ds
  * The page operations read lens, table, refs and write lens_out, table_out,
  * refs_out: either all three the same arrays (in place) or three that overlap
  * none of them.  1 <= R <= 8192; 1 <= n_pages <= 4194304; 1 <= max_pages with
- * R * max_pages <= 2^28 and page * max_pages < 2^31.
+ * R * max_pages <= 2^28 and page * max_pages <= 2^30.
  * A page number outside [0, n_pages) within a request's length sets
  * DSPARK_DEVERR_PAGE; such an entry is never followed.  A length outside
  * [0, page * max_pages] sets DSPARK_DEVERR_LENGTH and is read as 0.
@@ -193,7 +193,8 @@ dspark_status dspark_cache_compact(int R, int page, int max_pages, int n_pages,
  *   dt BF16 or F32 for q, the new rows, the pages and out; statistics and sums
  *     are fp32 (BF16: the probabilities enter the product as a bf16 and a bf16
  *     remainder, 16 bits together)
- *   Hq a multiple of Hkv, Hq <= 1024; D one of 64, 96, 128, 256
+ *   Hq a multiple of Hkv, Hq <= 1024; D one of 64, 96, 128, 256;
+ *     1 <= rows_capacity <= 1048576
  *   q [rows_capacity][Hq][D], q_stride elements from row to row
  *   k_new, v_new [rows_capacity][Hkv][D], kv_stride elements from row to row:
  *     written into their slots of k_pages and v_pages first; or NULL both when

@@ -89,7 +89,7 @@ OPS = {
 @pytest.mark.parametrize("over,expect", [
     (dict(R=0), SHAPE), (dict(R=8193), SHAPE), (dict(page=8), SHAPE), (dict(page=24), SHAPE),
     (dict(page=512), SHAPE), (dict(max_pages=0), SHAPE), (dict(max_pages=(1 << 27)), SHAPE),
-    (dict(R=1, page=256, max_pages=1 << 23), SHAPE), (dict(n_pages=0), SHAPE),
+    (dict(R=1, page=256, max_pages=(1 << 22) + 1), SHAPE), (dict(n_pages=0), SHAPE),
     (dict(n_pages=(1 << 22) + 1), SHAPE), (dict(lens=None), NULL), (dict(table_out=None), NULL),
     (dict(ws=None), NULL), (dict(refs=P3 + 4), ALIGN), (dict(ws_bytes=300), WS),
     (dict(lens_out=P), VALUE), (dict(lens_out=P, table_out=P2), VALUE), (dict(refs_out=P3), VALUE),

@@ -139,7 +139,7 @@ def test_values(rows, lens, Hq, Hkv, D, page, dt):
     pools_equal(c)
 
 
-@pytest.mark.parametrize("dt,window", [(BF, 1), (BF, 40), (F, 7), (F, 200), (BF, 5000)])
+@pytest.mark.parametrize("dt,window", [(BF, 1), (BF, 40), (F, 7), (F, 200), (BF, 5000), (F, 2 ** 31 - 1)])
 def test_window(dt, window):
     c = Case([1, 17, 6], [500, 300, 33], 8, 2, 64, 16, dt, seed=window)
     c.check(c.run(window=window), window=window)
