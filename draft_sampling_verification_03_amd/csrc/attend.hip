@@ -505,6 +505,7 @@ template <typename T>
 __device__ __forceinline__ floatx4 product_mixed(const u32x4 &v, const typename Step<T>::P &pr,
                                                  const RowState &r, int t0, floatx4 o) {
   const int col = threadIdx.x & 15;
+#pragma nounroll
   for (int c = 0; c < 16; ++c) {
     const int from = __shfl(r.low, c) - t0, to = __shfl(r.high, c) - t0;
     const floatx4 a = Step<T>::product(Step<T>::keep(v, from, to), pr, o);
@@ -699,8 +700,9 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
   constexpr int kKeys = St::kKeys, kMine = St::kMine, kTiles = St::kTiles;
   constexpr int kOut = D / 16;
   constexpr int kPieces = D / 8, kFetch = kPieces / kWaves;  // of a step; of a wave
-  constexpr int kDeep = D <= 128 ? 4 : 2;
-  __shared__ u32x4 ring[2][kPieces][kWave];
+  constexpr int kDeep = D <= 128 ? 2 : 2;
+  constexpr int kGroup = D <= 128 ? 2 : 1;  // steps a barrier
+  __shared__ u32x4 ring[2][kGroup][kPieces][kWave];
   __shared__ int32_t ids[kWindow];
   const AttendLaunch &L = p.L;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -758,60 +760,67 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
     int buf = 0;
     for (int t1 = w0; t1 < w1; t1 += kDeep * kKeys) {
 #pragma unroll
-      for (int i = 0; i < kDeep; ++i) {
-        const int t = t1 + i * kKeys;
-        if (t >= w1) break;  // uniform
-        u32x4(*to)[kWave] = ring[buf];
+      for (int i0 = 0; i0 < kDeep; i0 += kGroup) {
+        if (t1 + i0 * kKeys >= w1) break;  // uniform
 #pragma unroll
-        for (int f = 0; f < kFetch; ++f) to[wave * kFetch + f][lane] = ahead[i][f];
-        if (t + kDeep * kKeys < w1) fetch(t + kDeep * kKeys, ahead[i]);
-        // the step's pieces are in LDS; the buffer written next was last read
+        for (int i = i0; i < i0 + kGroup; ++i) {
+          const int t = t1 + i * kKeys;
+          if (t < w1) {
+#pragma unroll
+            for (int f = 0; f < kFetch; ++f) ring[buf][i - i0][wave * kFetch + f][lane] = ahead[i][f];
+            if (t + kDeep * kKeys < w1) fetch(t + kDeep * kKeys, ahead[i]);
+          }
+        }
+        // the steps' pieces are in LDS; the buffer written next was last read
         // before this barrier
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        u32x4(*const here)[kPieces][kWave] = ring[buf];
         buf ^= 1;
-
         if (16 * wave >= rows) continue;  // no rows of this wave
-        const bool edge = any_bad || t + kKeys > least_high || t < most_low;  // uniform
-        // two straight paths, so that the reads from LDS and the products overlap
-        auto step = [&](auto at_edge) __attribute__((always_inline)) {
-          constexpr bool kEdge = decltype(at_edge)::value;
-          const int t0 = t + kMine * g;
+        // one copy of the step for all of them: the kernel has to stay in the
+        // instruction cache
+#pragma nounroll
+        for (int i = 0; i < kGroup; ++i) {
+          const int t = t1 + (i0 + i) * kKeys, t0 = t + kMine * g;
+          if (t >= w1) break;
+          u32x4(*const to)[kWave] = here[i];
+          const bool edge = any_bad || t + kKeys > least_high || t < most_low;  // uniform
           float s[kMine];
-          typename St::template K<D> k;
+          {
+            typename St::template K<D> k;
 #pragma unroll
-          for (int u = 0; u < kTiles; ++u)
+            for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-            for (int f = 0; f < kOut / kTiles; ++f) k.v[u][f] = to[u * (kOut / kTiles) + f][lane];
+              for (int f = 0; f < kOut / kTiles; ++f) k.v[u][f] = to[u * (kOut / kTiles) + f][lane];
 #pragma unroll
-          for (int u = 0; u < kTiles; ++u) {
-            const floatx4 a = St::template scores<D>(k, u, q);
+            for (int u = 0; u < kTiles; ++u) {
+              const floatx4 a = St::template scores<D>(k, u, q);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[4 * u + e] = a[e];
-          }
-          bool bad = false;
-          if (kEdge) {
-            if (any_bad) {
-              bad = ids[(min(t0, w1 - 1) >> L.page_shift) - first_page] < 0;
-              if (bad) bits |= kErrPage;
+              for (int e = 0; e < 4; ++e) s[4 * u + e] = a[e];
             }
+          }
+          int seen = kMine;  // this lane's tokens whose values count
+          if (edge) {
+            const bool bad = any_bad && ids[(min(t0, w1 - 1) >> L.page_shift) - first_page] < 0;
+            if (bad) bits |= kErrPage;
             mask_scores<kMine>(s, row, t0, bad);
+            seen = bad ? 0 : sl.len - t0;
           }
           const typename St::P pr = weigh<T, kOut>(s, to_log2, row, o);
+          if (!edge) {
 #pragma unroll
-          for (int d = 0; d < kOut; ++d) {
-            u32x4 v = to[kOut + d][lane];
-            bool mixed = false;
-            if (kEdge) {
-              v = St::keep(v, 0, bad ? 0 : sl.len - t0);
-              mixed = __ballot(St::not_finite(v)) != 0;
+            for (int d = 0; d < kOut; ++d) o[d] = St::product(to[kOut + d][lane], pr, o[d]);
+          } else {
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) {
+              const u32x4 v = St::keep(to[kOut + d][lane], 0, seen);
+              if (__ballot(St::not_finite(v)) == 0) o[d] = St::product(v, pr, o[d]);
+              else o[d] = product_mixed<T>(v, pr, row, t0, o[d]);
             }
-            o[d] = mixed ? product_mixed<T>(v, pr, row, t0, o[d]) : St::product(v, pr, o[d]);
           }
-        };
-        if (edge) step(Flag<true>{});
-        else step(Flag<false>{});
+        }
       }
     }
     }
