@@ -378,6 +378,12 @@ namespace {
 
 template <bool B> struct Flag { static constexpr bool value = B; };
 
+// Where the window of page numbers that begins with token w0 ends: at a page's end,
+// for w0 may lie inside one.
+__device__ __forceinline__ int window_end(const AttendLaunch &L, int w0, int end) {
+  return min(end, ((w0 >> L.page_shift) + kWindow) << L.page_shift);
+}
+
 // The page numbers of tokens [begin, end) to LDS (-1 where there is no such page);
 // returns whether one is missing.  From LDS, because loads come back in order: a
 // number read from memory would be waited for behind every key in flight.
@@ -582,8 +588,8 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(At
     const T *kbase = reinterpret_cast<const T *>(L.k_pages) + ((int64_t)hk << L.page_shift) * D;
     const T *vbase = reinterpret_cast<const T *>(L.v_pages) + ((int64_t)hk * D << L.page_shift);
     const int stride = kWaves * kKeys;
-    for (int w0 = begin; w0 < end; w0 += kWindow << L.page_shift) {
-      const int w1 = min(end, w0 + (kWindow << L.page_shift));
+    for (int w0 = begin, w1; w0 < end; w0 = w1) {
+      w1 = window_end(L, w0, end);
       const bool any_bad = stage_ids(L, table, w0, w1, ids);
       const int first_page = w0 >> L.page_shift;
       // loads of the step at token t; tokens past the last read the last page again
@@ -693,15 +699,15 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(At
 // 16 rows a wave.  A step's keys and values are D / 8 pieces of 64 x 16 bytes, each
 // an operand of the matrix cores in lane order: waves 0 and 1 fetch the keys', 2 and
 // 3 the values', kDeep steps ahead in registers, and pass them on through two buffers
-// in LDS.  In lane order every LDS access is 1 KB in a row; one barrier a step.
+// in LDS of kGroup steps each.  In lane order every LDS access is 1 KB in a row; one
+// barrier a buffer.
 template <typename T, int D, bool kPast>
 __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(AttendParams p) {
   using St = Step<T>;
   constexpr int kKeys = St::kKeys, kMine = St::kMine, kTiles = St::kTiles;
   constexpr int kOut = D / 16;
   constexpr int kPieces = D / 8, kFetch = kPieces / kWaves;  // of a step; of a wave
-  constexpr int kDeep = D <= 128 ? 2 : 2;
-  constexpr int kGroup = D <= 128 ? 2 : 1;  // steps a barrier
+  constexpr int kGroup = D <= 128 ? 2 : 1, kDeep = 2;
   __shared__ u32x4 ring[2][kGroup][kPieces][kWave];
   __shared__ int32_t ids[kWindow];
   const AttendLaunch &L = p.L;
@@ -742,87 +748,87 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
     const int64_t page_stride = keys ? L.k_page_stride : L.v_page_stride;
     const int piece_step = keys ? 4 * kMine : 16 << L.page_shift;  // elements from piece to piece
     const int slot_step = keys ? D : 1;
-    for (int w0 = begin; w0 < end; w0 += kWindow << L.page_shift) {
-    const int w1 = min(end, w0 + (kWindow << L.page_shift));
-    const bool any_bad = stage_ids(L, table, w0, w1, ids);
-    const int first_page = w0 >> L.page_shift;
-    // tokens past the last read the last page again
-    auto fetch = [&](int t, u32x4 (&x)[kFetch]) __attribute__((always_inline)) {
-      const int id = max(0, ids[(min(t + my_token, w1 - 1) >> L.page_shift) - first_page]);
-      const T *at = base + (int64_t)id * page_stride + ((t + my_token) & page_mask) * slot_step;
+    for (int w0 = begin, w1; w0 < end; w0 = w1) {
+      w1 = window_end(L, w0, end);
+      const bool any_bad = stage_ids(L, table, w0, w1, ids);
+      const int first_page = w0 >> L.page_shift;
+      // tokens past the last read the last page again
+      auto fetch = [&](int t, u32x4 (&x)[kFetch]) __attribute__((always_inline)) {
+        const int id = max(0, ids[(min(t + my_token, w1 - 1) >> L.page_shift) - first_page]);
+        const T *at = base + (int64_t)id * page_stride + ((t + my_token) & page_mask) * slot_step;
 #pragma unroll
-      for (int i = 0; i < kFetch; ++i) x[i] = ld_cache<kPast>(at + i * piece_step);
-    };
-    u32x4 ahead[kDeep][kFetch];
+        for (int i = 0; i < kFetch; ++i) x[i] = ld_cache<kPast>(at + i * piece_step);
+      };
+      u32x4 ahead[kDeep][kFetch];
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i)
-      if (w0 + i * kKeys < w1) fetch(w0 + i * kKeys, ahead[i]);
-    int buf = 0;
-    for (int t1 = w0; t1 < w1; t1 += kDeep * kKeys) {
+      for (int i = 0; i < kDeep; ++i)
+        if (w0 + i * kKeys < w1) fetch(w0 + i * kKeys, ahead[i]);
+      int buf = 0;
+      for (int t1 = w0; t1 < w1; t1 += kDeep * kKeys) {
 #pragma unroll
-      for (int i0 = 0; i0 < kDeep; i0 += kGroup) {
-        if (t1 + i0 * kKeys >= w1) break;  // uniform
+        for (int i0 = 0; i0 < kDeep; i0 += kGroup) {
+          if (t1 + i0 * kKeys >= w1) break;  // uniform
 #pragma unroll
-        for (int i = i0; i < i0 + kGroup; ++i) {
-          const int t = t1 + i * kKeys;
-          if (t < w1) {
+          for (int i = i0; i < i0 + kGroup; ++i) {
+            const int t = t1 + i * kKeys;
+            if (t < w1) {
 #pragma unroll
-            for (int f = 0; f < kFetch; ++f) ring[buf][i - i0][wave * kFetch + f][lane] = ahead[i][f];
-            if (t + kDeep * kKeys < w1) fetch(t + kDeep * kKeys, ahead[i]);
-          }
-        }
-        // the steps' pieces are in LDS; the buffer written next was last read
-        // before this barrier
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-        u32x4(*const here)[kPieces][kWave] = ring[buf];
-        buf ^= 1;
-        if (16 * wave >= rows) continue;  // no rows of this wave
-        // one copy of the step for all of them: the kernel has to stay in the
-        // instruction cache
-#pragma nounroll
-        for (int i = 0; i < kGroup; ++i) {
-          const int t = t1 + (i0 + i) * kKeys, t0 = t + kMine * g;
-          if (t >= w1) break;
-          u32x4(*const to)[kWave] = here[i];
-          const bool edge = any_bad || t + kKeys > least_high || t < most_low;  // uniform
-          float s[kMine];
-          {
-            typename St::template K<D> k;
-#pragma unroll
-            for (int u = 0; u < kTiles; ++u)
-#pragma unroll
-              for (int f = 0; f < kOut / kTiles; ++f) k.v[u][f] = to[u * (kOut / kTiles) + f][lane];
-#pragma unroll
-            for (int u = 0; u < kTiles; ++u) {
-              const floatx4 a = St::template scores<D>(k, u, q);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[4 * u + e] = a[e];
+              for (int f = 0; f < kFetch; ++f) ring[buf][i - i0][wave * kFetch + f][lane] = ahead[i][f];
+              if (t + kDeep * kKeys < w1) fetch(t + kDeep * kKeys, ahead[i]);
             }
           }
-          int seen = kMine;  // this lane's tokens whose values count
-          if (edge) {
-            const bool bad = any_bad && ids[(min(t0, w1 - 1) >> L.page_shift) - first_page] < 0;
-            if (bad) bits |= kErrPage;
-            mask_scores<kMine>(s, row, t0, bad);
-            seen = bad ? 0 : sl.len - t0;
-          }
-          const typename St::P pr = weigh<T, kOut>(s, to_log2, row, o);
-          if (!edge) {
+          // the steps' pieces are in LDS; the buffer written next was last read
+          // before this barrier
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+          u32x4(*const here)[kPieces][kWave] = ring[buf];
+          buf ^= 1;
+          if (16 * wave >= rows) continue;  // no rows of this wave
+          // one copy of the step for all of them: the kernel has to stay in the
+          // instruction cache
+#pragma nounroll
+          for (int i = 0; i < kGroup; ++i) {
+            const int t = t1 + (i0 + i) * kKeys, t0 = t + kMine * g;
+            if (t >= w1) break;
+            u32x4(*const to)[kWave] = here[i];
+            const bool edge = any_bad || t + kKeys > least_high || t < most_low;  // uniform
+            float s[kMine];
+            {
+              typename St::template K<D> k;
 #pragma unroll
-            for (int d = 0; d < kOut; ++d) o[d] = St::product(to[kOut + d][lane], pr, o[d]);
-          } else {
+              for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-            for (int d = 0; d < kOut; ++d) {
-              const u32x4 v = St::keep(to[kOut + d][lane], 0, seen);
-              if (__ballot(St::not_finite(v)) == 0) o[d] = St::product(v, pr, o[d]);
-              else o[d] = product_mixed<T>(v, pr, row, t0, o[d]);
+                for (int f = 0; f < kOut / kTiles; ++f) k.v[u][f] = to[u * (kOut / kTiles) + f][lane];
+#pragma unroll
+              for (int u = 0; u < kTiles; ++u) {
+                const floatx4 a = St::template scores<D>(k, u, q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[4 * u + e] = a[e];
+              }
+            }
+            int seen = kMine;  // this lane's tokens whose values count
+            if (edge) {
+              const bool bad = any_bad && ids[(min(t0, w1 - 1) >> L.page_shift) - first_page] < 0;
+              if (bad) bits |= kErrPage;
+              mask_scores<kMine>(s, row, t0, bad);
+              seen = bad ? 0 : sl.len - t0;
+            }
+            const typename St::P pr = weigh<T, kOut>(s, to_log2, row, o);
+            if (!edge) {
+#pragma unroll
+              for (int d = 0; d < kOut; ++d) o[d] = St::product(to[kOut + d][lane], pr, o[d]);
+            } else {
+#pragma unroll
+              for (int d = 0; d < kOut; ++d) {
+                const u32x4 v = St::keep(to[kOut + d][lane], 0, seen);
+                if (__ballot(St::not_finite(v)) == 0) o[d] = St::product(v, pr, o[d]);
+                else o[d] = product_mixed<T>(v, pr, row, t0, o[d]);
+              }
             }
           }
         }
       }
-    }
     }
     if (bits) flag_error(L.err, bits);
     const int c = 16 * wave + col;

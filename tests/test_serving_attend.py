@@ -151,6 +151,35 @@ def test_long_context_is_split_and_joined(dt, rows, L):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("rows", [1, 20])
+def test_more_pages_than_a_workgroup_holds_at_once(rows):
+    """64 key-value heads leave 8 shares a head, each of more than 1024 pages of 16."""
+    c = Case([rows], [141000], 64, 64, 64, 16, BF, seed=8)
+    c.check(c.run())
+
+
+def test_many_short_requests_in_a_share():
+    """Stretches of a few tokens one after another, empty ones and whole ones among
+    them, more than one block of rows, a bad page in one of them."""
+    g = torch.Generator().manual_seed(2)
+    rows = torch.randint(0, 40, (300,), generator=g).tolist()
+    lens = [max(n, int(x)) if i % 7 else n // 2 for i, (n, x) in
+            enumerate(zip(rows, torch.randint(0, 260, (300,), generator=g)))]
+    for dt, D in ((BF, 128), (F, 96)):
+        c = Case(rows, lens, 8, 2, D, 16, dt, seed=9, append=False)
+        c.check(c.run())
+        full = [i for i, n in enumerate(lens) if n > 40 and rows[i]]
+        before = c.run()
+        c.table[full[3], 1] = -5
+        ws = ds.Workspace()
+        after = c.run(ws)
+        assert ws.error_code() == PAGE
+        keep = torch.ones(c.n, dtype=torch.bool, device="cuda")
+        keep[c.off[full[3]]:c.off[full[3] + 1]] = False
+        assert torch.equal(after["out"][keep], before["out"][keep])
+        assert torch.isfinite(after["out"].float()).all()
+
+
 def test_steep_scores_and_scale():
     """Scores of several hundred, rising along the context (the running maximum
     moves in almost every step) or falling."""
