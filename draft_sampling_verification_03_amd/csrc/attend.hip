@@ -376,7 +376,7 @@ __device__ __forceinline__ void store4(bf16_t *p, const float *v) {
 
 namespace {
 
-template <bool B> struct Flag { static constexpr bool value = B; };
+template <int N> struct Count { static constexpr int value = N; };
 
 // Where the window of page numbers that begins with token w0 ends: at a page's end,
 // for w0 may lie inside one.
@@ -847,7 +847,7 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
 }
 
 // The parts of the rows of units that were cut.  A row's part takes D / 4 lanes, so a
-// wave has 256 / D sides (two for D = 96), each with up to four parts in flight.
+// wave has 256 / D sides (two for D = 96), each with four or eight parts in flight.
 // Where a row has few parts every side takes a row of its own; where it may have
 // many, the workgroup's sides share one and are joined at the end.
 template <typename T, int D>
@@ -885,11 +885,12 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
     const int64_t slot_size = (int64_t)L.Hkv * p.block_rows;
     const int64_t base = (int64_t)hk * p.block_rows + row % p.block_rows;
     float m = kNone, all = 0.0f, x[4] = {0, 0, 0, 0};
-    for (int k0 = first; k0 < splits && there && splits > 1; k0 += 4 * stride) {
-      float2 ml[4];
-      floatx4 y[4];
+    auto take = [&](int k0, auto batch) __attribute__((always_inline)) {
+      constexpr int kBatch = decltype(batch)::value;
+      float2 ml[kBatch];
+      floatx4 y[kBatch];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
+      for (int v = 0; v < kBatch; ++v) {
         const int k = min(k0 + v * stride, splits - 1);
         const int64_t at = base + (2 * (int64_t)(s0 + k) + (k == 0)) * slot_size;
         ml[v] = p.part_ml[at];
@@ -897,14 +898,14 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
       }
       float now = m;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) now = fmaxf(now, ml[v].x);  // a part twice does no harm here
+      for (int v = 0; v < kBatch; ++v) now = fmaxf(now, ml[v].x);  // a part twice does no harm here
       const float old = exp2_fast(m - now);
       m = now;
       all *= old;
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] *= old;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
+      for (int v = 0; v < kBatch; ++v) {
         if (k0 + v * stride < splits) {
           const float f = exp2_fast(ml[v].x - m);
           all += f * ml[v].y;
@@ -912,6 +913,12 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
           for (int e = 0; e < 4; ++e) x[e] += f * y[v][e];
         }
       }
+    };
+    if (there && splits > 1) {
+      if (many)
+        for (int k0 = first; k0 < splits; k0 += 8 * stride) take(k0, Count<8>{});
+      else
+        for (int k0 = 0; k0 < splits; k0 += 4) take(k0, Count<4>{});
     }
     if (many) {  // uniform
       __syncthreads();
