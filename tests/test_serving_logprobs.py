@@ -107,6 +107,23 @@ def test_ties_and_uneven_rows(kind, dt):
     check(X, tok, k, 1.0, ds.logprobs(X, tok, k=k))
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("V", [257, 400, 1021, 1500, 4097, 9001])
+@pytest.mark.parametrize("levels", [1, 2, 3, 9, 70, 0])
+def test_small_vocabularies_with_ties(levels, V, dt):
+    """Fewer 128-byte lines than alternatives, so all elements reach the first
+    threshold; values from few levels, so that many share the one at the end."""
+    X, g = make(5, V, dt, 3)
+    if levels:
+        X.copy_((torch.randint(0, levels, (5, V), generator=g, device="cuda") * 0.25).to(dt))
+        X[3, : V // 2] = float("-inf")
+        X[4, 200] = 7.0  # one element above all the others
+    tok = torch.randint(-1, V, (5,), generator=g, device="cuda", dtype=torch.int32)
+    tok[3] = V - 1
+    for k in (1, 20, 64):
+        check(X, tok, k, 1.0, ds.logprobs(X, tok, k=k))
+
+
 @pytest.mark.parametrize("n,V,dt,k,masked", [(6, 30001, BF, 20, 0.98), (6, 5000, F, 64, 0.999),
                                              (64, 129277, F, 8, 0.5), (3, 70, BF, 64, 0.9)])
 def test_masked(n, V, dt, k, masked):
