@@ -320,11 +320,12 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
     }
     if (p.entropy != nullptr) p.entropy[row] = ok ? logS - E * 0.6931471805599453f / S : NAN;
     if (p.stats != nullptr) {
-      // S belongs to the exact max / T; the stored m is that rounded
+      // S belongs to the exact max / T; the stored m is that rounded, which is much of
+      // an exponent where logits are large
       const float m = mx * p.invT;
       const float off = fmaf(mx, p.invT_low, fmaf(mx, p.invT, -m));
       p.stats[2 * (int64_t)row] = ok ? m : NAN;
-      p.stats[2 * (int64_t)row + 1] = ok ? S + S * off : NAN;
+      p.stats[2 * (int64_t)row + 1] = ok ? S * expf(off) : NAN;
     }
     if (bits) flag_error(p.err, bits);
   }

@@ -291,6 +291,29 @@ def test_gradient_parts_alone_and_in_place():
     assert (wide[:, V:] == 5.0).all() and dx.data_ptr() == wide.data_ptr()
 
 
+@pytest.mark.parametrize("size", [1e4, -1e6, 3e7])
+def test_stats_and_gradient_of_large_logits(size):
+    """m = max / T is rounded to a 24th of its bits, which is far from small here; S
+    belongs to the rounded m.  A term of S is off by 3 u |d| (d its exponent, |d| e^d
+    <= 0.37) and two ulps, the sum by (V / 256 + 16) u, the factor e^off by two:
+    within 80 u.  p = e^d / S adds as much for its own term, so 170 u of p / T."""
+    V, T = 1000, 0.7
+    X, g = make(4, V, F, 12)
+    X.mul_(abs(size) * 2.0 ** -22).add_(size)
+    tok = torch.tensor([0, 5, V - 1, 77], dtype=torch.int32, device="cuda")
+    out = ds.logprobs(X, tok, temp=T)
+    z = X.double() / torch.tensor(T, device="cuda").double()
+    m, S = out["stats"][:, 0].double(), out["stats"][:, 1].double()
+    want = (z - m[:, None]).exp().sum(1)
+    close(S, want, 80 * U * want)
+    one = torch.ones(4, device="cuda")
+    dx = ds.logprobs_backward(X, out["stats"], None, tokens=tok, g_logp=one, temp=T)
+    p = z.softmax(1)
+    exact = -p
+    exact[torch.arange(4), tok.long()] += 1
+    close(dx, exact / T, 170 * U * (p + 0.02) / T)
+
+
 def test_gradient_against_differences():
     """Central differences of the forward formula in 64 bits, along random directions."""
     n, V, T = 4, 500, 0.8
