@@ -558,7 +558,7 @@ dspark_status dspark_cache_attend(int R, int rows_capacity, int Hq, int Hkv, int
   if (bad_attend_shape(R, rows_capacity, Hq, Hkv, D) || bad_cache_shape(R, page, max_pages, n_pages))
     return DSPARK_ERR_SHAPE;
   if (row_offset == nullptr && rows_capacity != R) return DSPARK_ERR_SHAPE;
-  if (!(scale > 0.0f) || !isfinite(scale) || window < 0) return DSPARK_ERR_VALUE;
+  if (!(scale >= 1e-30f && scale <= 1e30f) || window < 0) return DSPARK_ERR_VALUE;
   if (!q || !k_pages || !v_pages || !table || !kv_len || !out || !ws ||
       (k_new == nullptr) != (v_new == nullptr))
     return DSPARK_ERR_NULL;

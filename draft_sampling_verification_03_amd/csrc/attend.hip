@@ -45,8 +45,8 @@ constexpr int kFixed = 64;        // a unit's fixed cost, in tokens
 constexpr int kJoiners = 32;      // workgroups that join a request's rows, at most
 constexpr int kAppend = 8;        // rows whose values a workgroup writes at a time
 constexpr int kWindow = 1024;     // page numbers of a stretch that wait in LDS at a time
-constexpr float kNone = -1e30f;   // running maximum of a row that has seen nothing
-constexpr float kSlack = 8.0f;    // see rescale below
+constexpr float kNone = -3e38f;   // running maximum of a row that has seen nothing
+constexpr float kSlack = 8.0f;    // see weigh below
 
 struct AttendParams {
   AttendLaunch L;
@@ -56,7 +56,7 @@ struct AttendParams {
   int64_t *head;    // work units per share (tokens), of all requests
   int64_t *before;  // [R + 1] work units before each request
   int32_t *first;   // [most_shares] the request in which each share begins
-  float2 *part_ml;  // [2 most_shares][Hkv][block_rows]: (max in log2 units, sum)
+  float2 *part_ml;  // [2 most_shares][Hkv][block_rows]: (max, sum)
   float *part_o;    // [2 most_shares][Hkv][block_rows][D]
 };
 
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kBlock) void attend_prepare_kernel(AttendParams p) 
   const int b = blockIdx.x - 1, r = b % L.R, part = b / L.R / 4, parts = (gridDim.x - 1) / L.R / 4;
   const Slice s = slice_of(L, r, &bits);
   const int page_mask = (1 << L.page_shift) - 1;
-  const int elems = L.Hkv * L.D / 4, e0 = b / L.R % 4 * elems;  // a multiple of 16
+  const int elems = L.Hkv * L.D / 4, e0 = b / L.R % 4 * elems;  // a multiple of 8
   bits = 0;  // the layout reports the slices
   // the page of row j, null where it is not to be written
   auto page_of = [&](int j, void *pages, int64_t stride) __attribute__((always_inline)) {
@@ -440,7 +440,7 @@ __device__ __forceinline__ bool next_stretch(const AttendParams &p, Share *s, St
 }
 
 // One row (of Q) of a 16-row tile as a lane holds it: the tokens that it sees,
-// [low, high), the subtrahend m (log2 units) and its lane's share of the sum.
+// [low, high), the subtrahend m and its lane's share of the sum.
 struct RowState {
   int low, high;
   float m, l;
@@ -477,7 +477,8 @@ __device__ __forceinline__ void mask_scores(float *s, const RowState &r, int t0,
 // Scores to probabilities against the row's subtrahend.  That follows the running
 // maximum only when it is kSlack (a factor 2^8) behind: below that the sums just
 // grow, and what is summed so far needs no rescaling.  The lanes of a row (16, 32
-// and 48 apart) agree on it.
+// and 48 apart) agree on it.  The difference is formed before the factor: a fused
+// s to_log2 - m would leave the rounding of m, and beyond 2^30 that is an exponent.
 template <typename T, int kOut>
 __device__ __forceinline__ typename Step<T>::P weigh(float *s, float to_log2, RowState &r,
                                                      floatx4 (&o)[kOut]) {
@@ -485,11 +486,10 @@ __device__ __forceinline__ typename Step<T>::P weigh(float *s, float to_log2, Ro
   float top = s[0];
 #pragma unroll
   for (int i = 1; i < kMine; ++i) top = fmaxf(top, s[i]);
-  top *= to_log2;
-  if (__ballot(top > r.m + kSlack) != 0) {
+  if (__ballot((top - r.m) * to_log2 > kSlack) != 0) {
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float now = fmaxf(r.m, top), f = exp2_fast(r.m - now);
+    const float now = fmaxf(r.m, top), f = exp2_fast((r.m - now) * to_log2);
     r.m = now;
     r.l *= f;
 #pragma unroll
@@ -498,7 +498,7 @@ __device__ __forceinline__ typename Step<T>::P weigh(float *s, float to_log2, Ro
   float e[kMine], sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    e[i] = exp2_fast(fmaf(s[i], to_log2, -r.m));
+    e[i] = exp2_fast((s[i] - r.m) * to_log2);
     sum += e[i];
   }
   r.l += sum;
@@ -539,7 +539,7 @@ __device__ __forceinline__ void write_row(const AttendParams &p, const Slice &sl
   const int64_t out_row = (int64_t)(sl.row0 + j) * L.Hq + h;
   store4(reinterpret_cast<T *>(L.out) + out_row * L.D + d, y);
   if (d == 0 && L.lse != nullptr)
-    L.lse[out_row] = sum == 0.0f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(sum));
+    L.lse[out_row] = sum == 0.0f ? -INFINITY : fmaf(m, L.scale, logf(sum));
 }
 
 }  // namespace
@@ -685,7 +685,7 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(At
       float all = 0.0f, x[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int v = 0; v < kWaves; ++v) {
-        const float f = exp2_fast(lds_ml[v][c].x - mx);
+        const float f = exp2_fast((lds_ml[v][c].x - mx) * to_log2);
         all += f * lds_ml[v][c].y;
         const floatx4 y = *reinterpret_cast<const floatx4 *>(&lds_o[v][c][d]);
 #pragma unroll
@@ -859,6 +859,7 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int r = blockIdx.x;
   int bits = 0;
+  const float to_log2 = L.scale * kLog2e;
   const Slice s = slice_of(L, r, &bits);
   const Units u = units_of(p, s);
   const int64_t share = p.head[0], at0 = p.before[r];
@@ -899,7 +900,7 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
       float now = m;
 #pragma unroll
       for (int v = 0; v < kBatch; ++v) now = fmaxf(now, ml[v].x);  // a part twice does no harm here
-      const float old = exp2_fast(m - now);
+      const float old = exp2_fast((m - now) * to_log2);
       m = now;
       all *= old;
 #pragma unroll
@@ -907,7 +908,7 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
 #pragma unroll
       for (int v = 0; v < kBatch; ++v) {
         if (k0 + v * stride < splits) {
-          const float f = exp2_fast(ml[v].x - m);
+          const float f = exp2_fast((ml[v].x - m) * to_log2);
           all += f * ml[v].y;
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] += f * y[v][e];
@@ -933,7 +934,7 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
       for (int e = 0; e < 4; ++e) x[e] = 0.0f;
 #pragma unroll
       for (int v = 0; v < kSides; ++v) {
-        const float f = exp2_fast(lds_ml[v].x - m);
+        const float f = exp2_fast((lds_ml[v].x - m) * to_log2);
         all += f * lds_ml[v].y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += f * lds_x[v][d + e];

@@ -44,7 +44,9 @@ extern "C" {
  *   top_ids[i][j], top_logp[i][j], j < k: the k largest logits in descending
  *                 order, equal ones by ascending index, and their log
  *                 probabilities
- *   stats[i]    = (m, S), as dspark_tv_overlap takes them
+ *   stats[i]    = (m, S), as dspark_tv_overlap takes them (S belongs to the
+ *                 rounded m: with temp != 1 and |m| > 2^31 it may overflow, and
+ *                 dspark_logprobs_backward then takes the row as without stats)
  * A masked logit (-infinity) has probability 0, adds nothing to the entropy and
  * counts as an alternative (log probability -infinity) only behind every other.
  * Inputs
@@ -112,9 +114,11 @@ dspark_status dspark_logprobs_backward(int n_rows, int V, int64_t row_stride, ds
  * refs_out: either all three the same arrays (in place) or three that overlap
  * none of them.  1 <= R <= 8192; 1 <= n_pages <= 4194304; 1 <= max_pages with
  * R * max_pages <= 2^28 and page * max_pages <= 2^30.
- * A page number outside [0, n_pages) within a request's length sets
- * DSPARK_DEVERR_PAGE; such an entry is never followed.  A length outside
- * [0, page * max_pages] sets DSPARK_DEVERR_LENGTH and is read as 0.
+ * A page number outside [0, n_pages) that an operation comes upon within a
+ * request's length sets DSPARK_DEVERR_PAGE; such an entry is never followed.  A
+ * length outside [0, page * max_pages] sets DSPARK_DEVERR_LENGTH and is read as
+ * 0 by fork and release; commit and compact leave that request as it is, and
+ * reserve the whole state.
  * Workspace of every page operation: dspark_cache_workspace(R, n_pages) bytes. */
 size_t dspark_cache_workspace(int R, int n_pages);
 
@@ -135,8 +139,9 @@ dspark_status dspark_cache_fork(int R, int page, int max_pages, int n_pages, int
  * first copied to a new page (whole, in both pools), because the new tokens
  * will be written into it; where every holder writes it in this call, the
  * first of them keeps it.  All or nothing: with too few free pages (sets
- * DSPARK_DEVERR_NO_PAGES), a length past max_pages or a decreasing row_offset
- * (DSPARK_DEVERR_LENGTH) the state stays as it was.
+ * DSPARK_DEVERR_NO_PAGES), a length outside [0, page * max_pages] before or
+ * after, or a decreasing row_offset (DSPARK_DEVERR_LENGTH) the state stays as
+ * it was.
  *   k_pages, v_pages: the whole pools, page p at byte p * page_bytes of each
  *     (16-byte multiples); NULL both: no pages are copied (state only)
  *   missing [1] int32: 0 when done, the pages short, or -1 on a bad length */
@@ -202,7 +207,7 @@ dspark_status dspark_cache_compact(int R, int page, int max_pages, int n_pages,
  *   strides in elements, multiples of 16 bytes
  *   row_offset [R + 1], or NULL: one row each (rows_capacity = R)
  *   kv_len [R]: lens_out of dspark_cache_reserve; table, n_pages as above
- *   scale finite and > 0; window >= 0 (0: none)
+ *   1e-30 <= scale <= 1e30; window >= 0 (0: none)
  * Outputs: out [rows_capacity][Hq][D] (dt); lse [rows_capacity][Hq] fp32 or
  *   NULL.  Rows from row_offset[R] on stay as they were.
  * A slice of row_offset that decreases or passes rows_capacity, or a kv_len

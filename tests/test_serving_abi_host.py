@@ -128,6 +128,7 @@ def attend(**over):
     (dict(Hq=1), SHAPE), (dict(Hkv=0), SHAPE), (dict(Hq=2048), SHAPE), (dict(D=80), SHAPE),
     (dict(D=512), SHAPE), (dict(page=12), SHAPE), (dict(n_pages=0), SHAPE),
     (dict(row_offset=None), SHAPE), (dict(scale=0.0), VALUE), (dict(scale=float("inf")), VALUE),
+    (dict(scale=1e-31), VALUE), (dict(scale=1e31), VALUE),
     (dict(window=-1), VALUE), (dict(q=None), NULL), (dict(k_pages=None), NULL),
     (dict(v_pages=None), NULL), (dict(table=None), NULL), (dict(kv_len=None), NULL),
     (dict(out=None), NULL), (dict(ws=None), NULL), (dict(k_new=None), NULL), (dict(v_new=None), NULL),

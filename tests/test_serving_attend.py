@@ -191,6 +191,34 @@ def test_steep_scores_and_scale():
         c.check(c.run(scale=0.4), scale=0.4)
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("L", [128, 9000])
+@pytest.mark.parametrize("power,sign", [(40, 1), (40, -1), (113, 1), (113, -1)])
+def test_scores_of_any_size(power, sign, L, rows, dt):
+    """Scores sign m 2^power, m = t / L rounded down to 127 levels, and token L / 2 the
+    largest: all exact in fp32, and so far apart that the row is that token's value."""
+    c = Case([rows], [L], 4, 2, 64, 32, dt, append=False)
+    level = torch.arange(L, device="cuda") * 126 // L
+    level[L // 2] = 127
+    if sign < 0:
+        level = 128 - level
+    half = 2.0 ** (power // 2)
+    c.q.zero_()
+    c.q[..., 5] = half
+    c.K[0].zero_()
+    c.K[0][:, :, 5] = (sign * level[:, None] * (2.0 ** power / half)).to(dt)
+    c.fill(0, L)
+    ws = ds.Workspace()
+    o = c.run(ws, scale=1.0)
+    out, lse = o["out"], o["lse"]
+    assert ws.error_code() == 0
+    want = c.V[0][L // 2].repeat_interleave(2, 0)
+    assert torch.equal(out, want.expand(rows, 4, 64))
+    top = sign * float(level[L // 2]) * 2.0 ** power
+    assert torch.equal(lse, torch.full_like(lse, top))
+
+
 def test_rows_that_see_nothing():
     """kv_len 0, and rows before token 0; nothing is appended before it."""
     c = Case([1, 3, 2], [0, 2, 40], 4, 2, 64, 16, BF, append=False)
