@@ -27,7 +27,11 @@
 //
 // Bound: keys and values are read once from memory (2 Hkv D bytes a token for each
 // of K and V); the products are 4 Hq D n operations a token, far below the matrix
-// rate for the rows of a round.
+// rate for the rows of a round.  Measured (128 requests of 1 to 17 new rows over up to
+// 6000 tokens, 32 query and 8 key-value heads of 128, bf16, pages of 16; 1.60 GB):
+// layout and append 9 us, product 317 us (5.1 TB/s), join 16 us.  256 single tokens
+// over up to 4000 (2.10 GB): product 350 us (6.0 TB/s).  Three single fp32 tokens over
+// up to 120000 (92 MB): 4 + 22 + 7 us.
 #include <limits.h>
 
 #include "common.h"
@@ -39,9 +43,12 @@ namespace dspark {
 namespace {
 
 constexpr int kWaves = kBlock / kWave;
-constexpr int kShares = 2 * kComputeUnits;  // over all key-value heads: two workgroups a unit
+// Over all key-value heads: two workgroups a compute unit, as many as their registers
+// and LDS allow.  Three or four would only queue (verified batch 378 and 337 us for
+// 324 then, decoding 383 and 354 for 349).
+constexpr int kShares = 2 * kComputeUnits;
 constexpr int kCut = 128;         // a unit is cut at multiples of this many tokens
-constexpr int kFixed = 64;        // a unit's fixed cost, in tokens
+constexpr int kFixed = 64;        // a unit's fixed cost, in tokens (128 and 160: no change)
 constexpr int kJoiners = 32;      // workgroups that join a request's rows, at most
 constexpr int kAppend = 8;        // rows whose values a workgroup writes at a time
 constexpr int kWindow = 1024;     // page numbers of a stretch that wait in LDS at a time
@@ -175,7 +182,7 @@ __device__ __forceinline__ void lay_out(const AttendParams &p) {
 
 // Workgroups from 1 on: a quarter of the elements of up to kAppend rows of request
 // (b - 1) % R at a time.  Values lie along the tokens, so neighbouring lanes take
-// neighbouring rows: a store reaches 8 pieces of a page and not 64.
+// neighbouring rows: a store reaches 8 pieces of a page and not 64 (9 us for 10.5).
 template <typename T>
 __global__ __launch_bounds__(kBlock) void attend_prepare_kernel(AttendParams p) {
   if (blockIdx.x == 0) {
@@ -544,6 +551,9 @@ __device__ __forceinline__ void write_row(const AttendParams &p, const Slice &sl
 
 }  // namespace
 
+// Up to 16 rows, each wave its own steps: nothing passes through LDS but page numbers
+// and the joining of the waves, so the loads are bound by memory alone (6.0 TB/s with
+// two steps of 16 KB in flight a wave).
 template <typename T, int D, bool kPast>
 __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(AttendParams p) {
   using St = Step<T>;
@@ -700,7 +710,8 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(At
 // an operand of the matrix cores in lane order: waves 0 and 1 fetch the keys', 2 and
 // 3 the values', kDeep steps ahead in registers, and pass them on through two buffers
 // in LDS of kGroup steps each.  In lane order every LDS access is 1 KB in a row; one
-// barrier a buffer.
+// barrier a buffer (two steps a barrier and one copy of the step's code: 317 us, one
+// and two copies 325).  64 rows: with 128, two tiles a wave, the results spill.
 template <typename T, int D, bool kPast>
 __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(AttendParams p) {
   using St = Step<T>;
@@ -849,7 +860,8 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
 // The parts of the rows of units that were cut.  A row's part takes D / 4 lanes, so a
 // wave has 256 / D sides (two for D = 96), each with four or eight parts in flight.
 // Where a row has few parts every side takes a row of its own; where it may have
-// many, the workgroup's sides share one and are joined at the end.
+// many, the workgroup's sides share one and are joined at the end (verified batch: 16
+// us, 24 with a workgroup a row throughout).
 template <typename T, int D>
 __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
   constexpr int kLanes = D / 4, kSide = kWave / kLanes, kSides = kWaves * kSide;
