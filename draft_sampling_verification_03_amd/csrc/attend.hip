@@ -49,7 +49,8 @@ constexpr int kWaves = kBlock / kWave;
 constexpr int kShares = 2 * kComputeUnits;
 constexpr int kCut = 128;         // a unit is cut at multiples of this many tokens
 constexpr int kFixed = 64;        // a unit's fixed cost, in tokens (128 and 160: no change)
-constexpr int kJoiners = 32;      // workgroups that join a request's rows, at most
+constexpr int kJoiners = 32;      // workgroups that join a request's rows, at most;
+constexpr int kJoinGrid = 2048;   // more where requests are few, up to so many in all
 constexpr int kAppend = 8;        // rows whose values a workgroup writes at a time
 constexpr int kWindow = 1024;     // page numbers of a stretch that wait in LDS at a time
 constexpr float kNone = -3e38f;   // running maximum of a row that has seen nothing
@@ -104,6 +105,17 @@ __device__ __forceinline__ Units units_of(const AttendParams &p, const Slice &s)
   u.t0 = first_token(p.L, s);
   u.size = kFixed + (s.len - u.t0);
   return u;
+}
+// The order of a request's units: the first block, the last, the second, ...  A block
+// reads the tokens that its own rows see, so of a prompt's the first blocks are short
+// and the last long, and this way a share takes as many of both (a prompt of 4000
+// tokens, 32 and 8 heads of 128, bf16: 0.34 ms, 1.21 where every block passed over all
+// tokens and masked).
+__device__ __forceinline__ int block_at(int i, int blocks) {
+  return i & 1 ? blocks - 1 - i / 2 : i / 2;
+}
+__device__ __forceinline__ int place_of_block(int b, int blocks) {
+  return b < (blocks + 1) / 2 ? 2 * b : 2 * (blocks - 1 - b) + 1;
 }
 // Where a cut at `at` of a unit's `size` work units lies among its tokens.
 __device__ __forceinline__ int cut_at(int64_t at, int size) {
@@ -434,12 +446,16 @@ __device__ __forceinline__ bool next_stretch(const AttendParams &p, Share *s, St
   o->sl = slice_of(p.L, s->r, &bits);
   const Units u = units_of(p, o->sl);
   const int64_t rel = s->at - p.before[s->r];
-  const int b = (int)(rel / u.size);
-  const int64_t x = rel - (int64_t)b * u.size, x1 = min((int64_t)u.size, x + (s->end - s->at));
-  o->block_row = b * p.block_rows;
+  const int i = (int)(rel / u.size);
+  const int64_t x = rel - (int64_t)i * u.size, x1 = min((int64_t)u.size, x + (s->end - s->at));
+  o->block_row = block_at(i, u.blocks) * p.block_rows;
   o->rows = min(p.block_rows, o->sl.n * p.heads_per_group - o->block_row);
-  o->begin = u.t0 + cut_at(x, u.size);
-  o->end = u.t0 + cut_at(x1, u.size);
+  // of these tokens, those that some row of the block sees
+  const int past = o->sl.len - o->sl.n + 1;
+  const int high = max(0, past + (o->block_row + o->rows - 1) / p.heads_per_group);
+  const int low = p.L.window > 0 ? max(0, past + o->block_row / p.heads_per_group - p.L.window) & ~31 : 0;
+  o->begin = max(u.t0 + cut_at(x, u.size), low);
+  o->end = min(u.t0 + cut_at(x1, u.size), high);
   // a share has at most one part that begins within a unit and one that ends within
   o->slot = x > 0 ? 2 * s->index : x1 < u.size ? 2 * s->index + 1 : -1;
   s->at += x1 - x;
@@ -633,7 +649,7 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(At
           bool odd = false;
 #pragma unroll
           for (int d = 0; d < kOut; ++d) {
-            x.v.v[d] = St::keep(x.v.v[d], 0, bad ? 0 : sl.len - t0);
+            x.v.v[d] = St::keep(x.v.v[d], 0, bad ? 0 : end - t0);
             odd = odd || St::not_finite(x.v.v[d]);
           }
           mixed = __ballot(odd) != 0;
@@ -823,7 +839,7 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
               const bool bad = any_bad && ids[(min(t0, w1 - 1) >> L.page_shift) - first_page] < 0;
               if (bad) bits |= kErrPage;
               mask_scores<kMine>(s, row, t0, bad);
-              seen = bad ? 0 : sl.len - t0;
+              seen = bad ? 0 : end - t0;
             }
             const typename St::P pr = weigh<T, kOut>(s, to_log2, row, o);
             if (!edge) {
@@ -890,7 +906,7 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
     const int row = j * group + h % group, b = row / p.block_rows;
     if (b != unit) {  // most rows follow one of the same unit
       unit = b;
-      const int64_t at = at0 + (int64_t)b * u.size;
+      const int64_t at = at0 + (int64_t)place_of_block(b, u.blocks) * u.size;
       s0 = (int)(at / share);
       splits = (int)((at + u.size - 1) / share) - s0 + 1;
     }
@@ -1016,7 +1032,8 @@ template <typename T> hipError_t launch_attend_t(const AttendLaunch &L, hipStrea
   const int64_t spread = (kComputeUnits + L.R - 1) / L.R, sides = kWaves * (256 / L.D);
   int64_t gy = (heads + sides - 1) / sides;
   if (gy < spread) gy = heads < spread ? heads : spread;
-  const dim3 join(L.R, (unsigned)(gy < kJoiners ? gy : kJoiners));
+  const int64_t most = kJoiners * L.R < kJoinGrid ? kJoinGrid / L.R : kJoiners;
+  const dim3 join(L.R, (unsigned)(gy < most ? gy : most));
   switch (L.D) {
     case 64: launch_product<T, 64>(p, grid, join, stream); break;
     case 96: launch_product<T, 96>(p, grid, join, stream); break;

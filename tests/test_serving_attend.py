@@ -151,6 +151,19 @@ def test_long_context_is_split_and_joined(dt, rows, L):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("Hq,Hkv,window,page", [(4, 1, 0, 16), (6, 2, 0, 64), (7, 1, 50, 32), (8, 8, 333, 128)])
+def test_prompts(Hq, Hkv, window, page, dt):
+    """Many new rows a request: blocks that see the tokens to the end and blocks that
+    see a few, in odd and even number, cut and whole."""
+    c = Case([300, 1, 131, 70, 9], [300, 40, 400, 1200, 9], Hq, Hkv, 64, page, dt, seed=window)
+    ws = ds.Workspace()
+    o = c.run(ws, window=window)
+    assert ws.error_code() == 0
+    c.check(o, window=window)
+    pools_equal(c)
+
+
 @pytest.mark.parametrize("rows", [1, 20])
 def test_more_pages_than_a_workgroup_holds_at_once(rows):
     """64 key-value heads leave 8 shares a head, each of more than 1024 pages of 16."""
