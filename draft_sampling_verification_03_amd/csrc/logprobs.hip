@@ -340,7 +340,11 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
   // of each wave's lanes at least k lines reach the least of the four.
   float left = -INFINITY, thr = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) left = fmaxf(left, held[i]);
+  for (int b = 0; b < kHeld; b += 8) {
+    if (b * kBlock >= n_lines) continue;  // uniform
+#pragma unroll
+    for (int i = b; i < b + 8; ++i) left = fmaxf(left, held[i]);
+  }
   uint64_t out = 0;  // lanes taken
   for (int i = 0; i < (p.k + 3) / 4; ++i) {
     thr = wave_max(left);
@@ -357,11 +361,15 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
   // the lines that reach it (masked elements are filled in at the end)
   auto gather = [&](bool strictly) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const float m = held[i];
-      if (m != -INFINITY && (strictly ? m > thr : m >= thr)) {
-        const int at = atomicAdd(&n_list, 1);
-        if (at < kMaxLines) list[at] = i * kBlock + tid;
+    for (int b = 0; b < kHeld; b += 8) {
+      if (b * kBlock >= n_lines) continue;  // uniform
+#pragma unroll
+      for (int i = b; i < b + 8; ++i) {
+        const float m = held[i];
+        if (m != -INFINITY && (strictly ? m > thr : m >= thr)) {
+          const int at = atomicAdd(&n_list, 1);
+          if (at < kMaxLines) list[at] = i * kBlock + tid;
+        }
       }
     }
     __syncthreads();
