@@ -10,10 +10,12 @@
 // and pages: a few microseconds of latency, nothing to spread) while the other
 // workgroups copy the state when it does not change in place; then a wide
 // kernel that writes tables and counts and moves the pages.  commit and release
-// need no order: one launch, one wave per request.
+// need no order: one wave per request, after a copy of the state when it does not
+// change in place.  Of a small state one workgroup does all of a fork, commit or
+// release (by_one below).
 //
 // Bound: launches and the plan's latency (512 requests, 40000 pages: fork 3 + 3 us,
-// reserve 14 + 5, commit 3; 4 requests, 512 pages: 3 + 2, 6 + 3, 2), and for compact
+// reserve 14 + 5, commit 3; 4 requests, 512 pages: fork 4, reserve 6 + 3, commit 2), and for compact
 // the bytes moved (783 MB of pages: 142 us, 5.5 TB/s read and written; in stretches of
 // 16 KB a workgroup, all loads of one in flight before its stores).
 #include <limits.h>
@@ -180,22 +182,48 @@ __device__ __forceinline__ void give_back(const CacheState &s, int r, int from, 
 
 }  // namespace
 
-__global__ __launch_bounds__(kPlanBlock) void cache_copy_kernel(CacheState s) {
-  copy_state(s, blockIdx.x, gridDim.x);
-  for (int r = blockIdx.x * kPlanBlock + threadIdx.x; r < s.R; r += gridDim.x * kPlanBlock)
+// All of the state, lens too, by n_blocks workgroups.
+namespace {
+__device__ __forceinline__ void copy_all(const CacheState &s, int block, int n_blocks) {
+  copy_state(s, block, n_blocks);
+  for (int r = block * (int)blockDim.x + threadIdx.x; r < s.R; r += n_blocks * (int)blockDim.x)
     s.lens[r] = s.lens_in[r];
+}
+}  // namespace
+
+__global__ __launch_bounds__(kPlanBlock) void cache_copy_kernel(CacheState s) {
+  copy_all(s, blockIdx.x, gridDim.x);
 }
 
 // --------------------------------------------------------------------- fork
+// Request dst becomes src's first `len` tokens, by threads [thread, ...) in steps.
+namespace {
+__device__ __forceinline__ void share_pages(const CacheState &s, int src, int dst, int len, int thread,
+                                            int threads) {
+  if (len <= 0) return;
+  const int32_t *from = s.table + (int64_t)src * s.max_pages;
+  int32_t *to = s.table + (int64_t)dst * s.max_pages;
+  const int n = pages_of(len, s.page_shift);
+  for (int j = thread; j < n; j += threads) {
+    const int p = from[j];
+    to[j] = p;
+    if (bad_page(s, p)) flag_error(s.err, kErrPage);
+    else atomicAdd(&s.refs[p], 1);
+  }
+}
+}  // namespace
+
 // Which pairs hold: of those with the same destination the first does.  Leaves
-// each pair's length (-1: skipped) in the plan.
+// each pair's length (-1: skipped) in the plan; where it is the only workgroup
+// (`whole`), the pairs' pages follow at once.
 __global__ __launch_bounds__(kPlanBlock) void cache_fork_plan_kernel(CacheState s, int n,
                                                                      const int32_t *src,
-                                                                     const int32_t *dst) {
+                                                                     const int32_t *dst, bool whole) {
   if (blockIdx.x > 0) {
     copy_state(s, blockIdx.x - 1, gridDim.x - 1);
     return;
   }
+  if (whole && !s.in_place()) copy_state(s, 0, 1);
   const Plan plan(s);
   int32_t *owner = plan.per_request(0), *length = plan.per_request(1);
   const int tid = threadIdx.x;
@@ -224,21 +252,15 @@ __global__ __launch_bounds__(kPlanBlock) void cache_fork_plan_kernel(CacheState 
   for (int i = tid; i < n; i += kPlanBlock)
     if (length[i] >= 0) s.lens[dst[i]] = length[i];
   if (bits) flag_error(s.err, bits);
+  if (whole)  // the state is copied and every length known since the barriers above
+    for (int i = tid / kWave; i < n; i += kPlanWaves)
+      share_pages(s, src[i], dst[i], length[i], tid & (kWave - 1), kWave);
 }
 
 __global__ __launch_bounds__(kBlock) void cache_fork_kernel(CacheState s, const int32_t *src,
                                                             const int32_t *dst) {
-  const int i = blockIdx.x, len = Plan(s).per_request(1)[i];
-  if (len <= 0) return;
-  const int32_t *from = s.table + (int64_t)src[i] * s.max_pages;
-  int32_t *to = s.table + (int64_t)dst[i] * s.max_pages;
-  const int n = pages_of(len, s.page_shift);
-  for (int j = threadIdx.x; j < n; j += kBlock) {
-    const int p = from[j];
-    to[j] = p;
-    if (bad_page(s, p)) flag_error(s.err, kErrPage);
-    else atomicAdd(&s.refs[p], 1);
-  }
+  const int i = blockIdx.x;
+  share_pages(s, src[i], dst[i], Plan(s).per_request(1)[i], threadIdx.x, kBlock);
 }
 
 // ------------------------------------------------------------------ reserve
@@ -376,11 +398,10 @@ __global__ __launch_bounds__(kBlock) void cache_reserve_kernel(CacheState s, Cac
 }
 
 // ----------------------------------------------------------- commit, release
-__global__ __launch_bounds__(kBlock) void cache_commit_kernel(CacheState s,
-                                                              const int32_t *row_offset,
-                                                              const int32_t *n_acc) {
-  const int r = blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
-  if (r >= s.R) return;
+namespace {
+// One wave: request r keeps n_acc + 1 of its rows.
+__device__ __forceinline__ void commit_one(const CacheState &s, int r, const int32_t *row_offset,
+                                           const int32_t *n_acc) {
   const int lane = threadIdx.x & (kWave - 1);
   const int len = s.lens[r];
   const int64_t n = (int64_t)row_offset[r + 1] - row_offset[r], keep = (int64_t)n_acc[r] + 1;
@@ -393,11 +414,9 @@ __global__ __launch_bounds__(kBlock) void cache_commit_kernel(CacheState s,
   give_back(s, r, pages_of(now, s.page_shift), pages_of(len, s.page_shift));
 }
 
-__global__ __launch_bounds__(kBlock) void cache_release_kernel(CacheState s, int n,
-                                                               const int32_t *which) {
-  const int i = blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
-  if (i >= n) return;
-  const int lane = threadIdx.x & (kWave - 1), r = which[i];
+// One wave: request r leaves.
+__device__ __forceinline__ void release_one(const CacheState &s, int r) {
+  const int lane = threadIdx.x & (kWave - 1);
   if ((unsigned)r >= (unsigned)s.R) {
     if (lane == 0) flag_error(s.err, kErrLength);
     return;
@@ -410,6 +429,33 @@ __global__ __launch_bounds__(kBlock) void cache_release_kernel(CacheState s, int
     return;
   }
   give_back(s, r, 0, pages_of(len, s.page_shift));
+}
+
+// The number of this wave among all of the grid, and how many they are.  Where a
+// kernel is one workgroup that first copies the state, its waves see the copy.
+__device__ __forceinline__ int wave_index(const CacheState &s, bool whole, int *waves) {
+  if (whole) {
+    copy_all(s, 0, 1);
+    __threadfence_block();
+    __syncthreads();
+  }
+  *waves = gridDim.x * (blockDim.x / kWave);
+  return (blockIdx.x * blockDim.x + threadIdx.x) / kWave;
+}
+}  // namespace
+
+__global__ __launch_bounds__(kPlanBlock) void cache_commit_kernel(CacheState s,
+                                                                  const int32_t *row_offset,
+                                                                  const int32_t *n_acc, bool whole) {
+  int waves;
+  for (int r = wave_index(s, whole, &waves); r < s.R; r += waves)
+    commit_one(s, r, row_offset, n_acc);
+}
+
+__global__ __launch_bounds__(kPlanBlock) void cache_release_kernel(CacheState s, int n,
+                                                                   const int32_t *which, bool whole) {
+  int waves;
+  for (int i = wave_index(s, whole, &waves); i < n; i += waves) release_one(s, which[i]);
 }
 
 // ------------------------------------------------------------------ compact
@@ -511,16 +557,27 @@ int plan_blocks(const CacheState &s) {
 }
 int wave_blocks(int n) { return (n + kBlock / kWave - 1) / (kBlock / kWave); }
 void copy_out(const CacheState &s, hipStream_t stream) {
-  if (!s.in_place())
-    DSPARK_LAUNCH("cache_copy", stream, cache_copy_kernel, plan_blocks(s) - 1, kPlanBlock, s);
+  DSPARK_LAUNCH("cache_copy", stream, cache_copy_kernel, plan_blocks(s) - 1, kPlanBlock, s);
+}
+
+// Whether one workgroup does an operation on n requests that is else two launches:
+// up to 16 entries a thread to copy and as many of the requests' own.  It takes the
+// device no longer (16 requests, 600 pages: copy and release 4.3 us, 8.2 as two
+// launches) and the host 2.6 us less.  In place, commit and release are one launch
+// anyway.
+bool by_one(const CacheState &s, int n) {
+  const int64_t most = 16 * kPlanBlock;
+  return (s.in_place() || (int64_t)s.R * s.max_pages + s.n_pages <= most) &&
+         (int64_t)n * s.max_pages <= most;
 }
 }  // namespace
 
 hipError_t launch_cache_fork(const CacheState &S, int n, const int32_t *src, const int32_t *dst,
                              hipStream_t stream) {
-  DSPARK_LAUNCH("cache_fork_plan", stream, cache_fork_plan_kernel, plan_blocks(S), kPlanBlock, S, n,
-                src, dst);
-  DSPARK_LAUNCH("cache_fork", stream, cache_fork_kernel, n, kBlock, S, src, dst);
+  const bool whole = by_one(S, n);
+  DSPARK_LAUNCH("cache_fork_plan", stream, cache_fork_plan_kernel, whole ? 1 : plan_blocks(S),
+                kPlanBlock, S, n, src, dst, whole);
+  if (!whole) DSPARK_LAUNCH("cache_fork", stream, cache_fork_kernel, n, kBlock, S, src, dst);
   return hipGetLastError();
 }
 
@@ -534,15 +591,18 @@ hipError_t launch_cache_reserve(const CacheState &S, const CachePools &P, const 
 
 hipError_t launch_cache_commit(const CacheState &S, const int32_t *row_offset, const int32_t *n_acc,
                                hipStream_t stream) {
-  copy_out(S, stream);
-  DSPARK_LAUNCH("cache_commit", stream, cache_commit_kernel, wave_blocks(S.R), kBlock, S, row_offset,
-                n_acc);
+  const bool whole = !S.in_place() && by_one(S, S.R);
+  if (!whole && !S.in_place()) copy_out(S, stream);
+  DSPARK_LAUNCH("cache_commit", stream, cache_commit_kernel, whole ? 1 : wave_blocks(S.R),
+                whole ? kPlanBlock : kBlock, S, row_offset, n_acc, whole);
   return hipGetLastError();
 }
 
 hipError_t launch_cache_release(const CacheState &S, int n, const int32_t *which, hipStream_t stream) {
-  copy_out(S, stream);
-  DSPARK_LAUNCH("cache_release", stream, cache_release_kernel, wave_blocks(n), kBlock, S, n, which);
+  const bool whole = !S.in_place() && by_one(S, n);
+  if (!whole && !S.in_place()) copy_out(S, stream);
+  DSPARK_LAUNCH("cache_release", stream, cache_release_kernel, whole ? 1 : wave_blocks(n),
+                whole ? kPlanBlock : kBlock, S, n, which, whole);
   return hipGetLastError();
 }
 

@@ -174,6 +174,37 @@ def test_rounds(R, page, width, n_pages, elems, in_place):
 
 
 @pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("R,width", [(64, 200), (64, 300), (3, 5000), (3, 17000)])
+def test_states_on_both_sides_of_one_workgroup(R, width, in_place):
+    """Forks, commits and releases of states that one workgroup does alone (16384
+    entries to copy and of the requests' own) and of larger ones."""
+    m, d, rng = both(R, 16, width, 2 * R * 20 + 60, in_place, seed=width)
+    for step in range(3):
+        empty = [r for r in range(R) if not m.lens[r]]
+        full = [r for r in range(R) if m.lens[r]]
+        if full and empty:
+            k = len(empty)  # every empty request at once
+            src = [int(r) for r in rng.choice(full, k)]
+            m.fork(src, empty)
+            d.call(ds.cache_fork, cu(src), cu(empty))
+            d.check(m)
+        new = [int(rng.integers(0, 150)) for _ in range(R)]
+        off = offsets(new)
+        missing = m.reserve(new)
+        assert d.call(ds.cache_reserve, off, pools=True)["missing"].item() == missing == 0
+        acc = [int(rng.integers(-1, n)) for n in new]
+        for r in range(R):
+            m.cut(r, m.lens[r] - new[r] + acc[r] + 1)
+        d.call(ds.cache_commit, off, cu(acc))
+        d.check(m)
+        leave = [int(r) for r in rng.permutation(R)[: max(1, R // 3)]]
+        for r in leave:
+            m.cut(r, 0)
+        d.call(ds.cache_release, cu(leave))
+        d.check(m)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
 def test_shared_last_pages(in_place):
     """A shared, partly filled page: copied by every writer when somebody else
     keeps holding it, kept by the first when all write; a full page is never
