@@ -562,7 +562,7 @@ void copy_out(const CacheState &s, hipStream_t stream) {
 
 // Whether one workgroup does an operation on n requests that is else two launches:
 // up to 16 entries a thread to copy and as many of the requests' own.  It takes the
-// device no longer (16 requests, 600 pages: copy and release 4.3 us, 8.2 as two
+// device no longer (16 requests, 600 pages: copy and release 2.8 us, 3.6 as two
 // launches) and the host 2.6 us less.  In place, commit and release are one launch
 // anyway.
 bool by_one(const CacheState &s, int n) {
