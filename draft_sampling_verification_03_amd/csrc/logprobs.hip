@@ -378,6 +378,7 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
   int turn = 0;
   // Raises thr by halving the range of values until count(thr) is from k to most;
   // where equal values leave no such threshold, to the k-th largest, and false.
+  // Where thr is the maximum already it counts not once, so it passes no barrier.
   auto halve = [&](auto count, int most) __attribute__((always_inline)) {
     uint32_t lo = ordered(thr), hi = ordered(mx);
     bool found = false;
@@ -401,6 +402,7 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
       return block_count(n, counts, turn);
     };
     tied = !halve(lines_at, kMaxLines);
+    __syncthreads();  // every wave has read n_list
     if (tid == 0) n_list = 0;
     __syncthreads();
     gather(tied);  // strictly: fewer than k
@@ -463,6 +465,7 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinParams p) {
       return block_count(n, counts, turn);
     };
     tied = !halve(reach, kMaxCand);
+    __syncthreads();  // every wave has read n_cand
     if (tid == 0) n_cand = 0;
     __syncthreads();
     collect();

@@ -124,6 +124,28 @@ def test_small_vocabularies_with_ties(levels, V, dt):
         check(X, tok, k, 1.0, ds.logprobs(X, tok, k=k))
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("whole,k", [(True, 1), (True, 64), (False, 4), (False, 20)])
+def test_many_rows_whose_maxima_tie(whole, k, dt):
+    """The first threshold is the maximum already, so no value is counted between the
+    reading of a counter and its clearing: whole rows of one value (more lines than are
+    read again share it), and every third 128 bytes (fewer lines, but more elements
+    than are ranked)."""
+    n, V = 1500, 20480 // dt.itemsize * 2
+    X, g = make(n, V, dt, 21)
+    X.clamp_(max=2.5)
+    if whole:
+        X.fill_(3.0)
+    else:
+        X.view(n, -1, 128 // dt.itemsize)[:, ::3] = 3.0
+    tok = torch.randint(0, V, (n,), generator=g, device="cuda", dtype=torch.int32)
+    for _ in range(3):
+        ws = ds.Workspace()
+        out = ds.logprobs(X, tok, k=k, ws=ws)
+        assert ws.error_code() == 0
+        check(X, tok, k, 1.0, out)
+
+
 @pytest.mark.parametrize("n,V,dt,k,masked", [(6, 30001, BF, 20, 0.98), (6, 5000, F, 64, 0.999),
                                              (64, 129277, F, 8, 0.5), (3, 70, BF, 64, 0.9)])
 def test_masked(n, V, dt, k, masked):
