@@ -630,11 +630,12 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(GradParams p) {
     unpack16(raw[j], (T *)nullptr, x);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      // a masked logit has e = 0: its value and its d only have to be finite
-      const float v = fmaxf(x[q], -1e30f);
-      const float d = fmaf(v, p.invT_low, fmaf(v, p.invT, -m));
+      // A masked logit has e = 0 and its d only has to be finite.  Of -infinity the sum is
+      // -infinity or (times an invT_low of 0 or below) NaN, and the maximum takes the
+      // other operand for either; a row with a NaN has no statistics.
+      const float d = fmaxf(fmaf(x[q], p.invT_low, fmaf(x[q], p.invT, -m)), -1e4f);
       const float e = exp2_fast(d * kLog2e);
-      y[q] = e * r * fmaf(gH, fmaxf(d, -1e4f), base);
+      y[q] = e * r * fmaf(gH, d, base);
     }
     if (marked[local >> 5] >> (local & 31) & 1) {
       for (int i = 0; i <= p.k; ++i) {

@@ -336,6 +336,43 @@ def test_stats_and_gradient_of_large_logits(size):
     close(dx, exact / T, 170 * U * (p + 0.02) / T)
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("V", [700, 5003])
+@pytest.mark.parametrize("end", [1, -1])
+def test_gradient_of_rows_at_the_end_of_the_range(end, V, dt):
+    """Rows of the type's lowest (or largest) value, as a finite mask leaves them: every
+    entry alike; one entry a step of the type above or below the others; half of them
+    masked by -infinity; a large but ordinary floor.  Whole numbers of x - m, so the
+    probabilities are 1 / count or 0.  With incoming gradients, without, and in place."""
+    X, g = make(6, V, dt, 1)
+    top = end * torch.finfo(dt).max
+    X[:4] = top
+    X[1, 77] = top * (1 - torch.finfo(dt).eps)
+    X[2, 1::2] = float("-inf")
+    X[3] = -1e31
+    tok = torch.tensor([5, 77, 6, 3, -1, 4], dtype=torch.int32, device="cuda")
+    ws = ds.Workspace()
+    f = ds.logprobs(X, tok, k=3, ws=ws)
+    gl, gh, gt = (torch.randn(s, generator=g, device="cuda") for s in ((6,), (6,), (6, 3)))
+    kw = dict(tokens=tok, top_ids=f["top_ids"], ws=ws)
+    dx = ds.logprobs_backward(X, f["stats"], f["entropy"], g_logp=gl, g_entropy=gh, g_top=gt, **kw)
+    want, size = gradient(X, tok, gl, gh, f["top_ids"], gt, 1.0)
+    close(dx, want, 20 * U * size + 160 * U * (want.abs() + size / 40) + 1e-30
+          + (2.0 ** -8 * want.abs() if dt == BF else 0))
+    none = ds.logprobs_backward(X, f["stats"], f["entropy"], g_logp=0 * gl, g_entropy=0 * gh,
+                                g_top=0 * gt, **kw)
+    assert (none == 0).all()
+    # a temperature may take m out of range: such a row counts as one without statistics
+    for T in (0.7, 1.3):
+        h = ds.logprobs(X, tok, k=3, temp=T, ws=ds.Workspace())
+        assert ds.logprobs_backward(X, h["stats"], h["entropy"], tokens=tok, g_logp=gl, g_entropy=gh,
+                                    temp=T, ws=ds.Workspace()).isfinite().all()
+    wide = X.as_strided((6, X.stride(0)), (X.stride(0), 1)).clone()
+    ds.logprobs_backward(wide[:, :V], f["stats"], f["entropy"], g_logp=gl, g_entropy=gh, g_top=gt,
+                         out=wide[:, :V], **kw)
+    assert torch.equal(wide[:, :V], dx) and ws.error_code() == 0
+
+
 def test_gradient_against_differences():
     """Central differences of the forward formula in 64 bits, along random directions."""
     n, V, T = 4, 500, 0.8
