@@ -22,4 +22,4 @@ from ._abi import (  # noqa: F401
 from .api import (draft, draft_rnn, schedule, train_losses, tv_overlap, verify, verify_rnn,
                   Workspace)  # noqa: F401
 from .serving import (cache_attend, cache_commit, cache_compact, cache_fork, cache_release,
-                      cache_reserve, logprobs, logprobs_backward, PagedCache)  # noqa: F401
+                      cache_reserve, cache_reserved_rows, logprobs, logprobs_backward, PagedCache)  # noqa: F401

@@ -443,7 +443,8 @@ static dspark_status cache_state(int R, int page, int max_pages, int n_pages, co
   S->lens_in = lens; S->table_in = table; S->refs_in = refs;
   S->lens = lens_out; S->table = table_out; S->refs = refs_out;
   S->err = (int32_t *)ws;
-  S->plan = (int32_t *)((char *)ws + kWsHeader);
+  S->rows = (int32_t *)((char *)ws + kWsHeader);
+  S->plan = (int32_t *)((char *)ws + kWsHeader + ws_align(((size_t)R + 1) * 4));
   return DSPARK_OK;
 }
 

@@ -356,6 +356,8 @@ __global__ __launch_bounds__(kPlanBlock) void cache_reserve_plan_kernel(CacheSta
   for (int r = tid; r < s.R; r += kPlanBlock)
     if (go || !s.in_place())
       s.lens[r] = s.lens_in[r] + (go ? row_offset[r + 1] - row_offset[r] : 0);
+  // the round's other calls take these: of rows that found no room they do nothing
+  for (int r = tid; r <= s.R; r += kPlanBlock) s.rows[r] = go ? row_offset[r] : 0;
   if (tid == 0) {
     plan.head[0] = go ? n_copies : -1;
     *missing = bad ? -1 : max(total - all_free, 0);

@@ -139,6 +139,7 @@ struct CacheState {
   const int32_t *lens_in, *table_in, *refs_in;
   int32_t *lens, *table, *refs;
   int32_t *err;
+  int32_t *rows;  // [R + 1] behind the workspace's header: offsets that a reservation left
   int32_t *plan;  // scratch: cache_plan_ints(R, n_pages)
   __host__ __device__ bool in_place() const { return lens == lens_in; }
 };
@@ -214,7 +215,7 @@ inline size_t cache_plan_ints(int R, int n_pages) {
   return 64 + 3 * (size_t)R + 3 * (size_t)n_pages;
 }
 inline size_t cache_ws_bytes(int R, int n_pages) {
-  return kWsHeader + ws_align(cache_plan_ints(R, n_pages) * 4);
+  return kWsHeader + ws_align(((size_t)R + 1) * 4) + ws_align(cache_plan_ints(R, n_pages) * 4);
 }
 inline size_t overlap_ws_bytes(int n_rows, int V) {
   (void)V;

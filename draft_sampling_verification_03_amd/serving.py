@@ -294,11 +294,19 @@ def cache_fork(src, dst, lens, table, refs, *, page, ws=None, stream=None, out=N
     return s.run("dspark_cache_fork", page, ws, stream, out, (n, src.data_ptr(), dst.data_ptr()))
 
 
+def cache_reserved_rows(ws, R):
+    """The row offsets [R + 1] that the last cache_reserve() over `ws` left: those it was
+    given, or zeros where it found no room.  A view of the workspace: a round that does
+    not read `missing` gives it to cache_attend() and cache_commit() as row_offset."""
+    return ws.buf[256:256 + 4 * (R + 1)].view(I32)
+
+
 def cache_reserve(row_offset, lens, table, refs, k_pages, v_pages, *, page, ws=None, stream=None,
                   out=None):
     """Pages for row_offset[r + 1] - row_offset[r] new tokens of every request.
     k_pages, v_pages: the whole pools, [n_pages][...] (None both: the state
-    alone).  Returns the state and missing [1] (0: done)."""
+    alone).  Returns the state and missing [1] (0: done; else look at it before
+    the round goes on, or go on with cache_reserved_rows())."""
     s = _State("cache_reserve", lens, table, refs)
     s.a.req(row_offset, "row_offset", I32, (s.R + 1,))
     size = s.pools(k_pages, v_pages)
@@ -386,6 +394,7 @@ class PagedCache:
     A round: reserve(row_offset), attend(layer, ...) for every layer, and after
     the verification commit(n_acc).  All state lives on the device and changes
     in place; nothing waits for the host, and a captured round may be replayed.
+    A round that finds no room (see reserve()) changes nothing in any of the three.
     error_code() reads what the device found wrong so far."""
 
     def __init__(self, R, n_pages, *, Hkv, D, layers=1, page=16, max_pages=None,
@@ -401,14 +410,17 @@ class PagedCache:
         self.n_live = torch.zeros(1, dtype=I32, device=device)
         self.row_offset = None
         self.ws, self.attend_ws = Workspace(device), Workspace(device)
+        self.ws.get(_cache_ws(R, n_pages), None, self.lens.device)
+        self.rows = cache_reserved_rows(self.ws, R)
 
     def _state(self):
         return dict(lens=self.lens, table=self.table, refs=self.refs)
 
     def reserve(self, row_offset, stream=None):
-        """Room for the round's rows; missing[0] says how many pages were short
-        (then nothing has changed)."""
-        self.row_offset = row_offset
+        """Room for the round's rows; missing[0] says how many pages were short (-1: a
+        length out of bounds).  Then nothing has changed, and the round's attend() and
+        commit() change nothing either: row_offset here is all zeros."""
+        self.row_offset = self.rows
         cache_reserve(row_offset, self.lens, self.table, self.refs, self.k, self.v, page=self.page,
                       ws=self.ws, stream=stream, out=dict(self._state(), missing=self.missing))
         return self.missing

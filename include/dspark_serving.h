@@ -14,8 +14,11 @@
  * One round of a server with a paged target (Blog, "Variable-length
  * verification without wasting kernels"): dspark_draft -> dspark_schedule ->
  * dspark_cache_reserve(row_offset) -> the target's layers, each with one
- * dspark_cache_attend over the same row_offset -> dspark_verify ->
- * dspark_cache_commit(row_offset, n_acc) -> dspark_logprobs(P, y).
+ * dspark_cache_attend over the reserved rows -> dspark_verify ->
+ * dspark_cache_commit(reserved rows, n_acc) -> dspark_logprobs(P, y).  The reserved
+ * rows are row_offset again for a host that has read `missing` and found 0; one that
+ * does not wait for it (a captured round) passes the copy that reserve leaves in its
+ * workspace, and a round that found no room then changes nothing.
  *
  * The conventions of dspark.h hold: device pointers, 16-byte aligned unless
  * stated; caller-owned buffers; host-side validation first; asynchronous on
@@ -144,7 +147,14 @@ dspark_status dspark_cache_fork(int R, int page, int max_pages, int n_pages, int
  * it was.
  *   k_pages, v_pages: the whole pools, page p at byte p * page_bytes of each
  *     (16-byte multiples); NULL both: no pages are copied (state only)
- *   missing [1] int32: 0 when done, the pages short, or -1 on a bad length */
+ *   missing [1] int32: 0 when done, the pages short, or -1 on a bad length
+ * The reserved rows: R + 1 int32 at byte 256 of the workspace, row_offset where the
+ * call is done and zeros where it changed nothing.  They stay until the next reserve
+ * over the workspace (and a call over it with another R).  Given as row_offset,
+ * dspark_cache_attend has no rows after a reserve that changed nothing, so it writes
+ * neither pages nor outputs, and dspark_cache_commit leaves every request as it is
+ * (and sets DSPARK_DEVERR_LENGTH where n_acc >= 0).  With the caller's own row_offset
+ * they would take the last tokens held for the round's. */
 dspark_status dspark_cache_reserve(int R, int page, int max_pages, int n_pages,
                                    const int32_t *row_offset, const int32_t *lens,
                                    const int32_t *table, const int32_t *refs, int32_t *lens_out,

@@ -421,3 +421,62 @@ def test_prompt_then_rounds():
             for layer in range(2):
                 K[layer][1], V[layer][1] = K[layer][0], V[layer][0]
     assert cache.error_code() == 0
+
+
+def snapshot(cache):
+    return [t.clone() for t in (cache.lens, cache.table, cache.refs, cache.k, cache.v)]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("why", ["pages", "length"])
+def test_a_round_without_room_changes_nothing(why, captured):
+    """Nobody looks at `missing`: the rounds that find no pages (or pass max_pages) leave
+    every length, page number, count, key and value as it was, shared pages too, and
+    the first round that finds room goes on from there."""
+    R, Hq, Hkv, D = 4, 4, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = ds.PagedCache(R, 5, Hkv=Hkv, D=D, page=16, dtype=F, max_pages=3 if why == "pages" else 2)
+    cache.reserve(i32([0, 20, 20, 50, 50]))
+    cache.attend(0, r(50, Hq, D), r(50, Hkv, D), r(50, Hkv, D))
+    cache.commit(i32([19, -1, 29, -1]))
+    cache.fork(i32([0]), i32([1]))
+    # requests 0 and 1 write a shared page, 2 needs a new one: two pages, one is free (or
+    # 33 tokens in two pages of 16)
+    off, acc = i32([0, 3, 6, 9, 9]), i32([1, 0, 1, -1])
+    q, kn, vn = r(9, Hq, D), r(9, Hkv, D), r(9, Hkv, D)
+    out = dict(out=torch.full((9, Hq, D), 3.0, device="cuda"), lse=torch.full((9, Hq), 3.0, device="cuda"))
+
+    def go():
+        cache.reserve(off)
+        cache.attend(0, q, kn, vn, out=out)
+        cache.commit(acc)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go()
+        go = graph.replay
+    before = snapshot(cache)
+    for _ in range(3):
+        go()
+        torch.cuda.synchronize()
+        assert same(snapshot(cache), before)
+        assert cache.missing.item() == (1 if why == "pages" else -1)
+        assert (out["out"] == 3).all() and (out["lse"] == 3).all()
+        assert cache.error_code() == (LENGTH if why == "length" else LENGTH | 64)
+    cache.release(i32([2]))
+    go()
+    torch.cuda.synchronize()
+    assert cache.missing.item() == 0 and cache.lens.tolist() == [22, 21, 2, 0]
+    for i, (had, keep) in enumerate(((20, 2), (20, 1), (0, 2))):
+        for j in range(had + keep):
+            p, s = int(cache.table[i, j // 16]), j % 16
+            k = kn[3 * i + j - had] if j >= had else before[3][int(before[1][0, j // 16]), 0, :, s]
+            assert torch.equal(cache.k[p, 0, :, s], k)
+    assert cache.refs.tolist().count(0) == 1
