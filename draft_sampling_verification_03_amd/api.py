@@ -80,33 +80,51 @@ class _Args:
 
 class Workspace:
     """Device scratch for one entry point, zeroed once at allocation (the sticky
-    error word lives in its first 256 bytes); grows on demand.  The buffer is
-    allocated and zeroed on the stream of the call that needs it; a call on
-    another stream marks it as used there."""
+    error word lives in its first 256 bytes); grows on demand, to twice its size
+    at least.  An outgrown buffer (or another device's) is kept, for a captured graph
+    may still write to it, and its error word counts.  The buffer is allocated and
+    zeroed on the stream of the call that needs it; a call on another stream marks
+    it as used there."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = None
+        self.outgrown = []
         self._streams = set()
 
     def get(self, nbytes, stream=None, device=None):
-        dev = device if device is not None else self.device
-        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(dev):
-            with _on_stream(stream):
-                self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
-            self._streams = {id(stream)}
-        elif isinstance(stream, torch.cuda.Stream) and id(stream) not in self._streams:
+        dev = torch.device(device if device is not None else self.device)
+
+        def here(buf):
+            return buf.device.type == dev.type and dev.index in (None, buf.device.index)
+
+        if self.buf is None or self.buf.numel() < nbytes or not here(self.buf):
+            held = [*self.outgrown, *([] if self.buf is None else [self.buf])]
+            mine = [b for b in held if here(b)]  # more than one device: each has its own
+            buf, streams = next((b for b in mine if b.numel() >= nbytes), None), set()
+            if buf is None:
+                size = max([nbytes, 256] + [2 * b.numel() for b in mine])
+                with _on_stream(stream):
+                    buf = torch.zeros(size, dtype=torch.uint8, device=dev)
+                streams = {id(stream)}
+            self.outgrown = [b for b in held if b is not buf]
+            self.buf, self._streams = buf, streams
+        if isinstance(stream, torch.cuda.Stream) and id(stream) not in self._streams:
             self.buf.record_stream(stream)
             self._streams.add(id(stream))
         return self.buf
 
     def error_code(self, stream=None):
-        st, code = A.dspark_device_error(self.buf, _stream(stream))
-        _check(st, "dspark_device_error")
-        return code
+        bits = 0
+        for buf in (*self.outgrown, self.buf):
+            st, code = A.dspark_device_error(buf, _stream(stream))
+            _check(st, "dspark_device_error")
+            bits |= code
+        return bits
 
     def clear_error(self, stream=None):
-        _check(A.dspark_clear_device_error(self.buf, _stream(stream)), "dspark_clear_device_error")
+        for buf in (*self.outgrown, self.buf):
+            _check(A.dspark_clear_device_error(buf, _stream(stream)), "dspark_clear_device_error")
 
 
 def _empty(shape, dtype, dev):

@@ -3,6 +3,7 @@ function is exported, and every invalid argument is refused before any HIP
 call.  The pointers are fake aligned addresses that nothing dereferences."""
 import os
 import re
+import weakref
 
 import pytest
 import torch
@@ -206,3 +207,43 @@ def test_cache_object_refuses_out_of_order():
         cache.commit(host(2, dtype=I32))
     with pytest.raises(ValueError, match=r"reserve\(\) comes first"):
         cache.attend(0, host(2, 8, 64), host(2, 2, 64), host(2, 2, 64))
+
+
+def test_an_outgrown_workspace_is_kept_with_its_errors(monkeypatch):
+    """What a captured graph writes to stays allocated, and error bits in it count."""
+    def read(buf, stream):
+        return 0, int(buf[:4].view(I32))
+
+    def clear(buf, stream):
+        buf[:4].zero_()
+        return 0
+
+    monkeypatch.setattr(A, "dspark_device_error", read)
+    monkeypatch.setattr(A, "dspark_clear_device_error", clear)
+    monkeypatch.setattr(ds.api, "_stream", lambda stream, *device: stream)
+    ws = ds.Workspace("cpu")
+    first = ws.get(300)
+    alive = weakref.ref(first)
+    first[0] = 4
+    del first
+    second = ws.get(301)
+    assert second.numel() >= 301 and (second == 0).all()
+    assert alive() is not None and ws.error_code() == 4
+    second[0] = 8
+    ws.get(100000)[0] = 32
+    assert ws.error_code() == 4 | 8 | 32
+    alive()[0] = 2  # a replay of what was captured over the first
+    assert ws.error_code() == 2 | 8 | 32
+    ws.clear_error()
+    assert ws.error_code() == 0
+    # growing in small steps keeps no more than a few times what is needed
+    ws = ds.Workspace("cpu")
+    for n in range(1000, 100000, 1000):
+        ws.get(n)
+    assert sum(t.numel() for t in (ws.buf, *ws.outgrown)) <= 4 * 100000
+    # on two devices in turn: one buffer each
+    ws = ds.Workspace("cpu")
+    a, b = ws.get(300), ws.get(300, device="meta")
+    for n in (300, 200, 300):
+        assert ws.get(n) is a and ws.get(n, device="meta") is b
+    assert ws.outgrown == [a]

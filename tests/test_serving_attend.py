@@ -480,3 +480,43 @@ def test_a_round_without_room_changes_nothing(why, captured):
             k = kn[3 * i + j - had] if j >= had else before[3][int(before[1][0, j // 16]), 0, :, s]
             assert torch.equal(cache.k[p, 0, :, s], k)
     assert cache.refs.tolist().count(0) == 1
+
+
+def test_error_bits_survive_a_larger_call():
+    c = Case([1, 1], [40, 9], 8, 1, 64, 16, BF, seed=3)
+    big = Case([30, 1], [40, 9], 8, 1, 64, 16, BF, seed=4)
+    ws = ds.Workspace()
+    c.table[0, 1] = -1
+    c.run(ws)
+    small = ws.buf.numel()
+    big.run(ws)
+    assert ws.buf.numel() > small and ws.error_code() == PAGE
+    ws.clear_error()
+    assert ws.error_code() == 0
+
+
+def test_a_captured_round_outlives_a_larger_call():
+    """Single tokens are captured, a prompt then makes the workspace grow, its old
+    memory would be handed out: the replays leave what was allocated since alone."""
+    c = Case([1, 1, 1], [700, 30, 1200], 8, 2, 64, 16, BF, seed=6)
+    big = Case([90, 1, 3], [700, 30, 1200], 8, 2, 64, 16, BF, seed=7)
+    ws = ds.Workspace()
+    c.run(ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = c.run(ws)
+    size = ws.buf.numel()
+    big.check(big.run(ws))
+    assert ws.buf.numel() > size
+    other = [torch.full((size,), 77, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        c.q.copy_(torch.randn(c.q.shape, device="cuda").to(BF))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(o)
+        assert all((t == 77).all() for t in other)
+    c.table[1, 0] = -4  # what a replay finds wrong is reported too
+    graph.replay()
+    torch.cuda.synchronize()
+    assert ws.error_code() == PAGE
