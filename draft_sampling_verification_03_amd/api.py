@@ -84,7 +84,8 @@ class Workspace:
     at least.  An outgrown buffer (or another device's) is kept, for a captured graph
     may still write to it, and its error word counts.  The buffer is allocated and
     zeroed on the stream of the call that needs it; a call on another stream marks
-    it as used there."""
+    it as used there.  Made within a capture it is cleared by every replay: call once
+    before, or get() its size, where the error word is to last."""
 
     def __init__(self, device="cuda"):
         self.device = device

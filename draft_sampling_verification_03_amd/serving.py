@@ -409,8 +409,12 @@ class PagedCache:
         self.missing = torch.zeros(1, dtype=I32, device=device)
         self.n_live = torch.zeros(1, dtype=I32, device=device)
         self.row_offset = None
+        # made here and never outgrown: a buffer made within a capture would be cleared by
+        # every replay, and the errors found so far with it.  Of the attention's, the size
+        # for any number of rows and query heads (34 MB for heads of 128).
         self.ws, self.attend_ws = Workspace(device), Workspace(device)
         self.ws.get(_cache_ws(R, n_pages), None, self.lens.device)
+        self.attend_ws.get(_attend_ws(R, 1 << 20, Hkv, Hkv, D, A.DSPARK_F32), None, self.lens.device)
         self.rows = cache_reserved_rows(self.ws, R)
 
     def _state(self):

@@ -520,3 +520,31 @@ def test_a_captured_round_outlives_a_larger_call():
     graph.replay()
     torch.cuda.synchronize()
     assert ws.error_code() == PAGE
+
+
+def test_a_round_captured_at_once_keeps_its_errors():
+    """Nothing ran over the cache's workspaces before the capture: no replay clears what
+    an earlier one found."""
+    Hq, Hkv, D = 4, 2, 64
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = ds.PagedCache(2, 8, Hkv=Hkv, D=D, page=16, dtype=F)
+    off, acc = i32([0, 40, 41]), i32([39, 0])
+    q, kn = torch.randn(41, Hq, D, device="cuda"), torch.randn(41, Hkv, D, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.reserve(off)
+        cache.attend(0, q, kn, kn)
+        cache.commit(acc)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert cache.lens.tolist() == [40, 1] and cache.error_code() == 0
+    off.copy_(i32([0, 1, 2])), acc.copy_(i32([0, 0]))
+    page = cache.table[0, 0].clone()
+    cache.table[0, 0] = -4
+    graph.replay()
+    cache.table[0, 0] = page
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert cache.error_code() == PAGE
+    assert cache.lens.tolist() == [43, 4]
