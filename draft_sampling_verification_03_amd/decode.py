@@ -25,6 +25,8 @@ values in step: before the target rows it reserves pages for every scheduled
 row, and after the verification it gives back what the rejected rows held.
 With `logprobs` it returns what a server sends along with the tokens.
 """
+import contextlib
+
 import numpy as np
 import torch
 
@@ -72,6 +74,24 @@ def _record_logprobs(rec, lp, row_offset, n_acc, gamma):
             rec[name].append(full)
 
 
+@contextlib.contextmanager
+def _current(stream, device):
+    """Makes `stream` (or the address of one) current behind what is queued so far; what
+    follows is queued behind it."""
+    if stream is None:
+        yield None
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    before = torch.cuda.current_stream(stream.device)
+    stream.wait_stream(before)
+    try:
+        with torch.cuda.stream(stream):
+            yield stream
+    finally:
+        before.wait_stream(stream)
+
+
 def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, threshold=0.0,
            conf_of_round=None, history=None, temp=1.0, seed=0, first_round=0, stream=None,
            cache=None, logprobs=None):
@@ -94,6 +114,8 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
                   cache before the next round.  Too few pages raise RuntimeError.
     logprobs      number of alternatives (0: none) to report beside the log
                   probability and entropy of every emitted token
+    stream        a stream (or its address) to run on, behind what the current one
+                  has queued; it is the current one while the callables run
 
     Returns a dict of per-round host arrays (x, ell, n_acc, y, theta,
     n_admitted; with confidences also c and a, the predicted tokens
@@ -103,6 +125,13 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
     `logprobs` also lists of [R][gamma + 1] arrays beside y (NaN, and -1 for
     tokens, past the emitted ones): logp, entropy and, for alternatives,
     top_ids and top_logp with a last dimension of that number."""
+    with _current(stream, W1.device) as stream:
+        return _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold,
+                       conf_of_round, history, temp, seed, first_round, stream, cache, logprobs)
+
+
+def _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold, conf_of_round, history,
+            temp, seed, first_round, stream, cache, logprobs):
     ws_d, ws_s, ws_v, ws_l = api.Workspace(), api.Workspace(), api.Workspace(), api.Workspace()
     anchors = torch.as_tensor(np.asarray(x0, dtype=np.int32) if not torch.is_tensor(x0) else x0)
     anchors = anchors.to(W1.device, dtype=torch.int32).contiguous()
@@ -142,10 +171,7 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
         prev = np.concatenate([np.concatenate(([a[rho]], x[rho, : ell[rho]]))
                                for rho in range(R)]).astype(np.int64)
         if cache is not None:
-            missing = cache.reserve(s["row_offset"], stream=stream)
-            if isinstance(stream, torch.cuda.Stream):
-                stream.synchronize()
-            short = int(missing)
+            short = int(cache.reserve(s["row_offset"], stream=stream))
             if short:
                 raise RuntimeError(f"decode: round {t} needs {short} more pages than the cache has free"
                                    if short > 0 else f"decode: round {t} passes the cache's max_pages")

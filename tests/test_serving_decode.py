@@ -187,3 +187,40 @@ def test_decode_stops_when_pages_run_out():
     with pytest.raises(RuntimeError, match="more pages than the cache has free"):
         decode.decode(40, np.array([1, 2], np.int32), W1, W2, U, model.rows, cache=cache)
     assert cache.error_code() & 64
+
+
+@pytest.mark.parametrize("address", [False, True])
+def test_decode_on_another_stream(address):
+    """Slow draft logits and target rows on a stream that is not the current one: the
+    same tokens, log probabilities and pages as without it."""
+    R, gamma = 4, 3
+    rng = np.random.default_rng(9)
+    prompts = [rng.integers(0, V, n).tolist() for n in (3, 20, 6, 40)]
+    W1, W2, U = head(11, R, gamma)
+
+    def go(stream):
+        cache = ds.PagedCache(R, 40, Hkv=HKV, D=D, layers=LAYERS, page=16, dtype=torch.float32)
+        model = Model(12, R, prompts)
+        x0 = prefill(model, cache, prompts)
+        current = torch.cuda.current_stream() if stream is None else stream
+
+        def slowly(f):
+            def slow(*args):
+                assert torch.cuda.current_stream().cuda_stream == current.cuda_stream
+                torch.cuda._sleep(2_000_000)
+                return f(*args)
+            return slow
+
+        res = decode.decode(6, x0, W1, W2, slowly(U), slowly(model.rows), cache=cache, logprobs=2,
+                            stream=stream.cuda_stream if address and stream is not None else stream)
+        assert res["device_errors"] == (0,) * 5 and model.worst < 1e-4
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        return res, cache
+
+    want, held = go(None)
+    got, cache = go(torch.cuda.Stream())
+    for name in ("x", "ell", "n_acc", "y", "logp", "entropy", "top_ids", "top_logp"):
+        assert np.array_equal(got[name], want[name], equal_nan=got[name].dtype.kind == "f"), name
+    assert got["streams"] == want["streams"]
+    for name in ("lens", "table", "refs"):
+        assert torch.equal(getattr(cache, name), getattr(held, name))
