@@ -522,9 +522,9 @@ __global__ __launch_bounds__(kBlock) void cache_compact_kernel(CacheState s, Cac
   const Plan plan(s);
   const int moves = plan.head[0], n_live = plan.head[1];
   const int32_t *holes = plan.per_page(0), *movers = plan.per_page(1), *moved_to = plan.per_page(2);
-  if (moves == 0) return;
   const int lane = threadIdx.x & (kWave - 1);
   const int waves = gridDim.x * (kBlock / kWave);
+  // also where nothing moves: what is wrong in the state is flagged all the same
   for (int r = blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave; r < s.R; r += waves) {
     const int len = s.lens[r];
     if (bad_length(s, len)) {

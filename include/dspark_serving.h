@@ -186,7 +186,8 @@ dspark_status dspark_cache_release(int R, int page, int max_pages, int n_pages, 
 /* Moves the pages in use to the numbers [0, n_live): the i-th used page from
  * n_live on goes to the i-th free one below, in both pools (NULL both: numbers
  * only).  n_live [1] int32; the pool's end is then free, so a caller may shrink
- * it or hand it on. */
+ * it or hand it on.  A table entry that names a free page from n_live on sets
+ * DSPARK_DEVERR_PAGE too and stays as it is. */
 dspark_status dspark_cache_compact(int R, int page, int max_pages, int n_pages,
                                    const int32_t *lens, const int32_t *table, const int32_t *refs,
                                    int32_t *lens_out, int32_t *table_out, int32_t *refs_out,

@@ -303,6 +303,32 @@ def test_bad_pages_are_not_followed():
     assert d.s["lens"].tolist() == [0, 0, 0] and (d.s["table"] == -1).all()
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("moves", [True, False])
+@pytest.mark.parametrize("wrong", [99, -7, 9, "length"])
+def test_compact_of_a_wrong_state(wrong, moves, in_place):
+    """Page numbers out of range, of a free page behind the live ones and a length out
+    of bounds are flagged and left as they are, whether or not a page moves."""
+    m, d, _ = both(4, 16, 4, 12, in_place)
+    new = [40, 20, 17, 5]  # pages 0..2, 3..4, 5..6, 7
+    m.reserve(new)
+    d.call(ds.cache_reserve, offsets(new), pools=True)
+    if moves:
+        m.cut(0, 0)
+        d.call(ds.cache_release, cu([0]))
+    d.check(m)
+    if wrong == "length":
+        d.s["lens"][1] = 65
+    else:
+        d.s["table"][1, 1] = wrong
+    assert d.call(ds.cache_compact, pools=True)["n_live"].item() == m.compact()
+    if wrong == "length":
+        m.lens[1] = 65
+    else:
+        m.table[1][1] = wrong
+    d.check(m, LENGTH if wrong == "length" else PAGE)
+
+
 def test_state_without_pools_and_compact_of_nothing():
     m, d, _ = both(4, 16, 4, 9, True)
     assert ds.cache_compact(d.s["lens"], d.s["table"], d.s["refs"], None, None, page=16,
