@@ -136,6 +136,9 @@ def _check_tokens(a, tokens, row_offset, n_rows):
     a.req(row_offset, "row_offset", I32, (R + 1,))
     if R < 1:
         raise ValueError(f"{a.where}: row_offset must have shape [R + 1]")
+    if R > n_rows:
+        raise ValueError(f"{a.where}: X has {n_rows} rows, {R} requests need as many rows at least "
+                         "(those behind row_offset[R] are not read)")
     if tokens is None:
         return R, 0
     w = _width(a, tokens, "tokens")
@@ -148,7 +151,8 @@ def logprobs(X, tokens=None, *, k=0, row_offset=None, temp=1.0, ws=None, stream=
     row_offset [R + 1] the verified batch's layout [R][w] (y of verify()), -1
     for no token.  Returns logp (None without tokens), entropy and stats
     [n_rows][2] = (m, S), top_ids and top_logp [n_rows][k] (None for k = 0).  Rows from
-    row_offset[R] on keep what `out` held (undefined without `out`)."""
+    row_offset[R] on keep what `out` held (undefined without `out`); X has R rows at
+    least, also where the requests' rows are fewer."""
     a = _RowArgs("logprobs")
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("logprobs: X must be a [n_rows][V] tensor")

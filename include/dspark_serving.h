@@ -63,6 +63,9 @@ extern "C" {
  *   row_offset [R + 1] int32 as written by dspark_schedule, or NULL; rows from
  *     row_offset[R] on are not read and their outputs stay as they were.  An
  *     end past n_rows sets DSPARK_DEVERR_LENGTH and is taken as n_rows.
+ *     1 <= R <= n_rows: n_rows is the rows' capacity, as dspark_verify's
+ *     rows_capacity, so a batch whose requests have fewer rows than there are
+ *     requests still comes in a buffer of R rows.
  *   0 <= k <= 64, k <= V
  * Outputs (fp32; top_ids int32): logp, entropy, stats, top_ids, top_logp; each
  *   of logp, entropy, stats may be NULL; top_ids and top_logp are given iff k > 0.

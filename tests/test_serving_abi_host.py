@@ -170,6 +170,10 @@ I32 = torch.int32
     (lambda: ds.logprobs(host(4, 8), host(3, dtype=I32)), ValueError, "tokens"),
     (lambda: ds.logprobs(host(4, 8), host(3, 2, dtype=I32), row_offset=host(3, dtype=I32)),
      ValueError, "tokens"),
+    (lambda: ds.logprobs(host(2, 8), row_offset=host(4, dtype=I32)), ValueError,
+     "3 requests need as many rows"),
+    (lambda: ds.logprobs_backward(host(2, 8), host(2, 2), host(2), row_offset=host(4, dtype=I32)),
+     ValueError, "3 requests need as many rows"),
     (lambda: ds.logprobs(host(4, 8)), ValueError, "not a GPU tensor"),
     (lambda: ds.logprobs_backward(host(4, 8), host(4, 2), g_logp=host(4)), ValueError, "needs tokens"),
     (lambda: ds.logprobs_backward(host(4, 8), host(4, 2), g_entropy=host(4)), ValueError, "entropy"),

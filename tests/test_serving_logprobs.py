@@ -458,3 +458,22 @@ def test_same_bits_every_time():
     for name in a:
         assert torch.equal(a[name], b[name])
     assert math.isfinite(float(a["logp"].sum()))
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_more_requests_than_rows_in_use(dt):
+    """Requests without rows, three of eight with some: the buffer has eight rows."""
+    off = torch.tensor([0, 0, 2, 2, 3, 3, 3, 5, 5], dtype=torch.int32, device="cuda")
+    X, g = make(8, 501, dt, 2)
+    X[5:] = float("nan")
+    y = torch.randint(0, 501, (8, 3), generator=g, device="cuda", dtype=torch.int32)
+    ws = ds.Workspace()
+    f = ds.logprobs(X, y, k=2, row_offset=off, ws=ws)
+    tok = flat_tokens(y, off, 5)
+    check(X[:5], tok, 2, 1.0, {k: v[:5] for k, v in f.items()})
+    gl = torch.randn(8, generator=g, device="cuda")
+    dx = ds.logprobs_backward(X, f["stats"], tokens=y, g_logp=gl, row_offset=off, ws=ws)
+    want, size = gradient(X[:5], tok, gl[:5], None, None, None, 1.0)
+    close(dx[:5], want, U * (200 * want.abs() + 25 * size) + 1e-30
+          + (2.0 ** -8 * want.abs() if dt == BF else 0))
+    assert ws.error_code() == 0
