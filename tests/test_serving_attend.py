@@ -139,6 +139,31 @@ def test_values(rows, lens, Hq, Hkv, D, page, dt):
     pools_equal(c)
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("rows,lens,Hq,Hkv,page,window", [
+    ([17, 4, 70], [300, 37, 70], 8, 2, 16, 0),
+    ([17, 4, 70], [300, 37, 1500], 4, 1, 128, 0),
+    ([20, 9, 65], [1111, 9, 431], 6, 2, 32, 0),
+    ([17, 4, 70], [600, 999, 70], 4, 1, 16, 45),
+    ([33, 0, 12], [2500, 5, 47], 16, 4, 256, 700),
+])
+def test_heads_of_256_in_blocks_of_64_rows(rows, lens, Hq, Hkv, page, window, dt):
+    """One step a buffer: odd and even numbers of steps, pages of one and of several
+    pieces of 64 bytes, units cut between workgroups, a window that ends inside a step;
+    unseen slots are NaN (Case), and so is a new row's key and value afterwards."""
+    c = Case(rows, lens, Hq, Hkv, 256, page, dt, seed=sum(rows) + page)
+    ws = ds.Workspace()
+    good = c.run(ws, window=window)
+    assert ws.error_code() == 0
+    c.check(good, window=window)
+    pools_equal(c)
+    c.kn[5], c.vn[5] = float("nan"), float("inf")
+    o = c.run(ws, window=window)
+    keep = torch.ones(c.n, dtype=torch.bool, device="cuda")
+    keep[5:rows[0]] = False
+    assert torch.equal(o["out"][keep], good["out"][keep]) and not o["out"][5].isfinite().any()
+
+
 @pytest.mark.parametrize("dt,window", [(BF, 1), (BF, 40), (F, 7), (F, 200), (BF, 5000), (F, 2 ** 31 - 1)])
 def test_window(dt, window):
     c = Case([1, 17, 6], [500, 300, 33], 8, 2, 64, 16, dt, seed=window)
