@@ -115,17 +115,26 @@ class Workspace:
             self._streams.add(id(stream))
         return self.buf
 
+    def _buffers(self, stream):
+        """Every buffer with its device current, and `stream` or, where that is None or
+        of another device, the device's current one."""
+        for buf in (*self.outgrown, self.buf):
+            on_gpu = buf is not None and buf.is_cuda
+            with torch.cuda.device(buf.device) if on_gpu else contextlib.nullcontext():
+                other = isinstance(stream, torch.cuda.Stream) and on_gpu and stream.device != buf.device
+                yield buf, _stream(None if other else stream)
+
     def error_code(self, stream=None):
         bits = 0
-        for buf in (*self.outgrown, self.buf):
-            st, code = A.dspark_device_error(buf, _stream(stream))
+        for buf, s in self._buffers(stream):
+            st, code = A.dspark_device_error(buf, s)
             _check(st, "dspark_device_error")
             bits |= code
         return bits
 
     def clear_error(self, stream=None):
-        for buf in (*self.outgrown, self.buf):
-            _check(A.dspark_clear_device_error(buf, _stream(stream)), "dspark_clear_device_error")
+        for buf, s in self._buffers(stream):
+            _check(A.dspark_clear_device_error(buf, s), "dspark_clear_device_error")
 
 
 def _empty(shape, dtype, dev):

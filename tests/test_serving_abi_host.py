@@ -251,3 +251,32 @@ def test_an_outgrown_workspace_is_kept_with_its_errors(monkeypatch):
     for n in (300, 200, 300):
         assert ws.get(n) is a and ws.get(n, device="meta") is b
     assert ws.outgrown == [a]
+
+
+def test_errors_are_read_behind_the_buffers_own_device(monkeypatch):
+    """With another device current: its stream is not the one that the calls ran on."""
+    now = ["cuda:0"]
+
+    class On:
+        def __init__(self, device):
+            self.device = str(device)
+
+        def __enter__(self):
+            now.append(self.device)
+
+        def __exit__(self, *e):
+            now.pop()
+
+    class Buffer:
+        is_cuda, device = True, torch.device("cuda:1")
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "stream of " + str(device or now[-1]))
+    monkeypatch.setattr(A, "dspark_device_error", lambda buf, stream: seen.append((now[-1], stream)) or (0, 4))
+    monkeypatch.setattr(A, "dspark_clear_device_error", lambda buf, stream: seen.append((now[-1], stream)) or 0)
+    ws = ds.Workspace()
+    ws.buf = Buffer()
+    assert ws.error_code() == 4
+    ws.clear_error()
+    assert seen == [("cuda:1", "stream of cuda:1")] * 2
