@@ -95,16 +95,13 @@ class Workspace:
 
     def get(self, nbytes, stream=None, device=None):
         dev = torch.device(device if device is not None else self.device)
-
-        def here(buf):
-            return buf.device.type == dev.type and dev.index in (None, buf.device.index)
-
-        if self.buf is None or self.buf.numel() < nbytes or not here(self.buf):
+        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != dev:
             held = [*self.outgrown, *([] if self.buf is None else [self.buf])]
-            mine = [b for b in held if here(b)]  # more than one device: each has its own
-            buf, streams = next((b for b in mine if b.numel() >= nbytes), None), set()
-            if buf is None:
-                size = max([nbytes, 256] + [2 * b.numel() for b in mine])
+            # more than one device: each has its own
+            mine = [b for b in held if b.device.type == dev.type and dev.index in (None, b.device.index)]
+            buf, streams = max(mine, key=torch.Tensor.numel, default=None), set()
+            if buf is None or buf.numel() < nbytes:
+                size = max(nbytes, 256, 0 if buf is None else 2 * buf.numel())
                 with _on_stream(stream):
                     buf = torch.zeros(size, dtype=torch.uint8, device=dev)
                 streams = {id(stream)}
