@@ -302,6 +302,8 @@ def cache_reserved_rows(ws, R):
     """The row offsets [R + 1] that the last cache_reserve() over `ws` left: those it was
     given, or zeros where it found no room.  A view of the workspace: a round that does
     not read `missing` gives it to cache_attend() and cache_commit() as row_offset."""
+    if ws.buf is None or ws.buf.numel() < 256 + 4 * (R + 1):
+        raise ValueError("cache_reserved_rows: cache_reserve() over this workspace comes first")
     return ws.buf[256:256 + 4 * (R + 1)].view(I32)
 
 

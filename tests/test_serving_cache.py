@@ -391,3 +391,26 @@ def test_captured_round_replays():
         for r in range(6):
             m.cut(r, m.lens[r] - new[r] + a[r] + 1)
         d.check(m)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_reserved_rows(in_place):
+    """The offsets given where there was room, zeros where there was none; a commit of
+    them then leaves everything as it was, whatever n_acc says."""
+    m, d, _ = both(3, 16, 4, 5, in_place)
+    with pytest.raises(ValueError, match="comes first"):
+        ds.cache_reserved_rows(d.ws, 3)
+    for new, first in (([20, 5, 1], 7), ([0, 1, 30], 0), ([1, 0, 0], 3)):
+        off = offsets(new, first=first)
+        missing = m.reserve(new)
+        assert d.call(ds.cache_reserve, off, pools=True)["missing"].item() == missing
+        d.check(m, NO_PAGES if missing else 0)
+        rows = ds.cache_reserved_rows(d.ws, 3)
+        assert rows.tolist() == ([0] * 4 if missing else off.tolist())
+        acc = [n - 1 for n in new]
+        d.call(ds.cache_commit, rows, cu(acc))
+        d.check(m, LENGTH if missing else 0)
+    off = cu([0, 2, 1, 9])  # decreasing
+    assert d.call(ds.cache_reserve, off, pools=True)["missing"].item() == -1
+    assert ds.cache_reserved_rows(d.ws, 3).tolist() == [0] * 4
+    d.check(m, LENGTH)
