@@ -29,9 +29,10 @@
 // of K and V); the products are 4 Hq D n operations a token, far below the matrix
 // rate for the rows of a round.  Measured (128 requests of 1 to 17 new rows over up to
 // 6000 tokens, 32 query and 8 key-value heads of 128, bf16, pages of 16; 1.60 GB):
-// layout and append 9 us, product 317 us (5.1 TB/s), join 16 us.  256 single tokens
+// layout and append 10 us, product 325 us (4.9 TB/s), join 17 us.  256 single tokens
 // over up to 4000 (2.10 GB): product 350 us (6.0 TB/s).  Three single fp32 tokens over
-// up to 120000 (92 MB): 4 + 22 + 7 us.
+// up to 120000 (92 MB): 4 + 22 + 8 us.  A prompt is bound by its operations: one of
+// 16000 rows takes 5.2 ms in the product, 403 TFLOP/s in bf16.
 #include <limits.h>
 
 #include "common.h"
@@ -726,8 +727,9 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_few_kernel(At
 // an operand of the matrix cores in lane order: waves 0 and 1 fetch the keys', 2 and
 // 3 the values', kDeep steps ahead in registers, and pass them on through two buffers
 // in LDS of kGroup steps each.  In lane order every LDS access is 1 KB in a row; one
-// barrier a buffer (two steps a barrier and one copy of the step's code: 317 us, one
-// and two copies 325).  64 rows: with 128, two tiles a wave, the results spill.
+// barrier a buffer (timed in turn, two steps a barrier and one copy of the step's code
+// took 317 us, one step and two copies 325).  64 rows: with 128, two tiles a wave, the results spill in the
+// 256 registers that two workgroups a unit leave (verified batch 1207 us).
 template <typename T, int D, bool kPast>
 __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(AttendParams p) {
   using St = Step<T>;
@@ -876,7 +878,7 @@ __global__ __launch_bounds__(kBlock, D <= 128 ? 2 : 1) void attend_many_kernel(A
 // The parts of the rows of units that were cut.  A row's part takes D / 4 lanes, so a
 // wave has 256 / D sides (two for D = 96), each with four or eight parts in flight.
 // Where a row has few parts every side takes a row of its own; where it may have
-// many, the workgroup's sides share one and are joined at the end (verified batch: 16
+// many, the workgroup's sides share one and are joined at the end (verified batch: 17
 // us, 24 with a workgroup a row throughout).
 template <typename T, int D>
 __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {

@@ -17,8 +17,8 @@
 // k = 64, 19 us against 68 for ranking all 1021 and 28 for sorting them.
 //
 // Bound: one read of the logits.  1152 rows of 151936 bf16 with 20 alternatives (350
-// MB): chunks 69 us (5.1 TB/s), join 16; 224 of 129277 fp32, mostly masked, 8
-// alternatives: 21 + 8 us.  A top k in every chunk, the plainer way, made the chunks
+// MB): chunks 66 us (5.3 TB/s), join 16; 224 of 129277 fp32, mostly masked, 8
+// alternatives: 22 + 8 us.  A top k in every chunk, the plainer way, made the chunks
 // 124 us.  One row: 3 + 8 us, all of it latency.
 #include <limits.h>
 
@@ -91,7 +91,8 @@ template <typename T> __device__ __forceinline__ u32x4 keep_first(u32x4 v, int n
 }
 
 // The row's request: the number of rho in [1, R) with row_offset[rho] <= row
-// (the offsets do not decrease), by ballots over loads that are all in flight.
+// (the offsets do not decrease), 64 of them a ballot.  All R are looked at, so a row
+// costs R / 64 dependent steps: two for the 128 requests of a round.
 __device__ __forceinline__ int request_of_row(const int32_t *row_offset, int R, int row) {
   const int lane = threadIdx.x & (kWave - 1);
   int lo = 0;
@@ -553,7 +554,7 @@ __device__ __forceinline__ u32x4 pack16(const float *x, float *) {
 // plus its own incoming gradients / T at the token and the alternatives.  Those
 // k + 1 columns are looked up in a bit set of the chunk's 16-byte pieces, so a
 // thread tests one bit per piece and almost never looks at the list.  Bound: the
-// bytes; 1088 rows of 151936 bf16 (661 MB read and written) take 139 us, 4.75 TB/s,
+// bytes; 1088 rows of 151936 bf16 (661 MB read and written) take 136 us, 4.85 TB/s,
 // where a plain copy reaches 5.1; 39 of 129277 fp32 with 10 alternatives 10 us.
 template <typename T, int VPT>
 __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(GradParams p) {
