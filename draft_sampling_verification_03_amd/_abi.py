@@ -11,6 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdspark.so")
 
 DSPARK_F32, DSPARK_BF16 = 0, 1
+DSPARK_ROTARY_HALF, DSPARK_ROTARY_INTERLEAVED = 0, 1
+(DSPARK_ROTARY_PLAIN, DSPARK_ROTARY_LINEAR, DSPARK_ROTARY_BASE, DSPARK_ROTARY_BY_TURNS) = range(4)
 (DSPARK_SCHED_OFF, DSPARK_SCHED_EARLY_STOP, DSPARK_SCHED_FULL_SEARCH, DSPARK_SCHED_ASYNC_TOPK,
  DSPARK_SCHED_THRESHOLD) = range(5)
 STATUS_NAMES = ["DSPARK_OK", "DSPARK_ERR_NULL", "DSPARK_ERR_SHAPE", "DSPARK_ERR_DTYPE",
@@ -85,6 +87,22 @@ def library():
         L.dspark_cache_attend_workspace.restype = _sz
         L.dspark_cache_attend.argtypes = ([_i] * 9 + [_f, _i, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
                                           _i64, _i64] + [_vp] * 6 + [_sz, _vp])
+        # dspark_tokens.h
+        _d = C.c_double
+        L.dspark_rotary_frequencies.argtypes = [_i, _d, _i] + [_d] * 4 + [_vp]
+        L.dspark_rotary_turns.argtypes = [_i, _vp, _vp]
+        L.dspark_rotary.argtypes = ([_i] * 7 + [_f, _vp, _vp, _i, _vp, _vp] + [_vp, _i64] * 4
+                                    + [_vp, _sz, _vp])
+        L.dspark_rotary_backward.argtypes = L.dspark_rotary.argtypes
+        L.dspark_cache_append.argtypes = ([_i] * 11 + [_f, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                                          _i64, _vp, _vp, _i64, _i64] + [_vp] * 4 + [_sz, _vp])
+        L.dspark_edit_logits.argtypes = ([_i, _i, _i64, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i]
+                                         + [_vp] * 3 + [_i, _vp, _vp, _i, _vp, _i64, _vp, _vp, _i64,
+                                                        _vp, _sz, _vp])
+        L.dspark_edit_logits_backward.argtypes = ([_i, _i, _i64, _i, _vp, _vp, _i64, _i, _vp, _vp, _i]
+                                                  + [_vp] * 3 + [_i, _vp, _i, _vp, _i64, _vp, _vp,
+                                                                 _i64, _vp, _sz, _vp])
+        L.dspark_history_append.argtypes = [_i] * 3 + [_vp] * 3 + [_i] + [_vp] * 5 + [_sz, _vp]
         L.dspark_device_error.argtypes = [_vp, _vp, _vp]
         L.dspark_clear_device_error.argtypes = [_vp, _vp]
         L.dspark_trace_enable.argtypes = [_i]
@@ -97,7 +115,9 @@ def library():
                      "dspark_trace_collect", "dspark_trace_entry", "dspark_logprobs",
                      "dspark_logprobs_backward", "dspark_cache_fork", "dspark_cache_reserve",
                      "dspark_cache_commit", "dspark_cache_release", "dspark_cache_compact",
-                     "dspark_cache_attend"):
+                     "dspark_cache_attend", "dspark_rotary_frequencies", "dspark_rotary_turns",
+                     "dspark_rotary", "dspark_rotary_backward", "dspark_cache_append",
+                     "dspark_edit_logits", "dspark_edit_logits_backward", "dspark_history_append"):
             getattr(L, name).restype = _i
         _lib = L
     return _lib
@@ -283,6 +303,82 @@ def dspark_cache_attend(R, rows_capacity, Hq, Hkv, D, page, max_pages, n_pages, 
                                          kv_stride, _p(k_pages), _p(v_pages), k_page_stride,
                                          v_page_stride, _p(table), _p(row_offset), _p(kv_len),
                                          _p(out), _p(lse), _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_rotary_frequencies(rot, base, scaling, factor, context, slow, fast, freqs):
+    """freqs: the address of rot / 2 doubles in host memory."""
+    return library().dspark_rotary_frequencies(rot, base, scaling, factor, context, slow, fast,
+                                               _p(freqs))
+
+
+def dspark_rotary_turns(n, freqs, turns):
+    """freqs, turns: addresses in host memory."""
+    return library().dspark_rotary_turns(n, _p(freqs), _p(turns))
+
+
+def _rotary(f, n_rows, Hq, Hkv, D, rot, layout, dt, magnitude, turns, positions, R, row_offset, kv_len,
+            q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, ws, ws_bytes, stream):
+    return f(n_rows, Hq, Hkv, D, rot, layout, dt, magnitude, _p(turns), _p(positions), R,
+             _p(row_offset), _p(kv_len), _p(q), q_stride, _p(k), k_stride, _p(q_out), q_out_stride,
+             _p(k_out), k_out_stride, _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_rotary(n_rows, Hq, Hkv, D, rot, layout, dt, magnitude, turns, positions, R, row_offset,
+                  kv_len, q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, ws,
+                  ws_bytes, stream):
+    return _rotary(library().dspark_rotary, n_rows, Hq, Hkv, D, rot, layout, dt, magnitude, turns,
+                   positions, R, row_offset, kv_len, q, q_stride, k, k_stride, q_out, q_out_stride,
+                   k_out, k_out_stride, ws, ws_bytes, stream)
+
+
+def dspark_rotary_backward(n_rows, Hq, Hkv, D, rot, layout, dt, magnitude, turns, positions, R,
+                           row_offset, kv_len, g_q, q_stride, g_k, k_stride, q_out, q_out_stride,
+                           k_out, k_out_stride, ws, ws_bytes, stream):
+    return _rotary(library().dspark_rotary_backward, n_rows, Hq, Hkv, D, rot, layout, dt, magnitude,
+                   turns, positions, R, row_offset, kv_len, g_q, q_stride, g_k, k_stride, q_out,
+                   q_out_stride, k_out, k_out_stride, ws, ws_bytes, stream)
+
+
+def dspark_cache_append(R, rows_capacity, Hq, Hkv, D, page, max_pages, n_pages, dt, rot, layout,
+                        magnitude, turns, positions, q, q_stride, q_out, q_out_stride, k_new, v_new,
+                        kv_stride, k_pages, v_pages, k_page_stride, v_page_stride, table, row_offset,
+                        kv_len, ws, ws_bytes, stream):
+    return library().dspark_cache_append(R, rows_capacity, Hq, Hkv, D, page, max_pages, n_pages, dt,
+                                         rot, layout, magnitude, _p(turns), _p(positions), _p(q),
+                                         q_stride, _p(q_out), q_out_stride, _p(k_new), _p(v_new),
+                                         kv_stride, _p(k_pages), _p(v_pages), k_page_stride,
+                                         v_page_stride, _p(table), _p(row_offset), _p(kv_len),
+                                         _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_edit_logits(n_rows, V, row_stride, dt, X, R, row_offset, history, hist_stride, hist_len,
+                       prompt_len, drafts, gamma, repetition, frequency, presence, n_bias, bias_ids,
+                       bias, n_masks, mask, mask_stride, mask_index, out, out_stride, ws, ws_bytes,
+                       stream):
+    return library().dspark_edit_logits(n_rows, V, row_stride, dt, _p(X), R, _p(row_offset),
+                                        _p(history), hist_stride, _p(hist_len), _p(prompt_len),
+                                        _p(drafts), gamma, _p(repetition), _p(frequency),
+                                        _p(presence), n_bias, _p(bias_ids), _p(bias), n_masks,
+                                        _p(mask), mask_stride, _p(mask_index), _p(out), out_stride,
+                                        _p(ws), ws_bytes, _s(stream))
+
+
+def dspark_edit_logits_backward(n_rows, V, row_stride, dt, X, G, g_stride, R, row_offset, history,
+                                hist_stride, hist_len, prompt_len, drafts, gamma, repetition, n_masks,
+                                mask, mask_stride, mask_index, dX, dx_stride, ws, ws_bytes, stream):
+    return library().dspark_edit_logits_backward(n_rows, V, row_stride, dt, _p(X), _p(G), g_stride, R,
+                                                 _p(row_offset), _p(history), hist_stride,
+                                                 _p(hist_len), _p(prompt_len), _p(drafts), gamma,
+                                                 _p(repetition), n_masks, _p(mask), mask_stride,
+                                                 _p(mask_index), _p(dX), dx_stride, _p(ws), ws_bytes,
+                                                 _s(stream))
+
+
+def dspark_history_append(R, width, n_tokens, tokens, n_acc, row_offset, hist_stride, history,
+                          hist_len, hist_len_out, prompt_len, ws, ws_bytes, stream):
+    return library().dspark_history_append(R, width, n_tokens, _p(tokens), _p(n_acc), _p(row_offset),
+                                           hist_stride, _p(history), _p(hist_len), _p(hist_len_out),
+                                           _p(prompt_len), _p(ws), ws_bytes, _s(stream))
 
 
 def dspark_device_error(ws, stream):

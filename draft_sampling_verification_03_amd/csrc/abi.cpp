@@ -9,6 +9,7 @@
 
 #include "../../include/dspark.h"
 #include "../../include/dspark_serving.h"
+#include "../../include/dspark_tokens.h"
 #include "kernels.h"
 
 using namespace dspark;
@@ -21,6 +22,7 @@ static __device__ __align__(256) unsigned char scratch[DSPARK_NOALLOC_SCRATCH_BY
 
 namespace {
 
+constexpr long double kTwoPi = 6.283185307179586476925286766559L;
 constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
 void *g_scratch_ptr[kMaxDevices];  // device address of `scratch`, per device (nullptr: not yet)
@@ -587,6 +589,264 @@ dspark_status dspark_cache_attend(int R, int rows_capacity, int Hq, int Hkv, int
   L.v_page_stride = v_page_stride; L.k_pages = k_pages; L.v_pages = v_pages; L.table = table;
   L.row_offset = row_offset; L.kv_len = kv_len; L.out = out; L.lse = lse;
   return from_hip(launch_attend(L, stream));
+}
+
+// -------------------------------------------------------- dspark_tokens.h
+dspark_status dspark_rotary_frequencies(int rot, double base, dspark_rotary_scaling scaling,
+                                        double factor, double context, double slow, double fast,
+                                        double *freqs) {
+  if (scaling < DSPARK_ROTARY_PLAIN || scaling > DSPARK_ROTARY_BY_TURNS) return DSPARK_ERR_MODE;
+  if (rot < (scaling == DSPARK_ROTARY_BASE ? 4 : 2) || rot > 256 || rot % 2 != 0)
+    return DSPARK_ERR_SHAPE;
+  if (!(base > 1.0) || !isfinite(base)) return DSPARK_ERR_VALUE;
+  if (scaling != DSPARK_ROTARY_PLAIN && (!(factor >= 1.0) || !isfinite(factor)))
+    return DSPARK_ERR_VALUE;
+  if (scaling == DSPARK_ROTARY_BY_TURNS &&
+      (!(context > 0.0) || !isfinite(context) || !(slow > 0.0) || !(fast > slow) || !isfinite(fast)))
+    return DSPARK_ERR_VALUE;
+  if (!freqs) return DSPARK_ERR_NULL;
+  if (scaling == DSPARK_ROTARY_BASE) base *= pow(factor, (double)rot / (rot - 2));
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot);
+    if (scaling == DSPARK_ROTARY_LINEAR) f /= factor;
+    if (scaling == DSPARK_ROTARY_BY_TURNS) {
+      const double w = (context * f / (double)kTwoPi - slow) / (fast - slow);
+      const double keep = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+      f *= keep + (1.0 - keep) / factor;
+    }
+    freqs[i] = f;
+  }
+  return DSPARK_OK;
+}
+
+dspark_status dspark_rotary_turns(int n, const double *freqs, uint64_t *turns) {
+  if (n < 1 || n > 128) return DSPARK_ERR_SHAPE;
+  if (!freqs || !turns) return DSPARK_ERR_NULL;
+  for (int i = 0; i < n; ++i)
+    if (!(fabs(freqs[i]) < 1048576.0)) return DSPARK_ERR_VALUE;
+  for (int i = 0; i < n; ++i) {
+    // in 64 bits of fraction, so that the last bit counts below 2^-32 turns at any position;
+    // the part of a turn within [-1/2, 1/2], in units of 2^-64 (2^63 is the angle of -2^63)
+    const long double t = freqs[i] / kTwoPi;
+    const long double part = nearbyintl((t - nearbyintl(t)) * 18446744073709551616.0L);
+    turns[i] = part >= 9223372036854775808.0L ? (uint64_t)1 << 63 : (uint64_t)(int64_t)part;
+  }
+  return DSPARK_OK;
+}
+
+static bool bad_layout(dspark_rotary_layout layout) {
+  return layout != DSPARK_ROTARY_HALF && layout != DSPARK_ROTARY_INTERLEAVED;
+}
+
+static dspark_status rotary(bool back, int n_rows, int Hq, int Hkv, int D, int rot,
+                            dspark_rotary_layout layout, dspark_dtype dt, float magnitude,
+                            const uint64_t *turns, const int32_t *positions, int R,
+                            const int32_t *row_offset, const int32_t *kv_len, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride, void *q_out,
+                            int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *ws,
+                            size_t ws_bytes, hipStream_t stream) {
+  if (dt != DSPARK_F32 && dt != DSPARK_BF16) return DSPARK_ERR_DTYPE;
+  if (bad_layout(layout)) return DSPARK_ERR_MODE;
+  if (n_rows < 1 || n_rows > (1 << 22) || Hq < 1 || Hq > 1024 || Hkv < 0 || Hkv > 1024 || D < 8 ||
+      D > 256 || D % 8 != 0 || rot < 2 || rot > D || rot % 2 != 0)
+    return DSPARK_ERR_SHAPE;
+  if (row_offset != nullptr && (R < 1 || R > (1 << 22))) return DSPARK_ERR_SHAPE;
+  const int per = dt == DSPARK_BF16 ? 8 : 4;
+  if (q_stride < (int64_t)Hq * D || q_stride % per != 0 || q_out_stride < (int64_t)Hq * D ||
+      q_out_stride % per != 0)
+    return DSPARK_ERR_SHAPE;
+  if (Hkv > 0 && (k_stride < (int64_t)Hkv * D || k_stride % per != 0 ||
+                  k_out_stride < (int64_t)Hkv * D || k_out_stride % per != 0))
+    return DSPARK_ERR_SHAPE;
+  if (!isfinite(magnitude) || magnitude == 0.0f) return DSPARK_ERR_VALUE;
+  if (!turns || !q || !q_out || !ws || (Hkv > 0) != (k != nullptr) || (Hkv > 0) != (k_out != nullptr))
+    return DSPARK_ERR_NULL;
+  if ((q == q_out && q_stride != q_out_stride) || (Hkv > 0 && k == k_out && k_stride != k_out_stride))
+    return DSPARK_ERR_VALUE;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) || !aligned16(ws) ||
+      ((uintptr_t)turns & 7u) != 0)
+    return DSPARK_ERR_ALIGN;
+  if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  RotaryLaunch L{};
+  L.n_rows = n_rows; L.Hq = Hq; L.Hkv = Hkv; L.D = D; L.rot = rot; L.R = R;
+  L.interleaved = layout == DSPARK_ROTARY_INTERLEAVED; L.bf16 = dt == DSPARK_BF16; L.back = back;
+  L.magnitude = magnitude; L.turns = turns; L.positions = positions; L.row_offset = row_offset;
+  L.kv_len = kv_len; L.q = q; L.k = k; L.q_stride = q_stride; L.k_stride = k_stride; L.q_out = q_out;
+  L.k_out = k_out; L.qo_stride = q_out_stride; L.ko_stride = k_out_stride; L.err = (int32_t *)ws;
+  return from_hip(launch_rotary(L, stream));
+}
+
+dspark_status dspark_rotary(int n_rows, int Hq, int Hkv, int D, int rot, dspark_rotary_layout layout,
+                            dspark_dtype dt, float magnitude, const uint64_t *turns,
+                            const int32_t *positions, int R, const int32_t *row_offset,
+                            const int32_t *kv_len, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, void *q_out, int64_t q_out_stride, void *k_out,
+                            int64_t k_out_stride, void *ws, size_t ws_bytes, hipStream_t stream) {
+  return rotary(false, n_rows, Hq, Hkv, D, rot, layout, dt, magnitude, turns, positions, R, row_offset,
+                kv_len, q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, ws,
+                ws_bytes, stream);
+}
+
+dspark_status dspark_rotary_backward(int n_rows, int Hq, int Hkv, int D, int rot,
+                                     dspark_rotary_layout layout, dspark_dtype dt, float magnitude,
+                                     const uint64_t *turns, const int32_t *positions, int R,
+                                     const int32_t *row_offset, const int32_t *kv_len,
+                                     const void *g_q, int64_t q_stride, const void *g_k,
+                                     int64_t k_stride, void *q_out, int64_t q_out_stride,
+                                     void *k_out, int64_t k_out_stride, void *ws, size_t ws_bytes,
+                                     hipStream_t stream) {
+  return rotary(true, n_rows, Hq, Hkv, D, rot, layout, dt, magnitude, turns, positions, R, row_offset,
+                kv_len, g_q, q_stride, g_k, k_stride, q_out, q_out_stride, k_out, k_out_stride, ws,
+                ws_bytes, stream);
+}
+
+dspark_status dspark_cache_append(int R, int rows_capacity, int Hq, int Hkv, int D, int page,
+                                  int max_pages, int n_pages, dspark_dtype dt, int rot,
+                                  dspark_rotary_layout layout, float magnitude,
+                                  const uint64_t *turns, const int32_t *positions, const void *q,
+                                  int64_t q_stride, void *q_out, int64_t q_out_stride,
+                                  const void *k_new, const void *v_new, int64_t kv_stride,
+                                  void *k_pages, void *v_pages, int64_t k_page_stride,
+                                  int64_t v_page_stride, const int32_t *table,
+                                  const int32_t *row_offset, const int32_t *kv_len, void *ws,
+                                  size_t ws_bytes, hipStream_t stream) {
+  if (dt != DSPARK_F32 && dt != DSPARK_BF16) return DSPARK_ERR_DTYPE;
+  if (bad_layout(layout)) return DSPARK_ERR_MODE;
+  if ((q == nullptr) != (q_out == nullptr)) return DSPARK_ERR_NULL;
+  if (q == nullptr) Hq = Hkv;
+  if (bad_attend_shape(R, rows_capacity, Hq, Hkv, D) || bad_cache_shape(R, page, max_pages, n_pages))
+    return DSPARK_ERR_SHAPE;
+  if (row_offset == nullptr && rows_capacity != R) return DSPARK_ERR_SHAPE;
+  if (rot < 0 || rot > D || rot % 2 != 0) return DSPARK_ERR_SHAPE;
+  if (rot > 0 && (!isfinite(magnitude) || magnitude == 0.0f)) return DSPARK_ERR_VALUE;
+  if (!k_new || !v_new || !k_pages || !v_pages || !table || !kv_len || !ws ||
+      (rot > 0) != (turns != nullptr))
+    return DSPARK_ERR_NULL;
+  const int per = dt == DSPARK_BF16 ? 8 : 4;
+  const int64_t page_elems = (int64_t)Hkv * page * D;
+  if (kv_stride < (int64_t)Hkv * D || kv_stride % per != 0 || k_page_stride < page_elems ||
+      v_page_stride < page_elems || k_page_stride % per != 0 || v_page_stride % per != 0)
+    return DSPARK_ERR_SHAPE;
+  if (q != nullptr && (q_stride < (int64_t)Hq * D || q_stride % per != 0 ||
+                       q_out_stride < (int64_t)Hq * D || q_out_stride % per != 0))
+    return DSPARK_ERR_SHAPE;
+  if (q != nullptr && q == q_out && q_stride != q_out_stride) return DSPARK_ERR_VALUE;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k_new) || !aligned16(v_new) ||
+      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(ws) || ((uintptr_t)turns & 7u) != 0)
+    return DSPARK_ERR_ALIGN;
+  if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  AppendLaunch L{};
+  L.R = R; L.rows_capacity = rows_capacity; L.Hq = q != nullptr ? Hq : 0; L.Hkv = Hkv; L.D = D;
+  L.page_shift = shift_of(page); L.max_pages = max_pages; L.n_pages = n_pages; L.rot = rot;
+  L.interleaved = layout == DSPARK_ROTARY_INTERLEAVED; L.bf16 = dt == DSPARK_BF16;
+  L.magnitude = magnitude; L.turns = turns; L.positions = positions; L.table = table;
+  L.row_offset = row_offset; L.kv_len = kv_len; L.q = q; L.k_new = k_new; L.v_new = v_new;
+  L.q_stride = q_stride; L.qo_stride = q_out_stride; L.kv_stride = kv_stride;
+  L.k_page_stride = k_page_stride; L.v_page_stride = v_page_stride; L.q_out = q_out;
+  L.k_pages = k_pages; L.v_pages = v_pages; L.err = (int32_t *)ws;
+  return from_hip(launch_append(L, stream));
+}
+
+// What both directions of the edits share; L holds the arguments.
+static dspark_status check_edit(const EditLaunch &L, dspark_dtype dt, const void *ws, size_t ws_bytes) {
+  constexpr int kLongest = (1 << 20) - 1;
+  const int per = dt == DSPARK_BF16 ? 8 : 4;
+  auto bad_stride = [&](int64_t s) { return s < L.V || s % per != 0; };
+  if (dt != DSPARK_F32 && dt != DSPARK_BF16) return DSPARK_ERR_DTYPE;
+  if (L.n_rows < 1 || L.n_rows > (1 << 22) || L.V < 1 || L.V > 262144 || L.R < 1 || L.R > L.n_rows ||
+      (L.row_offset == nullptr && L.R != L.n_rows))
+    return DSPARK_ERR_SHAPE;
+  if (bad_stride(L.out_stride) || (L.X != nullptr && bad_stride(L.row_stride)) ||
+      (L.G != nullptr && bad_stride(L.g_stride)))
+    return DSPARK_ERR_SHAPE;
+  if (L.history != nullptr && (L.hist_stride < 1 || L.hist_stride > kLongest)) return DSPARK_ERR_SHAPE;
+  if (L.gamma < 0 || L.gamma > kLongest || (L.drafts != nullptr && L.gamma < 1) || L.n_bias < 0 ||
+      L.n_bias > 1023)
+    return DSPARK_ERR_SHAPE;
+  if (L.mask != nullptr &&
+      (L.n_masks < 1 || L.n_masks > (1 << 22) || L.mask_stride < (L.V + 31) / 32 ||
+       (L.mask_index == nullptr && L.n_masks < L.n_rows)))
+    return DSPARK_ERR_SHAPE;
+  if (!L.out || !ws || (L.history != nullptr && !L.hist_len) || (L.prompt_len != nullptr && !L.history) ||
+      (L.gamma > 0 && !L.drafts) || (L.n_bias > 0 && (!L.bias_ids || !L.bias)) ||
+      (L.mask_index != nullptr && !L.mask))
+    return DSPARK_ERR_NULL;
+  if (!aligned16(L.X) || !aligned16(L.G) || !aligned16(L.out) || !aligned16(ws)) return DSPARK_ERR_ALIGN;
+  auto aligned4 = [](const void *p) { return ((uintptr_t)p & 3u) == 0; };
+  if (!aligned4(L.row_offset) || !aligned4(L.history) || !aligned4(L.hist_len) ||
+      !aligned4(L.prompt_len) || !aligned4(L.drafts) || !aligned4(L.bias_ids) || !aligned4(L.bias) ||
+      !aligned4(L.mask) || !aligned4(L.mask_index) || !aligned4(L.repetition) ||
+      !aligned4(L.frequency) || !aligned4(L.presence))
+    return DSPARK_ERR_ALIGN;
+  if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_edit_logits(int n_rows, int V, int64_t row_stride, dspark_dtype dt,
+                                 const void *X, int R, const int32_t *row_offset,
+                                 const int32_t *history, int hist_stride, const int32_t *hist_len,
+                                 const int32_t *prompt_len, const int32_t *drafts, int gamma,
+                                 const float *repetition, const float *frequency,
+                                 const float *presence, int n_bias, const int32_t *bias_ids,
+                                 const float *bias, int n_masks, const uint32_t *mask,
+                                 int64_t mask_stride, const int32_t *mask_index, void *out,
+                                 int64_t out_stride, void *ws, size_t ws_bytes,
+                                 hipStream_t stream) {
+  if (!X) return DSPARK_ERR_NULL;
+  EditLaunch L{};
+  L.n_rows = n_rows; L.V = V; L.R = R; L.hist_stride = hist_stride; L.gamma = gamma;
+  L.n_bias = n_bias; L.n_masks = n_masks; L.row_stride = row_stride; L.out_stride = out_stride;
+  L.mask_stride = mask_stride; L.bf16 = dt == DSPARK_BF16; L.X = X; L.row_offset = row_offset;
+  L.history = history; L.hist_len = hist_len; L.prompt_len = prompt_len; L.drafts = drafts;
+  L.bias_ids = bias_ids; L.mask_index = mask_index; L.repetition = repetition;
+  L.frequency = frequency; L.presence = presence; L.bias = bias; L.mask = mask; L.out = out;
+  L.err = (int32_t *)ws;
+  dspark_status s = check_edit(L, dt, ws, ws_bytes);
+  if (s != DSPARK_OK) return s;
+  if (out == X && out_stride != row_stride) return DSPARK_ERR_VALUE;
+  return from_hip(launch_edit(L, stream));
+}
+
+dspark_status dspark_edit_logits_backward(int n_rows, int V, int64_t row_stride, dspark_dtype dt,
+                                          const void *X, const void *G, int64_t g_stride, int R,
+                                          const int32_t *row_offset, const int32_t *history,
+                                          int hist_stride, const int32_t *hist_len,
+                                          const int32_t *prompt_len, const int32_t *drafts,
+                                          int gamma, const float *repetition, int n_masks,
+                                          const uint32_t *mask, int64_t mask_stride,
+                                          const int32_t *mask_index, void *dX, int64_t dx_stride,
+                                          void *ws, size_t ws_bytes, hipStream_t stream) {
+  if (!G || (repetition != nullptr && !X)) return DSPARK_ERR_NULL;
+  EditLaunch L{};
+  L.n_rows = n_rows; L.V = V; L.R = R; L.hist_stride = hist_stride; L.gamma = gamma;
+  L.n_masks = n_masks; L.row_stride = row_stride; L.g_stride = g_stride; L.out_stride = dx_stride;
+  L.mask_stride = mask_stride; L.bf16 = dt == DSPARK_BF16; L.X = X; L.G = G;
+  L.row_offset = row_offset; L.history = history; L.hist_len = hist_len; L.prompt_len = prompt_len;
+  L.drafts = drafts; L.mask_index = mask_index; L.repetition = repetition; L.mask = mask;
+  L.out = dX; L.err = (int32_t *)ws;
+  dspark_status s = check_edit(L, dt, ws, ws_bytes);
+  if (s != DSPARK_OK) return s;
+  if ((dX == G && dx_stride != g_stride) || dX == X) return DSPARK_ERR_VALUE;
+  return from_hip(launch_edit(L, stream));
+}
+
+dspark_status dspark_history_append(int R, int width, int n_tokens, const int32_t *tokens,
+                                    const int32_t *n_acc, const int32_t *row_offset,
+                                    int hist_stride, int32_t *history, const int32_t *hist_len,
+                                    int32_t *hist_len_out, int32_t *prompt_len, void *ws,
+                                    size_t ws_bytes, hipStream_t stream) {
+  constexpr int kLongest = (1 << 20) - 1;
+  if (R < 1 || R > (1 << 20) || hist_stride < 1 || hist_stride > kLongest) return DSPARK_ERR_SHAPE;
+  if (row_offset != nullptr ? n_tokens < 0 : width < 1 || width > kLongest) return DSPARK_ERR_SHAPE;
+  if (row_offset != nullptr && n_acc != nullptr) return DSPARK_ERR_VALUE;
+  if (!tokens || !history || !hist_len || !hist_len_out || !ws) return DSPARK_ERR_NULL;
+  if (!aligned16(ws)) return DSPARK_ERR_ALIGN;
+  if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  HistoryLaunch L{};
+  L.R = R; L.width = width; L.n_tokens = n_tokens; L.hist_stride = hist_stride; L.tokens = tokens;
+  L.n_acc = n_acc; L.row_offset = row_offset; L.hist_len = hist_len; L.history = history;
+  L.hist_len_out = hist_len_out; L.prompt_len = prompt_len; L.err = (int32_t *)ws;
+  return from_hip(launch_history_append(L, stream));
 }
 
 size_t dspark_tv_overlap_workspace(int n_rows, int V) {

@@ -163,6 +163,54 @@ struct AttendLaunch {
   void *scratch;
 };
 
+struct RotaryLaunch {
+  int n_rows, Hq, Hkv, D, rot, R;
+  bool interleaved, bf16, back;
+  float magnitude;
+  const uint64_t *turns;
+  const int32_t *positions, *row_offset, *kv_len;  // each or NULL
+  const void *q, *k;
+  int64_t q_stride, k_stride;
+  void *q_out, *k_out;
+  int64_t qo_stride, ko_stride;
+  int32_t *err;
+};
+
+struct AppendLaunch {
+  int R, rows_capacity, Hq, Hkv, D, page_shift, max_pages, n_pages, rot;  // Hq 0: no queries
+  bool interleaved, bf16;
+  float magnitude;
+  const uint64_t *turns;
+  const int32_t *positions, *table, *row_offset, *kv_len;
+  const void *q, *k_new, *v_new;
+  int64_t q_stride, qo_stride, kv_stride, k_page_stride, v_page_stride;
+  void *q_out, *k_pages, *v_pages;
+  int32_t *err;
+};
+
+struct EditLaunch {
+  int n_rows, V, R, hist_stride, gamma, n_bias, n_masks;
+  int64_t row_stride, g_stride, out_stride, mask_stride;
+  bool bf16;
+  const void *X, *G;  // G: the gradient that comes back, NULL in the forward pass
+  const int32_t *row_offset, *history, *hist_len, *prompt_len, *drafts, *bias_ids, *mask_index;
+  const float *repetition, *frequency, *presence, *bias;
+  const uint32_t *mask;
+  void *out;
+  int32_t *err;
+};
+
+struct HistoryLaunch {
+  int R, width, n_tokens, hist_stride;
+  const int32_t *tokens, *n_acc, *row_offset, *hist_len;
+  int32_t *history, *hist_len_out, *prompt_len;
+  int32_t *err;
+};
+
+hipError_t launch_rotary(const RotaryLaunch &L, hipStream_t stream);
+hipError_t launch_append(const AppendLaunch &L, hipStream_t stream);
+hipError_t launch_edit(const EditLaunch &L, hipStream_t stream);
+hipError_t launch_history_append(const HistoryLaunch &L, hipStream_t stream);
 hipError_t launch_logprobs(const LogprobsLaunch &L, hipStream_t stream);
 hipError_t launch_logprobs_backward(const LogprobsGradLaunch &L, hipStream_t stream);
 hipError_t launch_cache_fork(const CacheState &S, int n, const int32_t *src, const int32_t *dst,

@@ -435,11 +435,31 @@ class PagedCache:
                       ws=self.ws, stream=stream, out=dict(self._state(), missing=self.missing))
         return self.missing
 
-    def attend(self, layer, q, k_new, v_new, *, scale=None, window=0, stream=None, out=None):
-        """The reserved rows' keys and values enter layer `layer`, and their
-        queries attend over it."""
+    def append(self, layer, q, k_new, v_new, *, rotary=None, positions=None, stream=None, out=None):
+        """The reserved rows' keys and values enter layer `layer`, keys and queries rotated
+        by the plan `rotary` (None: as they are).  Returns the rotated queries, for attend()
+        with k_new = v_new = None; q may be None."""
+        if self.row_offset is None:
+            raise ValueError("PagedCache.append: reserve() comes first")
+        from .tokens import cache_append
+        return cache_append(q, k_new, v_new, self.k[:, layer], self.v[:, layer], self.table, self.lens,
+                            plan=rotary, row_offset=self.row_offset, positions=positions,
+                            ws=self.attend_ws, stream=stream, out=out)
+
+    def attend(self, layer, q, k_new=None, v_new=None, *, rotary=None, positions=None, scale=None,
+               window=0, stream=None, out=None):
+        """The reserved rows' keys and values enter layer `layer` (None: append() put them
+        there), and their queries attend over it.  With `rotary`, a RotaryPlan, queries
+        and keys are rotated first, as append() does it."""
         if self.row_offset is None:
             raise ValueError("PagedCache.attend: reserve() comes first")
+        if rotary is not None:
+            if k_new is None:
+                raise ValueError("PagedCache.attend: rotary needs k_new and v_new")
+            q = self.append(layer, q, k_new, v_new, rotary=rotary, positions=positions, stream=stream)
+            k_new = v_new = None
+        elif positions is not None:
+            raise ValueError("PagedCache.attend: positions are for rotary")
         return cache_attend(q, self.k[:, layer], self.v[:, layer], self.table, self.lens,
                             row_offset=self.row_offset, k_new=k_new, v_new=v_new, scale=scale,
                             window=window, ws=self.attend_ws, stream=stream, out=out)
