@@ -837,8 +837,8 @@ dspark_status dspark_history_append(int R, int width, int n_tokens, const int32_
                                     size_t ws_bytes, hipStream_t stream) {
   constexpr int kLongest = (1 << 20) - 1;
   if (R < 1 || R > (1 << 20) || hist_stride < 1 || hist_stride > kLongest) return DSPARK_ERR_SHAPE;
-  if (row_offset != nullptr ? n_tokens < 0 : width < 1 || width > kLongest) return DSPARK_ERR_SHAPE;
-  if (row_offset != nullptr && n_acc != nullptr) return DSPARK_ERR_VALUE;
+  const bool flat = row_offset != nullptr && n_acc == nullptr;
+  if (flat ? n_tokens < 0 : width < 1 || width > kLongest) return DSPARK_ERR_SHAPE;
   if (!tokens || !history || !hist_len || !hist_len_out || !ws) return DSPARK_ERR_NULL;
   if (!aligned16(ws)) return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;

@@ -252,15 +252,21 @@ __global__ __launch_bounds__(kBlock) void history_append_kernel(HistoryLaunch L)
   const int len = L.hist_len[r];
   int64_t from = (int64_t)r * L.width, n = L.width;
   bool bad = len < 0 || len > L.hist_stride;
-  if (L.row_offset != nullptr) {
-    const int a = L.row_offset[r], b = L.row_offset[r + 1];
-    bad = bad || a < 0 || b < a || b > L.n_tokens;
-    from = a;
-    n = (int64_t)b - a;
-  } else if (L.n_acc != nullptr) {
+  if (L.n_acc != nullptr) {
     const int acc = L.n_acc[r];
     bad = bad || acc < -1 || acc >= L.width;
     n = (int64_t)acc + 1;
+  }
+  if (L.row_offset != nullptr) {
+    const int a = L.row_offset[r], b = L.row_offset[r + 1];
+    bad = bad || a < 0 || b < a;
+    if (L.n_acc != nullptr) {  // the rows that the round has
+      bad = bad || n > (int64_t)b - a;
+    } else {
+      bad = bad || b > L.n_tokens;
+      from = a;
+      n = (int64_t)b - a;
+    }
   }
   bad = bad || len + n > L.hist_stride;
   __syncthreads();  // every thread has the length before it changes

@@ -23,7 +23,10 @@ from integer counts in float64 and rounded once to float32.
 With a paged cache (serving.PagedCache) the loop keeps the target's keys and
 values in step: before the target rows it reserves pages for every scheduled
 row, and after the verification it gives back what the rejected rows held.
-With `logprobs` it returns what a server sends along with the tokens.
+With `logprobs` it returns what a server sends along with the tokens.  With
+`edits` and a `token_history` (tokens.TokenHistory) the target's rows are edited by what
+each request has said so far, the drafts before a row included, so the verification is
+exact for the edited law; the emitted tokens then join the history.
 """
 import contextlib
 
@@ -31,7 +34,7 @@ import numpy as np
 import torch
 
 from . import _abi as A
-from . import api, serving
+from . import api, serving, tokens
 
 
 class AcceptanceHistory:
@@ -94,7 +97,7 @@ def _current(stream, device):
 
 def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, threshold=0.0,
            conf_of_round=None, history=None, temp=1.0, seed=0, first_round=0, stream=None,
-           cache=None, logprobs=None):
+           cache=None, logprobs=None, token_history=None, edits=None):
     """Run `rounds` rounds for R requests.
 
     x0            [R] int32 anchors of the first round (host or device)
@@ -114,6 +117,11 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
                   cache before the next round.  Too few pages raise RuntimeError.
     logprobs      number of alternatives (0: none) to report beside the log
                   probability and entropy of every emitted token
+    token_history tokens.TokenHistory that holds every token up to the anchors (included);
+                  the emitted tokens join it
+    edits         arguments of tokens.edit_logits for the target's rows (repetition,
+                  bias_ids, ...), or a callable (prev, the rows' previous tokens) -> such
+                  arguments (a grammar's mask and mask_index of the round's rows)
     stream        a stream (or its address) to run on, behind what the current one
                   has queued; it is the current one while the callables run
 
@@ -127,11 +135,13 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
     top_ids and top_logp with a last dimension of that number."""
     with _current(stream, W1.device) as stream:
         return _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold,
-                       conf_of_round, history, temp, seed, first_round, stream, cache, logprobs)
+                       conf_of_round, history, temp, seed, first_round, stream, cache, logprobs,
+                       token_history, edits)
 
 
 def _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold, conf_of_round, history,
-            temp, seed, first_round, stream, cache, logprobs):
+            temp, seed, first_round, stream, cache, logprobs, token_history, edits):
+    ws_e = api.Workspace() if token_history is None else token_history.ws
     ws_d, ws_s, ws_v, ws_l = api.Workspace(), api.Workspace(), api.Workspace(), api.Workspace()
     anchors = torch.as_tensor(np.asarray(x0, dtype=np.int32) if not torch.is_tensor(x0) else x0)
     anchors = anchors.to(W1.device, dtype=torch.int32).contiguous()
@@ -178,10 +188,17 @@ def _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold, c
             P = target_rows(prev, cache)
         else:
             P = target_rows(prev)
+        if edits is not None:
+            how = dict(edits(prev) if callable(edits) else edits, row_offset=s["row_offset"],
+                       drafts=d["x"], ws=ws_e, stream=stream)
+            P = (tokens.edit_logits(P, **how) if token_history is None
+                 else token_history.edit(P, **how))
         v = api.verify(s["ell"], s["row_offset"], P, U, W1, W2, anchors, d["x"], d["q_stats"],
                        d["q_x"], temp=temp, seed=seed, round=t, ws=ws_v, stream=stream)
         if cache is not None:
             cache.commit(v["n_acc"], stream=stream)
+        if token_history is not None:
+            token_history.append(v["y"], v["n_acc"], stream=stream)
         lp = None
         if logprobs is not None:
             lp = serving.logprobs(P, v["y"], k=logprobs, row_offset=s["row_offset"], temp=temp,
@@ -219,5 +236,7 @@ def _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold, c
         errs += (cache.error_code(stream),)
     if logprobs is not None:
         errs += (ws_l.error_code(stream),)
+    if token_history is not None or edits is not None:
+        errs += (ws_e.error_code(stream),)
     out["device_errors"] = errs
     return out

@@ -284,7 +284,9 @@ def history_append(history, hist_len, tokens, *, n_acc=None, row_offset=None, pr
                    stream=None, out=None):
     """Request r's new tokens join history [R][capacity] behind its hist_len [R]: the first
     n_acc[r] + 1 of tokens [R][width] (the y of verify(); all of them without n_acc), or
-    with row_offset [R + 1] its part of a flat list.  prompt_len [R], if given, becomes the
+    with row_offset [R + 1] alone its part of a flat list.  With both, row_offset is
+    cache_reserved_rows(): a request with fewer than n_acc + 1 rows stays as it is (a round
+    that found no pages changes nothing).  prompt_len [R], if given, becomes the
     new length where a request got tokens (a prompt's).  Returns the lengths (`out`, which
     may be hist_len)."""
     a = _RowArgs("history_append")
@@ -295,14 +297,10 @@ def history_append(history, hist_len, tokens, *, n_acc=None, row_offset=None, pr
     a.req(history, "history", I32, (R, cap))
     a.req(hist_len, "hist_len", I32, (R,))
     w = _width(a, tokens, "tokens")
-    if row_offset is not None:
-        if n_acc is not None:
-            raise ValueError("history_append: n_acc or row_offset, not both")
-        a.req(tokens, "tokens", I32, (w,))
-        a.req(row_offset, "row_offset", I32, (R + 1,))
-    else:
-        a.req(tokens, "tokens", I32, (R, w))
-        a.req(n_acc, "n_acc", I32, (R,), optional=True)
+    flat = row_offset is not None and n_acc is None
+    a.req(tokens, "tokens", I32, (w,) if flat else (R, w))
+    a.req(n_acc, "n_acc", I32, (R,), optional=True)
+    a.req(row_offset, "row_offset", I32, (R + 1,), optional=True)
     a.req(prompt_len, "prompt_len", I32, (R,), optional=True)
     index, dev = a.gpu(), history.device
     with _on_stream(stream):
@@ -339,14 +337,16 @@ class TokenHistory:
         history_append(self.tokens, self.lens, tokens, row_offset=row_offset,
                        prompt_len=self.prompt_lens, ws=self.ws, stream=stream, out=self.lens)
 
-    def append(self, y, n_acc=None, stream=None):
-        """The emitted tokens of a round: the first n_acc + 1 of y."""
-        history_append(self.tokens, self.lens, y, n_acc=n_acc, ws=self.ws, stream=stream, out=self.lens)
+    def append(self, y, n_acc, row_offset=None, stream=None):
+        """The emitted tokens of a round: the first n_acc + 1 of y.  A captured round gives
+        the rows of its PagedCache as row_offset: what found no pages changes nothing."""
+        history_append(self.tokens, self.lens, y, n_acc=n_acc, row_offset=row_offset, ws=self.ws,
+                       stream=stream, out=self.lens)
 
-    def edit(self, X, *, stream=None, **edits):
+    def edit(self, X, *, ws=None, stream=None, **edits):
         """edit_logits(X) by this history."""
         return edit_logits(X, history=self.tokens, hist_len=self.lens, prompt_len=self.prompt_lens,
-                           ws=self.ws, stream=stream, **edits)
+                           ws=self.ws if ws is None else ws, stream=stream, **edits)
 
     def error_code(self, stream=None):
         return self.ws.error_code(stream)

@@ -200,11 +200,17 @@ dspark_status dspark_edit_logits_backward(int n_rows, int V, int64_t row_stride,
  * The histories that dspark_edit_logits reads grow: request rho's new tokens go to
  * history[rho][hist_len[rho] ..] and its length to hist_len_out (which may be hist_len).
  *   tokens [R][width]: the first n_acc[rho] + 1 (the y of dspark_verify; -1: none), or
- *     with n_acc NULL all of them; or with row_offset [R + 1] given (n_acc NULL) a flat
- *     list of n_tokens, request rho's [row_offset[rho], row_offset[rho + 1]): prompts
+ *     with n_acc and row_offset NULL all of them;
+ *   tokens [n_tokens] with row_offset [R + 1] alone: request rho's are those in
+ *     [row_offset[rho], row_offset[rho + 1]), a prompt's;
+ *   with n_acc and row_offset both, tokens [R][width], and row_offset is what
+ *     dspark_cache_reserve left in its workspace: as in dspark_cache_commit, n_acc[rho] + 1
+ *     has to be within the request's rows, so that a round which found no pages (and
+ *     has no rows there) leaves the histories as they were
  *   prompt_len [R] or NULL: set to the new length where a request got tokens
- * A request whose tokens do not fit, or with n_acc outside [-1, width), a bad slice or a
- * hist_len outside [0, hist_stride], sets DSPARK_DEVERR_LENGTH and stays as it is.
+ * A request whose tokens do not fit, or with n_acc outside [-1, width) or past its rows,
+ * a bad slice or a hist_len outside [0, hist_stride], sets DSPARK_DEVERR_LENGTH and
+ * stays as it is.
  * 1 <= R <= 1048576; 1 <= hist_stride <= 1048575; 1 <= width <= 1048575. */
 dspark_status dspark_history_append(int R, int width, int n_tokens, const int32_t *tokens,
                                     const int32_t *n_acc, const int32_t *row_offset,

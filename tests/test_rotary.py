@@ -1,0 +1,459 @@
+"""GPU tests of rotary positions and of cache_append against the rotation in 64 bits.
+
+Tolerances (u = 2^-24): the angle is exact but for one rounding to fp32 of at most
+pi / 4 (half a step, under 2^-25), the sums of sine and cosine end below 2^-25 and round
+their last sum at 0.5 u: cos and sin are off by at most 2 u, times the magnitude (one
+more rounding) by 3 u m.  Two products and a sum round once each: a rotated element is
+off by at most 6 u m (|a| + |b|), and a bf16 result half a step more, 2^-8 of the value.
+The reference takes the plan's own turns (position * turns mod 2^64, whole numbers), so
+it is right at any position; that the turns are the frequencies' is tested on the host.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import draft_sampling_verification_03_amd as ds
+from test_serving_attend import Case, pools_equal, same, snapshot
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+LENGTH, PAGE = 4, 32
+I32 = torch.int32
+
+
+def i32(a):
+    return torch.tensor(a, dtype=I32, device="cuda")
+
+
+def angles(plan, positions):
+    """Radians within half a turn, [n][rot / 2] in 64 bits, by whole numbers."""
+    turns = [int(t) for t in plan.turns.cpu().numpy().view(np.uint64)]
+    out = []
+    for p in positions:
+        w = [(int(p) * t) % 2 ** 64 for t in turns]
+        out.append([(x - 2 ** 64 if x >= 2 ** 63 else x) / 2 ** 64 * 2 * math.pi for x in w])
+    return torch.tensor(out, dtype=torch.float64, device="cuda")
+
+
+def rotated(x, plan, positions, back=False):
+    """(64-bit rotation of x [n][heads][D], its tolerance)."""
+    a = angles(plan, positions)[:, None]
+    c, s = plan.magnitude * torch.cos(a), plan.magnitude * torch.sin(a) * (-1 if back else 1)
+    y, tol, rot = x.double(), torch.zeros_like(x, dtype=torch.float64), plan.rot
+    i = torch.arange(rot // 2)
+    first, second = (i, i + rot // 2) if plan.layout == 0 else (2 * i, 2 * i + 1)
+    p, q = y[..., first].clone(), y[..., second].clone()
+    y[..., first], y[..., second] = p * c - q * s, q * c + p * s
+    e = 6 * U * abs(plan.magnitude) * (p.abs() + q.abs())
+    tol[..., first], tol[..., second] = e, e
+    if x.dtype == BF:
+        turned = tol > 0
+        tol = torch.where(turned, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * y.abs(), tol)
+    return y, tol
+
+
+def check(got, x, plan, positions, back=False):
+    y, tol = rotated(x, plan, positions, back)
+    err = (got.double() - y).abs()
+    assert (err <= tol).all(), ((err - tol).max().item(), (err > tol).sum().item())
+
+
+def rnd(seed, *shape, dt=F):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dt)
+
+
+SHAPES = [(64, 64, 4, 1), (128, 128, 32, 8), (96, 48, 3, 3), (128, 32, 8, 1), (80, 20, 2, 2),
+          (64, 2, 5, 1), (256, 256, 2, 1), (112, 54, 7, 1), (8, 6, 1, 1), (72, 72, 1, 1), (256, 250, 1, 4)]
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D,rot,Hq,Hkv", SHAPES)
+def test_values_and_gradient(D, rot, Hq, Hkv, layout, dt):
+    """Rows in odd number, positions near and far; the backward pass turns back."""
+    n = 37
+    plan = ds.RotaryPlan(rot, layout=layout, magnitude=1.2)
+    q, k = rnd(D, n, Hq, D, dt=dt), rnd(rot, n, Hkv, D, dt=dt)
+    pos = [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1000003] + list(range(7, 7 + n - 6))
+    ws = ds.Workspace()
+    o = ds.rotary(q, k, plan=plan, positions=i32(pos), ws=ws)
+    check(o["q"], q, plan, pos)
+    check(o["k"], k, plan, pos)
+    b = ds.rotary_backward(q, k, plan=plan, positions=i32(pos), ws=ws)
+    check(b["q"], q, plan, pos, back=True)
+    check(b["k"], k, plan, pos, back=True)
+    assert torch.equal(o["q"][..., rot:], q[..., rot:]) and ws.error_code() == 0
+    # position 0 only scales
+    assert ((o["q"][0].double() - q[0].double() * torch.where(torch.arange(D, device="cuda") < rot, 1.2, 1.0))
+            .abs() <= 2.0 ** -8 * 1.3 * q[0].double().abs()).all()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_gradient_against_differences(layout):
+    """The rotation is linear: its difference quotient along any direction is the rotated
+    direction, so <g, (f(x + h d) - f(x)) / h> = <backward(g), d>, each fp32 result off by
+    6 u (|a| + |b|) m and the quotient by twice that over h = 1."""
+    n, D = 9, 64
+    plan = ds.RotaryPlan(40, layout=layout, base=50.0)
+    x, d, g = rnd(1, n, 2, D), rnd(2, n, 2, D), rnd(3, n, 2, D)
+    f = lambda t: ds.rotary(t, plan=plan)["q"].double()  # noqa: E731
+    left = (g.double() * (f(x + d) - f(x))).sum()
+    right = (ds.rotary_backward(g, plan=plan)["q"].double() * d.double()).sum()
+    # |a| + |b| <= 2 max; x + d rounds once, u |x + d|
+    size = (g.abs().double() * (x.abs() + d.abs()).double().amax()).sum() * 4
+    assert (left - right).abs() <= 30 * U * size
+
+
+def test_positions_of_sequences():
+    """row_offset with empty requests, with and without kv_len; rows of no request stay."""
+    rows = [3, 0, 0, 5, 1, 0, 70, 2, 0]
+    off = np.concatenate(([0], np.cumsum(rows)))
+    n, D = int(off[-1]) + 3, 64
+    lens = [10, 7, 0, 5, 100, 2, 70, 5000, 1]
+    plan = ds.RotaryPlan(64)
+    q, k = rnd(1, n, 2, D), rnd(2, n, 1, D)
+    ws = ds.Workspace()
+    for kv in (None, lens):
+        pos = []
+        for r, m in enumerate(rows):
+            pos += [j + (0 if kv is None else kv[r] - m) for j in range(m)]
+        out = {"q": torch.full_like(q, 7.0), "k": torch.full_like(k, 7.0)}
+        ds.rotary(q, k, plan=plan, row_offset=i32(off.tolist()), ws=ws, out=out,
+                  kv_len=None if kv is None else i32(kv))
+        check(out["q"][:-3], q[:-3], plan, pos)
+        check(out["k"][:-3], k[:-3], plan, pos)
+        assert (out["q"][-3:] == 7).all() and (out["k"][-3:] == 7).all()
+        # positions of their own, the rows still the requests'
+        out["q"].fill_(7.0)
+        own = list(range(1000, 1000 + n))
+        ds.rotary(q, k, plan=plan, positions=i32(own), row_offset=i32(off.tolist()), ws=ws, out=out,
+                  kv_len=None if kv is None else i32(kv))
+        check(out["q"][:-3], q[:-3], plan, own[:-3])
+        assert (out["q"][-3:] == 7).all()
+    assert ws.error_code() == 0
+    check(ds.rotary(q, plan=plan)["q"], q, plan, range(n))
+    check(ds.rotary(q, plan=plan, kv_len=i32(list(range(5, 5 + n))))["q"], q, plan, range(4, 4 + n))
+
+
+def test_many_requests():
+    """More requests than a wave, most of them empty, and runs of more than 64 empty ones."""
+    g = torch.Generator().manual_seed(4)
+    rows = (torch.randint(0, 9, (5000,), generator=g) - 6).clamp(min=0)
+    rows[100:400] = 0
+    rows[4900:] = 0
+    off = [0, *rows.cumsum(0).tolist()]
+    pos = [j for m in rows.tolist() for j in range(m)]
+    q = rnd(3, off[-1], 1, 64, dt=BF)
+    plan = ds.RotaryPlan(64)
+    ws = ds.Workspace()
+    check(ds.rotary(q, plan=plan, row_offset=i32(off), ws=ws)["q"], q, plan, pos)
+    assert ws.error_code() == 0
+
+
+@pytest.mark.parametrize("off", [[0, 5, 3, 9], [-1, 2, 3, 9], [0, 2, 3, 30], [4, 2, 8, 1], [2 ** 31 - 1] * 4,
+                                 [-2 ** 31, 0, 2 ** 31 - 1, 9]])
+def test_bad_offsets_are_reported(off):
+    q = rnd(1, 9, 2, 64)
+    buffer = torch.full((29, 2, 64), 7.0, device="cuda")
+    ws = ds.Workspace()
+    ds.rotary(q, plan=ds.RotaryPlan(64), row_offset=i32(off), ws=ws, out={"q": buffer[10:19]})
+    assert ws.error_code() == LENGTH and (buffer[:10] == 7).all() and (buffer[19:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("layout,rot", [("half", 64), ("half", 20), ("interleaved", 30)])
+def test_in_place_and_strided(layout, rot, dt):
+    """Slices of one projection's output, in place: what lies between them stays."""
+    qkv = rnd(5, 21, 8, 64, dt=dt)
+    q, k = qkv[:, :5], qkv[:, 5:6]
+    plan = ds.RotaryPlan(rot, layout=layout)
+    want = ds.rotary(q.contiguous(), k.contiguous(), plan=plan)
+    rest = qkv[:, 6:].clone()
+    ds.rotary(q, k, plan=plan, out={"q": q, "k": k})
+    assert torch.equal(q, want["q"]) and torch.equal(k, want["k"]) and torch.equal(qkv[:, 6:], rest)
+
+
+def test_not_finite_stays_in_its_pair():
+    plan = ds.RotaryPlan(64)
+    q = rnd(1, 3, 1, 64)
+    good = ds.rotary(q, plan=plan)["q"].clone()
+    q[1, 0, 5], q[2, 0, 33] = float("nan"), float("inf")
+    o = ds.rotary(q, plan=plan)["q"]
+    keep = torch.ones_like(o, dtype=torch.bool)
+    keep[1, 0, [5, 37]] = False
+    keep[2, 0, [1, 33]] = False
+    assert torch.equal(o[keep], good[keep]) and not o[~keep].isfinite().any()
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 elements from the first row to the last."""
+    n, H, D = 3000, 1, 64
+    buffer = torch.empty(n, (1 << 31) // n // 8 * 8 + 800, dtype=BF, device="cuda")
+    q = buffer[:, :H * D].view(n, H, D)
+    q.copy_(rnd(3, n, H, D, dt=BF))
+    plan = ds.RotaryPlan(64)
+    want = ds.rotary(q.contiguous(), plan=plan)["q"]
+    assert torch.equal(ds.rotary(q, plan=plan, out={"q": q})["q"], want)
+    check(want[-2:], rnd(3, n, H, D, dt=BF)[-2:], plan, [n - 2, n - 1])
+
+
+def test_streams_and_replays():
+    plan = ds.RotaryPlan(128, layout="interleaved")
+    q, k = rnd(1, 50, 4, 128, dt=BF), rnd(2, 50, 2, 128, dt=BF)
+    pos, ws = i32(list(range(50))), ds.Workspace()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o = ds.rotary(q, k, plan=plan, positions=pos, ws=ws, stream=side)
+    side.synchronize()
+    check(o["q"], q, plan, range(50))
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a = ds.rotary(q, k, plan=plan, positions=pos, ws=ws)
+    with torch.cuda.graph(other):
+        b = ds.rotary_backward(q, k, plan=plan, positions=pos, ws=ws)
+    for i in range(4):
+        pos.add_(77)
+        q.copy_(rnd(10 + i, 50, 4, 128, dt=BF))
+        graph.replay()
+        other.replay()
+        torch.cuda.synchronize()
+        want = ds.rotary(q, k, plan=plan, positions=pos)
+        back = ds.rotary_backward(q, k, plan=plan, positions=pos)
+        for name in ("q", "k"):
+            assert torch.equal(a[name], want[name]) and torch.equal(b[name], back[name]), i
+    assert ws.error_code() == 0
+
+
+# ------------------------------------------------------------- cache_append
+def run_append(c, plan=None, q=True, ws=None, **kw):
+    return ds.cache_append(c.q if q else None, c.kn, c.vn, c.k, c.v, c.table, c.kv_len, plan=plan,
+                           row_offset=c.row_offset, ws=ws, **kw)
+
+
+def check_append(c, got, plan, before, positions=None):
+    """Queries, the new rows' slots, and every other slot as it was, bit for bit."""
+    k0, v0 = before
+    bits = lambda t: t.contiguous().view(torch.int16 if t.dtype == BF else I32)  # noqa: E731
+    untouched_k = torch.ones(c.k.shape[0], c.page, dtype=torch.bool, device="cuda")
+    untouched_v = untouched_k.clone()
+    for r, (n, L) in enumerate(zip(c.rows, c.lens)):
+        if n == 0:
+            continue
+        at = slice(c.off[r], c.off[r + 1])
+        pos = list(range(L - n, L)) if positions is None else positions[at]
+        if got is not None:
+            check(got[at], c.q[at], plan, pos)
+        want, tol = rotated(c.kn[at], plan, pos)
+        for j in range(n):
+            t = L - n + j
+            if t < 0:
+                continue
+            p, s = int(c.table[r, t // c.page]), t % c.page
+            assert ((c.k[p, :, s].double() - want[j]).abs() <= tol[j]).all(), (r, j)
+            assert torch.equal(c.v[p, :, :, s], c.vn[c.off[r] + j]), (r, j)
+            untouched_k[p, s] = untouched_v[p, s] = False
+    assert torch.equal(bits(c.k.transpose(1, 2)[untouched_k]), bits(k0.transpose(1, 2)[untouched_k]))
+    assert torch.equal(bits(c.v.permute(0, 3, 1, 2)[untouched_v]), bits(v0.permute(0, 3, 1, 2)[untouched_v]))
+
+
+APPENDS = [
+    ([1], [1], 1, 1, 64, 16, 64), ([1], [17], 8, 2, 128, 16, 128), ([1, 1, 1], [31, 32, 33], 4, 4, 64, 32, 20),
+    ([3, 0, 5], [3, 100, 129], 6, 2, 96, 16, 48), ([1, 9, 17, 2], [700, 9, 300, 16], 8, 1, 128, 16, 96),
+    ([17, 4], [1000, 2049], 32, 8, 128, 64, 128), ([2, 1], [130, 515], 7, 1, 256, 32, 256),
+    ([40, 16, 33], [170, 16, 48], 4, 2, 64, 256, 64), ([300, 1, 0, 131], [300, 40, 7, 400], 4, 1, 96, 64, 26),
+]
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rows,lens,Hq,Hkv,D,page,rot", APPENDS)
+def test_append(rows, lens, Hq, Hkv, D, page, rot, layout, dt):
+    c = Case(rows, lens, Hq, Hkv, D, page, dt, seed=sum(lens))
+    before = c.k.clone(), c.v.clone()
+    plan = ds.RotaryPlan(rot, layout=layout, magnitude=0.9)
+    ws = ds.Workspace()
+    got = run_append(c, plan, ws=ws)
+    assert ws.error_code() == 0
+    check_append(c, got, plan, before)
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_append_then_attend(dt):
+    """Attention over what append wrote is attention over the rotated keys."""
+    c = Case([1, 9, 40, 2], [700, 9, 300, 17], 8, 2, 64, 16, dt, seed=3)
+    plan = ds.RotaryPlan(64)
+    q = run_append(c, plan)
+    o = ds.cache_attend(q, c.k, c.v, c.table, c.kv_len, row_offset=c.row_offset)
+    for r, (n, L) in enumerate(zip(c.rows, c.lens)):  # the stored keys, of which check() asks
+        for j in range(n):
+            t = L - n + j
+            c.K[r][t] = c.k[int(c.table[r, t // 16]), :, t % 16]
+    c.q = q
+    c.check(o)
+    pools_equal(c)
+
+
+def test_append_without_a_plan_is_the_attentions_own():
+    """No rotation: the pages and the results are bit for bit what cache_attend makes of
+    k_new and v_new itself."""
+    a = Case([5, 1, 30], [90, 33, 30], 8, 2, 64, 16, BF, seed=5)
+    b = Case([5, 1, 30], [90, 33, 30], 8, 2, 64, 16, BF, seed=5)
+    want = a.run()
+    q = run_append(b)
+    got = ds.cache_attend(q, b.k, b.v, b.table, b.kv_len, row_offset=b.row_offset)
+    assert torch.equal(q, b.q) and torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    assert torch.equal(a.k.view(torch.int16), b.k.view(torch.int16))
+    assert torch.equal(a.v.view(torch.int16), b.v.view(torch.int16))
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_append_packed_layers_positions_and_keys_alone(dt):
+    """Slices of one projection, three layers side by side, positions of their own, the
+    queries in place; then keys and values without queries."""
+    c = Case([5, 1, 2], [90, 33, 2], 8, 2, 64, 16, dt, layers=3, packed=True)
+    others = c.k_all[:, :2].clone(), c.v_all[:, :2].clone()
+    before = c.k.clone(), c.v.clone()
+    plan = ds.RotaryPlan(32)
+    pos = [5, 100, -3, 7, 7, 1 << 20, 0, 2]
+    raw = c.q.clone()
+    got = run_append(c, plan, positions=i32(pos), out=c.q)
+    assert got is c.q
+    c.q = raw
+    check_append(c, got, plan, before, positions=pos)
+    c.k.copy_(before[0]), c.v.copy_(before[1])
+    assert run_append(c, plan, q=False, positions=i32(pos)) is None
+    check_append(c, None, plan, before, positions=pos)
+    for was, now in zip(others, (c.k_all[:, :2], c.v_all[:, :2])):
+        assert torch.equal(was.view(torch.int16), now.contiguous().view(torch.int16))
+
+
+def test_append_one_row_each_and_rows_behind_the_last():
+    c = Case([1, 1, 1], [50, 1, 129], 4, 2, 64, 16, BF)
+    before = c.k.clone(), c.v.clone()
+    plan = ds.RotaryPlan(64)
+    got = ds.cache_append(c.q, c.kn, c.vn, c.k, c.v, c.table, c.kv_len, plan=plan)
+    check_append(c, got, plan, before)
+    c = Case([2, 3], [50, 70], 4, 2, 64, 16, BF)
+    before = c.k.clone(), c.v.clone()
+    pad = lambda t: torch.cat([t, torch.full_like(t[:2], 9.0)])  # noqa: E731
+    out = torch.full((7, 4, 64), 3.0, dtype=BF, device="cuda")
+    ds.cache_append(pad(c.q), pad(c.kn), pad(c.vn), c.k, c.v, c.table, c.kv_len, plan=plan,
+                    row_offset=c.row_offset, out=out)
+    assert (out[5:] == 3).all()
+    check_append(c, out[:5], plan, before)
+
+
+def test_append_before_token_0_and_bad_pages():
+    """Rows before token 0, pages outside the pool and lengths out of bounds reach no
+    page and are reported; the others are written, and queries are rotated all the same."""
+    plan = ds.RotaryPlan(64)
+    c = Case([1, 30, 2], [0, 20, 40], 4, 2, 64, 16, F, append=False)
+    c.k.fill_(5.0), c.v.fill_(5.0)
+    before = c.k.clone(), c.v.clone()
+    ws = ds.Workspace()
+    got = run_append(c, plan, ws=ws)
+    assert ws.error_code() == LENGTH
+    ws.clear_error()
+    check_append(c, got, plan, before)
+    c = Case([20, 2], [100, 60], 4, 2, 64, 16, BF, seed=4)
+    c.k.fill_(5.0), c.v.fill_(5.0)
+    before = c.k.clone(), c.v.clone()
+    c.table[0, 5], c.table[1, 3] = c.n_pages + 5, -3  # tokens 80..95 of 0, both rows of 1
+    got = run_append(c, plan, ws=ws)
+    assert ws.error_code() == PAGE
+    ws.clear_error()
+    check(got[:20], c.q[:20], plan, range(80, 100))
+    check(got[20:], c.q[20:], plan, range(58, 60))
+    page = int(c.table[0, 6])
+    want, tol = rotated(c.kn[16:20], plan, range(96, 100))
+    assert ((c.k[page, :, :4].transpose(0, 1).double() - want).abs() <= tol).all()
+    c.k[page], c.v[page] = 5.0, 5.0
+    assert torch.equal(c.k, before[0]) and torch.equal(c.v, before[1])
+    for off, lens in (([0, 5, 3], [100, 60]), ([0, 20, 2000], [100, 60]), ([-1, 20, 22], [100, 60]),
+                      ([0, 20, 22], [-1, 60]), ([0, 20, 22], [1 << 20, 60]),
+                      ([2 ** 31 - 1, -2 ** 31, 22], [100, 60]), ([22, 0, 22], [100, 60])):
+        c.row_offset, c.kv_len = i32(off), i32(lens)
+        run_append(c, plan, ws=ws)
+        assert ws.error_code() & LENGTH, (off, lens)
+        ws.clear_error()
+
+
+def test_append_past_32_bit_offsets():
+    """A pool of more than 2^32 bytes and 2^31 elements, the request in its last pages."""
+    Hkv, D, page = 8, 128, 16
+    n_pages = (1 << 31) // (Hkv * D * page) + 40
+    c = Case([20], [100], 8, 8, D, page, BF)
+    few = c.n_pages
+    k = torch.zeros((n_pages, Hkv, page, D), dtype=BF, device="cuda")
+    v = torch.zeros((n_pages, Hkv, D, page), dtype=BF, device="cuda")
+    plan = ds.RotaryPlan(128)
+    ds.cache_append(None, c.kn, c.vn, k, v, torch.where(c.table >= 0, c.table + n_pages - few, c.table),
+                    c.kv_len, plan=plan, row_offset=c.row_offset)
+    c.k.zero_(), c.v.zero_()
+    run_append(c, plan, q=False)
+    assert torch.equal(k[-few:], c.k) and torch.equal(v[-few:], c.v)
+    assert not k[:-few].any() and not v[:-few].any()
+
+
+def test_append_streams_and_two_graphs_over_one_workspace():
+    c = Case([3, 1, 40], [60, 2000, 47], 8, 2, 64, 16, BF, seed=6)
+    before = c.k.clone(), c.v.clone()
+    plan, ws, side = ds.RotaryPlan(64), ds.Workspace(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run_append(c, plan, ws=ws, stream=side)
+    side.synchronize()
+    check_append(c, got, plan, before)
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        a = run_append(c, plan, ws=ws)
+    with torch.cuda.graph(g2):
+        b = run_append(c, plan, ws=ws)
+    for i in range(3):
+        c.q.copy_(rnd(20 + i, *c.q.shape, dt=BF))
+        c.lens = [60, 2000 - 300 * i, 47 - i]  # within the pages that the table has
+        c.kv_len.copy_(i32(c.lens))
+        c.k.copy_(before[0]), c.v.copy_(before[1])
+        g1.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        check_append(c, a, plan, before)
+        assert torch.equal(a, b)
+    assert ws.error_code() == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_round_without_room_appends_nothing(captured):
+    """reserve finds no pages and nobody looks: the append and the attention behind it
+    leave pages and outputs as they were."""
+    R, Hq, Hkv, D = 2, 4, 2, 64
+    cache = ds.PagedCache(R, 3, Hkv=Hkv, D=D, page=16, dtype=F)
+    plan = ds.RotaryPlan(64)
+    cache.reserve(i32([0, 30, 40]))
+    cache.attend(0, rnd(1, 40, Hq, D), rnd(2, 40, Hkv, D), rnd(3, 40, Hkv, D), rotary=plan)
+    cache.commit(i32([29, 9]))
+    off, acc = i32([0, 3, 20]), i32([1, 2])
+    q, kn, vn = rnd(4, 20, Hq, D), rnd(5, 20, Hkv, D), rnd(6, 20, Hkv, D)
+    out = dict(out=torch.full((20, Hq, D), 3.0, device="cuda"), lse=torch.full((20, Hq), 3.0, device="cuda"))
+
+    def go():
+        cache.reserve(off)
+        cache.attend(0, q, kn, vn, rotary=plan, out=out)
+        cache.commit(acc)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go()
+        go = graph.replay
+    before = snapshot(cache)
+    for _ in range(3):
+        go()
+        torch.cuda.synchronize()
+        assert same(snapshot(cache), before)
+        assert cache.missing.item() == 2  # one more page for each request
+        assert (out["out"] == 3).all() and (out["lse"] == 3).all()

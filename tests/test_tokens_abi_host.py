@@ -1,0 +1,316 @@
+"""Host-side checks of include/dspark_tokens.h (no GPU needed): every declared function
+is exported, every invalid argument is refused before any HIP call (the pointers are
+fake aligned addresses that nothing dereferences), and the frequencies of a rotary plan."""
+import math
+import os
+import re
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+import draft_sampling_verification_03_amd as ds
+from draft_sampling_verification_03_amd import _abi as A
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, NULL, SHAPE, DTYPE, VALUE, WS, SPS, MODE, ALIGN = range(9)
+P, P2, P3 = 0x10000, 0x20000, 0x30000
+I32 = torch.int32
+
+
+def test_library_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "dspark_tokens.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\b(dspark_[a-z_0-9]+)\s*\(", text)))
+    assert len(names) == 8, names
+    for name in names:
+        assert hasattr(ds.library(), name)
+        assert callable(getattr(ds, name))
+
+
+# ------------------------------------------------------------- frequencies
+def frequencies(rot, base, scaling=0, factor=1.0, context=0.0, slow=1.0, fast=32.0):
+    f = np.full(rot // 2, np.nan)
+    return A.dspark_rotary_frequencies(rot, base, scaling, factor, context, slow, fast,
+                                       f.ctypes.data), f
+
+
+@pytest.mark.parametrize("rot", [2, 4, 24, 64, 128, 256])
+def test_frequencies(rot):
+    """Each against its formula; pow and the quotients are off by a few 2^-53."""
+    i = np.arange(rot // 2)
+    plain = np.array([10000.0 ** (-2.0 * j / rot) for j in i])
+    st, f = frequencies(rot, 10000.0)
+    assert st == OK and np.allclose(f, plain, rtol=1e-15, atol=0)
+    st, f = frequencies(rot, 10000.0, A.DSPARK_ROTARY_LINEAR, 4.0)
+    assert st == OK and np.allclose(f, plain / 4, rtol=1e-15, atol=0)
+    if rot > 2:
+        st, f = frequencies(rot, 10000.0, A.DSPARK_ROTARY_BASE, 4.0)
+        # 2^-53 of the exponents grows by the logarithm of the base
+        assert st == OK and f[0] == 1.0 and np.allclose(f[-1] * 4, plain[-1], rtol=1e-13, atol=0)
+        assert (np.diff(np.log(f / plain)) < 0).all()
+    st, f = frequencies(rot, 10000.0, A.DSPARK_ROTARY_BY_TURNS, 8.0, 4096.0, 1.0, 32.0)
+    want = []
+    for p in plain:
+        c = 4096.0 * p / (2 * math.pi)
+        w = min(max((c - 1.0) / 31.0, 0.0), 1.0)
+        want.append(p * (w + (1 - w) / 8.0))
+    assert st == OK and np.allclose(f, want, rtol=1e-14, atol=0)
+
+
+@pytest.mark.parametrize("args,expect", [
+    ((0, 1e4), SHAPE), ((3, 1e4), SHAPE), ((258, 1e4), SHAPE), ((2, 1e4, 2, 2.0), SHAPE),
+    ((64, 1.0), VALUE), ((64, float("inf")), VALUE), ((64, float("nan")), VALUE),
+    ((64, 1e4, 1, 0.5), VALUE), ((64, 1e4, 3, 8.0, 0.0), VALUE), ((64, 1e4, 3, 8.0, 4096.0, 0.0), VALUE),
+    ((64, 1e4, 3, 8.0, 4096.0, 4.0, 4.0), VALUE), ((64, 1e4, 4), MODE), ((64, 1e4, -1), MODE),
+])
+def test_frequencies_validation(args, expect):
+    assert frequencies(*args)[0] == expect
+    assert A.dspark_rotary_frequencies(64, 1e4, 0, 1.0, 0.0, 1.0, 32.0, None) == NULL
+
+
+# 2 pi to 60 digits
+TWO_PI = Fraction("6.28318530717958647692528676655900576839433879875021164194989")
+
+
+def test_turns():
+    """f / (2 pi) in 64 fractional bits, off by at most one unit and what a long double's
+    64-bit mantissa leaves of the turns."""
+    f = np.array([1.0, 0.5, 1e-6, 0.0, -0.25, 3.0, math.pi, -math.pi, 12345.678, 1e-15])
+    t = np.zeros(len(f), np.uint64)
+    assert A.dspark_rotary_turns(len(f), f.ctypes.data, t.ctypes.data) == OK
+    for x, got in zip(f, t):
+        exact = Fraction(float(x)) / TWO_PI * 2 ** 64
+        off = (int(got) - exact) % 2 ** 64
+        off = min(off, 2 ** 64 - off)
+        assert off <= 1 + abs(float(exact)) * 2.0 ** -63, (x, got)
+    one = np.array([1.0])
+    for bad in (np.inf, np.nan, 2.0 ** 20, -2.0 ** 20):
+        b = np.array([bad])
+        assert A.dspark_rotary_turns(1, b.ctypes.data, t.ctypes.data) == VALUE
+    assert A.dspark_rotary_turns(0, one.ctypes.data, t.ctypes.data) == SHAPE
+    assert A.dspark_rotary_turns(129, one.ctypes.data, t.ctypes.data) == SHAPE
+    assert A.dspark_rotary_turns(1, None, t.ctypes.data) == NULL
+    assert A.dspark_rotary_turns(1, one.ctypes.data, None) == NULL
+
+
+def test_plan():
+    plan = ds.RotaryPlan(64, base=500000.0, scaling="by_turns", factor=8.0, context=8192.0,
+                         magnitude=1.25, layout="interleaved", device="cpu")
+    assert plan.turns.shape == (32,) and plan.turns.dtype == torch.int64 and plan.magnitude == 1.25
+    assert np.array_equal(plan.frequencies, frequencies(64, 500000.0, 3, 8.0, 8192.0)[1])
+    own = ds.RotaryPlan(64, frequencies=torch.from_numpy(plan.frequencies), device="cpu")
+    assert torch.equal(own.turns, plan.turns)
+    for kw, error in ((dict(layout="other"), ValueError), (dict(scaling="other"), ValueError),
+                      (dict(frequencies=np.ones(31)), ValueError),
+                      (dict(frequencies=np.ones(32), scaling="linear"), ValueError),
+                      (dict(base=0.5), ds.DSparkError), (dict(scaling="by_turns"), ds.DSparkError),
+                      (dict(frequencies=np.full(32, np.nan)), ds.DSparkError)):
+        with pytest.raises(error):
+            ds.RotaryPlan(64, device="cpu", **kw)
+    for rot in (0, 7, 258):
+        with pytest.raises(ValueError):
+            ds.RotaryPlan(rot, device="cpu")
+
+
+# --------------------------------------------------------------- validation
+def rotary(**over):
+    a = dict(n_rows=8, Hq=4, Hkv=2, D=64, rot=32, layout=0, dt=A.DSPARK_BF16, magnitude=1.0, turns=P,
+             positions=P, R=2, row_offset=P, kv_len=P, q=P, q_stride=256, k=P, k_stride=128, q_out=P2,
+             q_out_stride=256, k_out=P2, k_out_stride=128, ws=P, ws_bytes=256, stream=None)
+    a.update(over)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dt=5), DTYPE), (dict(layout=2), MODE), (dict(n_rows=0), SHAPE),
+    (dict(n_rows=(1 << 22) + 1), SHAPE), (dict(Hq=0), SHAPE), (dict(Hq=1025), SHAPE),
+    (dict(Hkv=-1), SHAPE), (dict(D=0), SHAPE), (dict(D=60), SHAPE), (dict(D=264), SHAPE),
+    (dict(rot=0), SHAPE), (dict(rot=33), SHAPE), (dict(rot=66), SHAPE), (dict(R=0), SHAPE),
+    (dict(q_stride=248), SHAPE), (dict(q_stride=260), SHAPE), (dict(k_stride=120), SHAPE),
+    (dict(q_out_stride=252), SHAPE), (dict(k_out_stride=124), SHAPE),
+    (dict(magnitude=0.0), VALUE), (dict(magnitude=float("nan")), VALUE), (dict(turns=None), NULL),
+    (dict(q=None), NULL), (dict(k=None), NULL), (dict(Hkv=0), NULL), (dict(q_out=None), NULL),
+    (dict(k_out=None), NULL), (dict(ws=None), NULL), (dict(q_out=P, q_out_stride=264), VALUE),
+    (dict(k_out=P, k_out_stride=136), VALUE), (dict(q=P + 8), ALIGN), (dict(k_out=P2 + 4), ALIGN),
+    (dict(turns=P + 4), ALIGN), (dict(ws=P + 8), ALIGN), (dict(ws_bytes=255), WS),
+])
+@pytest.mark.parametrize("f", [A.dspark_rotary, A.dspark_rotary_backward])
+def test_rotary_validation(f, over, expect):
+    assert f(*rotary(**over)) == expect
+
+
+def append(**over):
+    a = dict(R=4, rows_capacity=12, Hq=8, Hkv=2, D=64, page=16, max_pages=8, n_pages=64,
+             dt=A.DSPARK_BF16, rot=64, layout=0, magnitude=1.0, turns=P, positions=None, q=P,
+             q_stride=512, q_out=P2, q_out_stride=512, k_new=P, v_new=P, kv_stride=128, k_pages=P,
+             v_pages=P, k_page_stride=2048, v_page_stride=2048, table=P, row_offset=P, kv_len=P, ws=P,
+             ws_bytes=256, stream=None)
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dt=3), DTYPE), (dict(layout=-1), MODE), (dict(R=0), SHAPE), (dict(rows_capacity=0), SHAPE),
+    (dict(Hq=9), SHAPE), (dict(Hkv=0), SHAPE), (dict(D=80), SHAPE), (dict(page=12), SHAPE),
+    (dict(n_pages=0), SHAPE), (dict(max_pages=1 << 29), SHAPE), (dict(row_offset=None), SHAPE),
+    (dict(rot=-2), SHAPE), (dict(rot=31), SHAPE), (dict(rot=66), SHAPE), (dict(magnitude=0.0), VALUE),
+    (dict(rot=0), NULL), (dict(turns=None), NULL), (dict(q=None), NULL), (dict(q_out=None), NULL),
+    (dict(k_new=None), NULL), (dict(v_new=None), NULL), (dict(k_pages=None), NULL),
+    (dict(v_pages=None), NULL), (dict(table=None), NULL), (dict(kv_len=None), NULL),
+    (dict(ws=None), NULL), (dict(q_stride=504), SHAPE), (dict(q_out_stride=516), SHAPE),
+    (dict(kv_stride=120), SHAPE), (dict(k_page_stride=2040), SHAPE), (dict(v_page_stride=2052), SHAPE),
+    (dict(q_out=P, q_out_stride=520), VALUE), (dict(q=P + 8), ALIGN), (dict(q_out=P2 + 2), ALIGN),
+    (dict(k_new=P + 4), ALIGN), (dict(v_pages=P + 8), ALIGN), (dict(turns=P + 4), ALIGN),
+    (dict(ws_bytes=128), WS),
+])
+def test_append_validation(over, expect):
+    assert A.dspark_cache_append(**append(**over)) == expect
+
+
+def edit(**over):
+    a = dict(n_rows=8, V=1001, row_stride=1008, dt=A.DSPARK_BF16, X=P, R=2, row_offset=P, history=P,
+             hist_stride=100, hist_len=P, prompt_len=P, drafts=P, gamma=4, repetition=P, frequency=P,
+             presence=P, n_bias=3, bias_ids=P, bias=P, n_masks=2, mask=P, mask_stride=32, mask_index=P,
+             out=P2, out_stride=1008, ws=P, ws_bytes=256, stream=None)
+    a.update(over)
+    return a
+
+
+SHARED = [
+    (dict(dt=2), DTYPE), (dict(n_rows=0), SHAPE), (dict(n_rows=(1 << 22) + 1), SHAPE), (dict(V=0), SHAPE),
+    (dict(V=262145, row_stride=262152), SHAPE), (dict(R=0), SHAPE), (dict(R=9), SHAPE),
+    (dict(row_offset=None), SHAPE), (dict(row_stride=1000), SHAPE), (dict(row_stride=1012), SHAPE),
+    (dict(hist_stride=0), SHAPE), (dict(hist_stride=1 << 20), SHAPE), (dict(gamma=-1), SHAPE),
+    (dict(gamma=0), SHAPE), (dict(gamma=1 << 20), SHAPE), (dict(n_masks=0), SHAPE),
+    (dict(mask_stride=31), SHAPE), (dict(mask_index=None), SHAPE), (dict(X=None), NULL),
+    (dict(hist_len=None), NULL), (dict(history=None), NULL), (dict(drafts=None), NULL),
+    (dict(mask=None), NULL), (dict(ws=None), NULL), (dict(X=P + 8), ALIGN), (dict(ws=P + 4), ALIGN),
+    (dict(history=P + 2), ALIGN), (dict(mask=P + 1), ALIGN), (dict(repetition=P + 2), ALIGN),
+    (dict(ws_bytes=100), WS),
+]
+
+
+@pytest.mark.parametrize("over,expect", SHARED + [
+    (dict(out_stride=1000), SHAPE), (dict(n_bias=-1), SHAPE), (dict(n_bias=1024), SHAPE),
+    (dict(bias=None), NULL), (dict(bias_ids=None), NULL), (dict(out=None), NULL),
+    (dict(out=P2 + 8), ALIGN), (dict(bias=P + 3), ALIGN), (dict(out=P, out_stride=1016), VALUE),
+])
+def test_edit_validation(over, expect):
+    assert A.dspark_edit_logits(**edit(**over)) == expect
+
+
+@pytest.mark.parametrize("over,expect", SHARED + [
+    (dict(G=None), NULL), (dict(dX=None), NULL), (dict(g_stride=1000), SHAPE),
+    (dict(dx_stride=1004), SHAPE), (dict(dX=P3 + 8), ALIGN), (dict(dX=P2, dx_stride=1016), VALUE),
+    (dict(dX=P), VALUE),
+])
+def test_edit_backward_validation(over, expect):
+    a = edit(G=P2, g_stride=1008, dX=P3, dx_stride=1008)
+    for name in ("frequency", "presence", "n_bias", "bias_ids", "bias", "out", "out_stride"):
+        a.pop(name)
+    a.update(over)
+    assert A.dspark_edit_logits_backward(**a) == expect
+
+
+def history(**over):
+    a = dict(R=4, width=5, n_tokens=20, tokens=P, n_acc=P, row_offset=None, hist_stride=64, history=P,
+             hist_len=P, hist_len_out=P, prompt_len=P, ws=P, ws_bytes=256, stream=None)
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(R=0), SHAPE), (dict(R=(1 << 20) + 1), SHAPE), (dict(width=0), SHAPE),
+    (dict(width=1 << 20), SHAPE), (dict(hist_stride=0), SHAPE), (dict(hist_stride=1 << 20), SHAPE),
+    (dict(row_offset=P, n_acc=None, n_tokens=-1), SHAPE), (dict(row_offset=P, width=0), SHAPE),
+    (dict(tokens=None), NULL), (dict(history=None), NULL), (dict(hist_len=None), NULL),
+    (dict(hist_len_out=None), NULL), (dict(ws=None), NULL), (dict(ws=P + 4), ALIGN),
+    (dict(ws_bytes=16), WS),
+])
+def test_history_validation(over, expect):
+    assert A.dspark_history_append(**history(**over)) == expect
+
+
+# ---------------------------------------------------------- the torch wrappers
+def host(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=I32)
+
+
+def plan():
+    return ds.RotaryPlan(32, device="cpu")
+
+
+@pytest.mark.parametrize("call,error,match", [
+    (lambda: ds.rotary(host(4, 64), plan=plan()), ValueError, r"\[rows\]\[heads\]\[D\]"),
+    (lambda: ds.rotary(host(4, 2, 64, dtype=torch.float16), plan=plan()), TypeError, "bfloat16 or"),
+    (lambda: ds.rotary(host(4, 2, 64), host(5, 1, 64), plan=plan()), ValueError, "k must have shape"),
+    (lambda: ds.rotary(host(4, 2, 64), host(4, 1, 64, dtype=torch.bfloat16), plan=plan()), TypeError, "k"),
+    (lambda: ds.rotary(host(4, 2, 64), plan=None), TypeError, "RotaryPlan"),
+    (lambda: ds.rotary(host(4, 2, 64), plan=plan(), positions=i32(3)), ValueError, "positions"),
+    (lambda: ds.rotary(host(4, 2, 64), plan=plan(), positions=torch.zeros(4, dtype=torch.int64)),
+     TypeError, "positions"),
+    (lambda: ds.rotary(host(4, 2, 64), plan=plan(), kv_len=i32(3)), ValueError, "kv_len"),
+    (lambda: ds.rotary(host(4, 64, 2).transpose(1, 2), plan=plan()), ValueError, "contiguous past"),
+    (lambda: ds.rotary(host(4, 2, 64), plan=plan()), ValueError, "not a GPU tensor"),
+    (lambda: ds.rotary_backward(host(4, 2, 64), plan=plan()), ValueError, "rotary_backward"),
+    (lambda: ds.cache_append(None, host(4, 2), host(4, 2, 64), host(9, 2, 16, 64), host(9, 2, 64, 16),
+                             i32(4, 8), i32(4)), ValueError, "k_new"),
+    (lambda: ds.cache_append(None, host(4, 2, 64), host(4, 3, 64), host(9, 2, 16, 64),
+                             host(9, 2, 64, 16), i32(4, 8), i32(4)), ValueError, "v_new"),
+    (lambda: ds.cache_append(None, host(4, 2, 64), host(4, 2, 64), host(9, 2, 16, 64),
+                             host(9, 2, 16, 64), i32(4, 8), i32(4)), ValueError, "v_pages"),
+    (lambda: ds.cache_append(None, host(5, 2, 64), host(5, 2, 64), host(9, 2, 16, 64),
+                             host(9, 2, 64, 16), i32(4, 8), i32(4)), ValueError, "row_offset"),
+    (lambda: ds.cache_append(host(3, 2, 64), host(4, 2, 64), host(4, 2, 64), host(9, 2, 16, 64),
+                             host(9, 2, 64, 16), i32(4, 8), i32(4)), ValueError, "q must have shape"),
+    (lambda: ds.cache_append(None, host(4, 2, 64), host(4, 2, 64), host(9, 2, 16, 64),
+                             host(9, 2, 64, 16), i32(4, 8), i32(4), out=host(4, 2, 64)), ValueError,
+     "out is for the queries"),
+    (lambda: ds.edit_logits(host(4)), ValueError, r"\[n_rows\]\[V\]"),
+    (lambda: ds.edit_logits(host(4, 7)), ValueError, "16-byte pieces"),
+    (lambda: ds.edit_logits(host(4, 8), row_offset=i32(6)), ValueError, "5 requests"),
+    (lambda: ds.edit_logits(host(4, 8), history=i32(3, 5), hist_len=i32(3)), ValueError, "history"),
+    (lambda: ds.edit_logits(host(4, 8), history=i32(4, 5)), ValueError, "hist_len is required"),
+    (lambda: ds.edit_logits(host(4, 8), prompt_len=i32(4)), ValueError, "belong to a history"),
+    (lambda: ds.edit_logits(host(4, 8), drafts=i32(3, 2)), ValueError, "drafts"),
+    (lambda: ds.edit_logits(host(4, 8), repetition=host(3)), ValueError, "repetition"),
+    (lambda: ds.edit_logits(host(4, 8), bias_ids=i32(4, 2)), ValueError, "bias is required"),
+    (lambda: ds.edit_logits(host(4, 8), bias=host(4, 2)), ValueError, "bias_ids is required"),
+    (lambda: ds.edit_logits(host(4, 40), mask=i32(4, 1)), ValueError, r"\[n_masks\]\[2\]"),
+    (lambda: ds.edit_logits(host(4, 8), mask=i32(3, 1)), ValueError, "need mask_index"),
+    (lambda: ds.edit_logits(host(4, 8), mask=host(4, 1)), TypeError, "mask"),
+    (lambda: ds.edit_logits(host(4, 8), mask_index=i32(4)), ValueError, "without a mask"),
+    (lambda: ds.edit_logits(host(4, 8)), ValueError, "not a GPU tensor"),
+    (lambda: ds.edit_logits_backward(host(4, 8), repetition=host(4)), ValueError, "X is required"),
+    (lambda: ds.edit_logits_backward(host(4, 8), host(4, 9)), ValueError, "X must have shape"),
+    (lambda: ds.history_append(i32(4), i32(4), i32(4, 2)), ValueError, r"\[R\]\[capacity\]"),
+    (lambda: ds.history_append(i32(4, 9), i32(3), i32(4, 2)), ValueError, "hist_len"),
+    (lambda: ds.history_append(i32(4, 9), i32(4), i32(3, 2)), ValueError, "tokens"),
+    (lambda: ds.history_append(i32(4, 9), i32(4), i32(4, 2), row_offset=i32(5)), ValueError, "tokens"),
+    (lambda: ds.history_append(i32(4, 9), i32(4), i32(4, 2), n_acc=i32(4), row_offset=i32(4)),
+     ValueError, "row_offset"),
+    (lambda: ds.history_append(i32(4, 9), i32(4), i32(4, 2)), ValueError, "not a GPU tensor"),
+])
+def test_wrapper_refusals(call, error, match):
+    with pytest.raises(error, match=match):
+        call()
+
+
+def test_objects_on_the_host():
+    cache = ds.PagedCache(2, 8, Hkv=2, D=64, device="cpu")
+    with pytest.raises(ValueError, match=r"reserve\(\) comes first"):
+        cache.append(0, host(2, 8, 64), host(2, 2, 64), host(2, 2, 64))
+    cache.row_offset = cache.rows
+    with pytest.raises(ValueError, match="rotary needs"):
+        cache.attend(0, host(2, 8, 64), rotary=plan())
+    with pytest.raises(ValueError, match="positions are for rotary"):
+        cache.attend(0, host(2, 8, 64), positions=i32(2))
+    h = ds.TokenHistory(3, 10, device="cpu")
+    assert h.tokens.shape == (3, 12) and (h.tokens == -1).all() and h.lens.tolist() == [0, 0, 0]
+    assert h.prompt_lens.tolist() == [0, 0, 0] and h.ws.buf.numel() >= 256
