@@ -23,35 +23,65 @@ namespace {
 
 constexpr int kCountBits = 21, kBiasShift = 22;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1, kPromptBit = 1u << kCountBits;
-constexpr int kOwn = 16;                // tokens of a thread
-constexpr int kChunk = kBlock * kOwn;   // tokens of a workgroup
-
-template <typename T> struct Edit {
-  static constexpr int kPer = Elem<T>::kPerVec, kVecs = kOwn / kPer;
-  static constexpr uint32_t kAll = (1u << kPer) - 1;
-};
+constexpr int kOwn = 16;  // tokens of a thread
 
 // f(token, index) for the tokens [0, n) at p, spread over the workgroup; -1 is skipped,
-// what lies outside the vocabulary sets *bits.
-template <typename F>
+// what lies outside the vocabulary sets *bits.  16-byte loads, four of them in flight.
+template <int kThreads, typename F>
 __device__ __forceinline__ void each_token(const int32_t *p, int n, int V, int *bits, F f) {
   auto one = [&](int v, int i) __attribute__((always_inline)) {
     if ((unsigned)v < (unsigned)V) f(v, i);
     else if (v != -1) *bits |= kErrToken;
   };
-  // 16-byte loads of the aligned middle
+  const int tid = threadIdx.x;
   const int head = min(n, (int)((16 - ((uintptr_t)p & 15)) & 15) / 4);
   const int quads = (n - head) / 4, tail = head + 4 * quads;
-#pragma unroll 4
-  for (int q = threadIdx.x; q < quads; q += kBlock) {
-    const int4 v = *reinterpret_cast<const int4 *>(p + head + 4 * q);
-    one(v.x, head + 4 * q);
-    one(v.y, head + 4 * q + 1);
-    one(v.z, head + 4 * q + 2);
-    one(v.w, head + 4 * q + 3);
+  const int4 *mid = reinterpret_cast<const int4 *>(p + head);
+  for (int q0 = tid; q0 < quads; q0 += 4 * kThreads) {
+    int4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = q0 + i * kThreads;
+      v[i] = q < quads ? mid[q] : make_int4(-1, -1, -1, -1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = head + 4 * (q0 + i * kThreads);
+      one(v[i].x, at);
+      one(v[i].y, at + 1);
+      one(v[i].z, at + 2);
+      one(v[i].w, at + 3);
+    }
   }
-  if ((int)threadIdx.x < head) one(p[threadIdx.x], threadIdx.x);
-  if ((int)threadIdx.x < n - tail) one(p[tail + threadIdx.x], tail + threadIdx.x);
+  if (tid < head) one(p[tid], tid);
+  if (tid < n - tail) one(p[tail + tid], tail + tid);
+}
+
+template <typename T> __device__ __forceinline__ void unpack(u32x4 v, float *x) {
+  if constexpr (sizeof(T) == 2) {
+    const u16x8 h = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = bf16_to_f32(h[i]);
+  } else {
+    const floatx4 f = __builtin_bit_cast(floatx4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f[i];
+  }
+}
+template <typename T> __device__ __forceinline__ u32x4 pack(const float *x) {
+  if constexpr (sizeof(T) == 2) {
+    bf16x8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (__bf16)x[i];
+    return __builtin_bit_cast(u32x4, h);
+  } else {
+    return __builtin_bit_cast(u32x4, floatx4{x[0], x[1], x[2], x[3]});
+  }
+}
+// element i of a piece
+template <typename T> __device__ __forceinline__ void store_piece(T *to, u32x4 v, int i) {
+  if constexpr (sizeof(T) == 2) to[i].bits = __builtin_bit_cast(u16x8, v)[i];
+  else to[i] = __builtin_bit_cast(floatx4, v)[i];
 }
 
 struct Rules {  // of one request
@@ -89,23 +119,25 @@ __device__ __forceinline__ float parameter(const float *p, int r, float none, fl
 
 }  // namespace
 
-// Units of work: (request, part of its rows, chunk), chunks innermost.
-template <typename T, bool kGrad>
-__global__ __launch_bounds__(kBlock) void edit_kernel(EditLaunch L, int chunks, int parts) {
-  using E = Edit<T>;
-  constexpr int kPer = E::kPer, kVecs = E::kVecs;
-  __shared__ __attribute__((aligned(16))) uint32_t word[kChunk];
-  const int tid = threadIdx.x;
-  const int64_t units = (int64_t)L.R * parts * chunks;
-  const bool counts = L.history != nullptr || L.drafts != nullptr || L.n_bias > 0;
+// Units of work: (request, part of its rows, chunk), chunks innermost.  kCounts: whether
+// histories, drafts or biases are given at all.
+//
+// The rows are a pipeline: the mask bits of row j + 2 and the logits of row j + 1 are on
+// their way while row j is edited and stored.
+template <typename T, bool kGrad, bool kCounts, int kThreads>
+__global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned chunks, unsigned parts) {
+  constexpr int kPer = Elem<T>::kPerVec, kVecs = kOwn / kPer, kChunk = kThreads * kOwn;
+  constexpr uint32_t kAll = (1u << kPer) - 1;
+  __shared__ __attribute__((aligned(16))) uint32_t word[kCounts ? kChunk : 4];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const unsigned units = L.R * parts * chunks;
   const bool in_place = L.out == (kGrad ? L.G : L.X);
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int chunk = (int)(unit % chunks);
-    const int64_t rest = unit / chunks;
-    const int r = (int)(rest / parts), part = (int)(rest % parts);
-    const bool report = chunk == 0 && part == 0;
-    int bits = 0;
-    int a = r, n = 1;
+  const T *source = reinterpret_cast<const T *>(kGrad ? L.G : L.X);
+  const int64_t stride = kGrad ? L.g_stride : L.row_stride;
+  for (unsigned unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const unsigned rest = unit / chunks, r = rest / parts, part = rest % parts;
+    const int chunk = unit % chunks, base = chunk * kChunk;
+    int bits = 0, a = r, n = 1;
     if (L.row_offset != nullptr) {
       a = L.row_offset[r];
       const int b = L.row_offset[r + 1];
@@ -121,128 +153,172 @@ __global__ __launch_bounds__(kBlock) void edit_kernel(EditLaunch L, int chunks, 
     rules.inverse = 1.0f / rules.repetition;
     rules.bias_end = L.n_bias > 0 ? L.bias + ((int64_t)r + 1) * L.n_bias : nullptr;
     int len = 0, prompt = 0;
-    if (L.history != nullptr) {
+    if (kCounts && L.history != nullptr) {
       len = L.hist_len[r];
       if (len < 0 || len > L.hist_stride) bits |= kErrLength, len = 0;
       prompt = L.prompt_len != nullptr ? L.prompt_len[r] : 0;
       if (prompt < 0 || prompt > len) bits |= kErrLength, prompt = 0;
     }
-    const int base = chunk * kChunk;
-    const int32_t *drafts = L.drafts != nullptr ? L.drafts + (int64_t)r * L.gamma : nullptr;
-    uint32_t has[kVecs];  // which of the thread's tokens have a word
+    const int32_t *drafts = kCounts && L.drafts != nullptr ? L.drafts + (int64_t)r * L.gamma : nullptr;
+    uint32_t has = 0;  // which of the thread's tokens have a word, and the words
+    uint32_t w[kCounts ? kOwn : 1];
+    // vector u of the thread begins at token e(u); its bits are u * kPer on
+    auto e = [&](int u) { return base + (u * kThreads + tid) * kPer; };
+    // mask and draft of 64 rows, a row a lane
+    int mask_of, draft_of;
+    auto look_ahead = [&](int j) {
+      const int row = j + lane;
+      mask_of = draft_of = -1;
+      if (L.mask != nullptr && row < j1) {
+        const int m = L.mask_index != nullptr ? L.mask_index[a + row] : a + row;
+        if (m >= 0 && m < L.n_masks) mask_of = m;
+        else if (m != -1) bits |= kErrLength;
+      }
+      if (drafts != nullptr && row > j0 && row < j1 && row <= L.gamma) {
+        const int v = drafts[row - 1];
+        if ((unsigned)v < (unsigned)L.V) draft_of = v;
+        else if (v != -1) bits |= kErrToken;
+      }
+    };
+    // what row k of the 64 allows of the thread's tokens
+    auto allowed_by = [&](int k) {
+      uint32_t all = (1u << kOwn) - 1;
+      const int m = __builtin_amdgcn_readlane(mask_of, k);
+      if (m < 0) return all;
+      const uint8_t *mask = reinterpret_cast<const uint8_t *>(L.mask + m * L.mask_stride);
+      all = 0;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) has[u] = 0;
-    if (counts && j0 < j1) {
+      for (int u = 0; u < kVecs; ++u)
+        if (e(u) < L.V) all |= ((uint32_t)mask[e(u) / 8] >> (e(u) & 7) & kAll) << (u * kPer);
+      return all;
+    };
+    // the thread's bit of row k's draft, 0 where another thread has it
+    auto draft_bit = [&](int k) -> uint32_t {
+      if (drafts == nullptr) return 0;
+      const int at = __builtin_amdgcn_readlane(draft_of, k) - base;  // of no draft negative
+      if ((unsigned)at >= (unsigned)kChunk || at / kPer % kThreads != tid) return 0;
+      return 1u << (at / kPer / kThreads * kPer + at % kPer);
+    };
+    struct Row {
+      u32x4 v[kVecs], raw[kGrad && kCounts ? kVecs : 1];
+    };
+    auto fetch = [&](Row &o, int j, uint32_t allowed, uint32_t marked, bool every) {
+      const int64_t row = a + j;
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) {
+        // a piece that ends behind the row's last token is read whole: it is aligned, and
+        // so within the page of memory that holds the token
+        const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
+        if (e(u) >= L.V) continue;
+        if (every || (al != 0 && (al != kAll || mk != 0)))
+          o.v[u] = *reinterpret_cast<const u32x4 *>(source + row * stride + e(u));
+        if constexpr (kGrad && kCounts)
+          if (mk != 0 && L.repetition != nullptr)
+            o.raw[u] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const T *>(L.X) +
+                                                        row * L.row_stride + e(u));
+      }
+    };
+    auto finish = [&](const Row &in, int j, uint32_t allowed, uint32_t marked) {
+      T *to = reinterpret_cast<T *>(L.out) + (int64_t)(a + j) * L.out_stride;
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) {
+        const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
+        if (e(u) >= L.V || (in_place && al == kAll && mk == 0)) continue;
+        u32x4 out = in.v[u];
+        if (al != kAll || mk != 0) {
+          float x[kPer];
+          unpack<T>(in.v[u], x);
+          if constexpr (kCounts) {
+            float y[kPer];
+            if constexpr (kGrad) unpack<T>(in.raw[u], y);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (mk >> i & 1) {
+                if constexpr (!kGrad) x[i] = edited(x[i], w[u * kPer + i], rules);
+                else if (L.repetition != nullptr) x[i] = edited_gradient(x[i], y[i], w[u * kPer + i], rules);
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (!(al >> i & 1)) x[i] = kGrad ? 0.0f : -INFINITY;
+          out = pack<T>(x);
+        }
+        if (e(u) + kPer <= L.V) {
+          *reinterpret_cast<u32x4 *>(to + e(u)) = out;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (e(u) + i < L.V) store_piece<T>(to + e(u), out, i);
+        }
+      }
+    };
+
+    Row now;
+    look_ahead(j0);
+    if (!in_place && j0 < j1) fetch(now, j0, 0, 0, true);
+    if (kCounts && j0 < j1) {
       __syncthreads();  // the unit before is done with the words
 #pragma unroll
       for (int i = 0; i < kOwn / 4; ++i)
-        reinterpret_cast<uint4 *>(word)[i * kBlock + tid] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4 *>(word)[i * kThreads + tid] = make_uint4(0, 0, 0, 0);
       __syncthreads();
       auto here = [&](int v) { return (unsigned)(v - base) < (unsigned)kChunk; };
       if (L.n_bias > 0) {
-        each_token(L.bias_ids + (int64_t)r * L.n_bias, L.n_bias, L.V, &bits, [&](int v, int i) {
+        each_token<kThreads>(L.bias_ids + (int64_t)r * L.n_bias, L.n_bias, L.V, &bits, [&](int v, int i) {
           if (here(v)) atomicMax(&word[v - base], (uint32_t)(L.n_bias - i) << kBiasShift);
         });
         __syncthreads();
       }
       if (len > 0)
-        each_token(L.history + (int64_t)r * L.hist_stride, len, L.V, &bits, [&](int v, int i) {
+        each_token<kThreads>(L.history + (int64_t)r * L.hist_stride, len, L.V, &bits, [&](int v, int i) {
           if (!here(v)) return;
           if (i < prompt) atomicOr(&word[v - base], kPromptBit);
           else atomicAdd(&word[v - base], 1u);
         });
       if (drafts != nullptr)
-        each_token(drafts, min(j0, L.gamma), L.V, &bits, [&](int v, int) {
+        each_token<kThreads>(drafts, min(j0, L.gamma), L.V, &bits, [&](int v, int) {
           if (here(v)) atomicAdd(&word[v - base], 1u);
         });
       __syncthreads();
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (word[(u * kBlock + tid) * kPer + i] != 0) has[u] |= 1u << i;
-    }
-    for (int j = j0; j < j1; ++j) {
-      const int64_t row = a + j;
-      if (j > j0 && drafts != nullptr && j <= L.gamma) {
-        const int v = drafts[j - 1];
-        if ((unsigned)v >= (unsigned)L.V) {
-          if (v != -1) bits |= kErrToken;
-        } else if ((unsigned)(v - base) < (unsigned)kChunk) {
-          const int at = (v - base) / kPer;  // its vector of the chunk
-          if (at % kBlock == tid) {
-            word[v - base] += 1;
-#pragma unroll
-            for (int u = 0; u < kVecs; ++u)
-              if (at / kBlock == u) has[u] |= 1u << ((v - base) % kPer);
-          }
-        }
-      }
-      const uint8_t *mask = nullptr;
-      if (L.mask != nullptr) {
-        const int m = L.mask_index != nullptr ? L.mask_index[row] : (int)row;
-        if (m >= 0 && m < L.n_masks) mask = reinterpret_cast<const uint8_t *>(L.mask + m * L.mask_stride);
-        else if (m != -1) bits |= kErrLength;
-      }
-      const T *from = reinterpret_cast<const T *>(kGrad ? L.G : L.X) +
-                      row * (kGrad ? L.g_stride : L.row_stride);
-      const T *raw = reinterpret_cast<const T *>(L.X) + row * L.row_stride;
-      T *to = reinterpret_cast<T *>(L.out) + row * L.out_stride;
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const int e = base + (u * kBlock + tid) * kPer;
-        if (e >= L.V) continue;
-        uint32_t allowed = E::kAll;
-        if (mask != nullptr) allowed = mask[e / 8] >> (e & 7) & E::kAll;
-        const bool whole = e + kPer <= L.V;
-        if (in_place && allowed == E::kAll && has[u] == 0) continue;
-        float x[kPer];
-        u32x4 v;
-        if (allowed != 0 || !whole) {
-          if (whole) {
-            v = *reinterpret_cast<const u32x4 *>(from + e);
-          } else {
-            uint32_t bits16[4] = {0, 0, 0, 0};
-            for (int i = 0; i < L.V - e; ++i)
-              __builtin_memcpy((char *)bits16 + i * sizeof(T), from + e + i, sizeof(T));
-            v = u32x4{bits16[0], bits16[1], bits16[2], bits16[3]};
-          }
-        }
-        if (whole && allowed == E::kAll && has[u] == 0) {
-          *reinterpret_cast<u32x4 *>(to + e) = v;
-          continue;
-        }
-        const T *vs = reinterpret_cast<const T *>(&v);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          x[i] = allowed != 0 ? Elem<T>::at(vs, i) : 0.0f;
-          if (has[u] >> i & 1) {
-            const uint32_t w = word[(u * kBlock + tid) * kPer + i];
-            if constexpr (kGrad) {
-              if (L.repetition != nullptr)
-                x[i] = edited_gradient(x[i], Elem<T>::at(raw, e + i), w, rules);
-            } else {
-              x[i] = edited(x[i], w, rules);
-            }
-          }
-          if (!(allowed >> i & 1)) x[i] = kGrad ? 0.0f : -INFINITY;
-        }
-        if (whole) {
-          T o[kPer];
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) store_elem(o, i, x[i]);
-          u32x4 out;
-          __builtin_memcpy(&out, o, 16);
-          *reinterpret_cast<u32x4 *>(to + e) = out;
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (e + i < L.V) store_elem(to, e + i, x[i]);
-        }
+      for (int i = 0; i < kOwn; ++i) {
+        w[i] = word[(i / kPer * kThreads + tid) * kPer + i % kPer];
+        has |= (w[i] != 0 ? 1u : 0u) << i;
       }
     }
-    // a mask or draft that is wrong is seen by every chunk; the first reports it
-    if (bits && chunk == 0) flag_error(L.err, report ? bits : bits & (kErrToken | kErrLength));
+    for (int jb = j0; jb < j1; jb += kWave) {
+      const int rows = min(j1 - jb, kWave);
+      if (jb > j0) look_ahead(jb);
+      uint32_t al = allowed_by(0), next_al = rows > 1 ? allowed_by(1) : 0;
+      auto count = [&](uint32_t bit) {  // one of the thread's tokens is a draft before this row
+        if constexpr (kCounts) {
+          has |= bit;
+          if (bit != 0) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) w[i] += bit >> i & 1;
+          }
+        }
+      };
+      count(draft_bit(0));
+      if (in_place || jb > j0) fetch(now, jb, al, has, !in_place);
+      else if constexpr (kGrad && kCounts) fetch(now, jb, 0, has, false);  // the raw logits
+      for (int k = 0; k < rows; ++k) {
+        Row next;
+        uint32_t last_al = 0, bit = 0;
+        if (k + 2 < rows) last_al = allowed_by(k + 2);
+        if (k + 1 < rows) {
+          bit = draft_bit(k + 1);
+          fetch(next, jb + k + 1, next_al, has | bit, !in_place);
+        }
+        finish(now, jb + k, al, has);
+        count(bit);
+        now = next;
+        al = next_al;
+        next_al = last_al;
+      }
+    }
+    // every chunk sees what is wrong; the first of them reports it
+    if (bits && chunk == 0) flag_error(L.err, bits);
   }
 }
 
@@ -282,24 +358,30 @@ __global__ __launch_bounds__(kBlock) void history_append_kernel(HistoryLaunch L)
 
 // ----------------------------------------------------------------- launches
 hipError_t launch_edit(const EditLaunch &L, hipStream_t stream) {
-  const int chunks = (L.V + kChunk - 1) / kChunk;
-  const int64_t base = (int64_t)L.R * chunks;
-  const int most = (L.n_rows + L.R - 1) / L.R;
-  int64_t parts = (8 * kComputeUnits + base - 1) / base;
-  if (parts > most) parts = most;
-  const int64_t units = base * parts;
-  const int grid = (int)(units < (1 << 20) ? units : 1 << 20);
-  auto go = [&](auto type, auto grad) {
+  const bool counts = L.history != nullptr || L.drafts != nullptr || L.n_bias > 0;
+  auto go = [&](auto type, auto grad, auto has_counts) {
     using T = decltype(type);
-    constexpr bool kGrad = decltype(grad)::value;
-    DSPARK_LAUNCH(kGrad ? "edit_logits_backward" : "edit_logits", stream, (edit_kernel<T, kGrad>), grid,
-                  kBlock, L, chunks, (int)parts);
+    constexpr bool kGrad = decltype(grad)::value, kCounts = decltype(has_counts)::value;
+    constexpr int kThreads = kBlock;
+    const unsigned chunks = (L.V + kThreads * kOwn - 1) / (kThreads * kOwn);
+    const unsigned base = L.R * chunks;  // R <= 2^22, chunks <= 64
+    const unsigned most = (L.n_rows + L.R - 1) / L.R;
+    unsigned parts = (8 * kComputeUnits + base - 1) / base;
+    if (parts > most) parts = most;
+    const unsigned units = base * parts, grid = units < (1u << 20) ? units : 1u << 20;
+    DSPARK_LAUNCH(kGrad ? "edit_logits_backward" : "edit_logits", stream,
+                  (edit_kernel<T, kGrad, kCounts, kThreads>), grid, kThreads, L, chunks, parts);
   };
-  const bool grad = L.G != nullptr;
-  if (L.bf16 && grad) go(bf16_t(), std::true_type());
-  else if (L.bf16) go(bf16_t(), std::false_type());
-  else if (grad) go(float(), std::true_type());
-  else go(float(), std::false_type());
+  auto with = [&](auto type) {
+    const std::true_type yes;
+    const std::false_type no;
+    if (L.G != nullptr && counts) go(type, yes, yes);
+    else if (L.G != nullptr) go(type, yes, no);
+    else if (counts) go(type, no, yes);
+    else go(type, no, no);
+  };
+  if (L.bf16) with(bf16_t());
+  else with(float());
   return hipGetLastError();
 }
 
