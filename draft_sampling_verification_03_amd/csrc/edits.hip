@@ -24,59 +24,79 @@ namespace {
 constexpr int kCountBits = 21, kBiasShift = 22;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1, kPromptBit = 1u << kCountBits;
 constexpr int kOwn = 16;  // tokens of a thread
+constexpr int kRequestsX = 1 << 16;  // requests along the grid's first dimension
 
-// f(token, index) for the tokens [0, n) at p, spread over the workgroup; -1 is skipped,
-// what lies outside the vocabulary sets *bits.  16-byte loads, four of them in flight.
-template <int kThreads, typename F>
-__device__ __forceinline__ void each_token(const int32_t *p, int n, int V, int *bits, F f) {
-  auto one = [&](int v, int i) __attribute__((always_inline)) {
-    if ((unsigned)v < (unsigned)V) f(v, i);
-    else if (v != -1) *bits |= kErrToken;
-  };
-  const int tid = threadIdx.x;
-  const int head = min(n, (int)((16 - ((uintptr_t)p & 15)) & 15) / 4);
-  const int quads = (n - head) / 4, tail = head + 4 * quads;
-  const int4 *mid = reinterpret_cast<const int4 *>(p + head);
-  for (int q0 = tid; q0 < quads; q0 += 4 * kThreads) {
-    int4 v[4];
+// The tokens [0, n) at p, spread over the workgroup in 16-byte pieces: load() brings the
+// first of them on their way, each() calls f(token, index) for all; -1 is skipped, what
+// lies outside the vocabulary sets *bits.
+template <int kThreads, int kFlight> struct Tokens {
+  const int32_t *p;
+  int n, head, quads;
+  int4 v[kFlight];
+  __device__ __forceinline__ Tokens(const int32_t *at, int count) : p(at), n(count) {
+    head = min(n, (int)((16 - ((uintptr_t)p & 15)) & 15) / 4);
+    quads = (n - head) / 4;
+  }
+  __device__ __forceinline__ void load(int q0) {
+    const int4 *mid = reinterpret_cast<const int4 *>(p + head);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kFlight; ++i) {
       const int q = q0 + i * kThreads;
-      v[i] = q < quads ? mid[q] : make_int4(-1, -1, -1, -1);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = head + 4 * (q0 + i * kThreads);
-      one(v[i].x, at);
-      one(v[i].y, at + 1);
-      one(v[i].z, at + 2);
-      one(v[i].w, at + 3);
+      v[i] = make_int4(-1, -1, -1, -1);
+      if (q < quads) v[i] = mid[q];
     }
   }
-  if (tid < head) one(p[tid], tid);
-  if (tid < n - tail) one(p[tail + tid], tail + tid);
-}
+  __device__ __forceinline__ void load() { load(threadIdx.x); }
+  template <typename F> __device__ __forceinline__ void each(int V, int *bits, F f) {
+    auto one = [&](int v, int i) __attribute__((always_inline)) {
+      if ((unsigned)v < (unsigned)V) f(v, i);
+      else if (v != -1) *bits |= kErrToken;
+    };
+    const int tid = threadIdx.x, tail = head + 4 * quads;
+    for (int q0 = tid;;) {
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int at = head + 4 * (q0 + i * kThreads);
+        one(v[i].x, at);
+        one(v[i].y, at + 1);
+        one(v[i].z, at + 2);
+        one(v[i].w, at + 3);
+      }
+      q0 += kFlight * kThreads;
+      if (q0 >= quads) break;
+      load(q0);
+    }
+    if (tid < head) one(p[tid], tid);
+    if (tid < n - tail) one(p[tail + tid], tail + tid);
+  }
+};
 
-template <typename T> __device__ __forceinline__ void unpack(u32x4 v, float *x) {
+// Element i of a piece, i known at compile time.
+template <typename T> __device__ __forceinline__ float element(u32x4 v, int i) {
+  if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+  else return __uint_as_float(v[i]);
+}
+template <typename T> __device__ __forceinline__ void set_element(u32x4 &v, int i, float x) {
   if constexpr (sizeof(T) == 2) {
-    const u16x8 h = __builtin_bit_cast(u16x8, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = bf16_to_f32(h[i]);
+    const uint32_t h = __builtin_bit_cast(uint16_t, (__bf16)x);
+    v[i / 2] = i & 1 ? h << 16 | (v[i / 2] & 0xFFFFu) : (v[i / 2] & 0xFFFF0000u) | h;
   } else {
-    const floatx4 f = __builtin_bit_cast(floatx4, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = f[i];
+    v[i] = __float_as_uint(x);
   }
 }
-template <typename T> __device__ __forceinline__ u32x4 pack(const float *x) {
-  if constexpr (sizeof(T) == 2) {
-    bf16x8 h;
+// The piece with `none` (a whole dword of it) in the elements that `allowed` leaves out.
+template <typename T> __device__ __forceinline__ u32x4 masked(u32x4 v, uint32_t allowed, uint32_t none) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (__bf16)x[i];
-    return __builtin_bit_cast(u32x4, h);
-  } else {
-    return __builtin_bit_cast(u32x4, floatx4{x[0], x[1], x[2], x[3]});
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t lo = allowed >> (2 * k) & 1 ? 0xFFFFu : 0;
+      const uint32_t keep = lo | (allowed >> (2 * k + 1) & 1 ? 0xFFFF0000u : 0);
+      v[k] = (v[k] & keep) | (none & ~keep);
+    } else {
+      v[k] = allowed >> k & 1 ? v[k] : none;
+    }
   }
+  return v;
 }
 // element i of a piece
 template <typename T> __device__ __forceinline__ void store_piece(T *to, u32x4 v, int i) {
@@ -108,218 +128,278 @@ __device__ __forceinline__ float edited_gradient(float g, float x, uint32_t w, c
   return g;
 }
 
-__device__ __forceinline__ float parameter(const float *p, int r, float none, float lo, float hi,
-                                           int *bits) {
-  if (p == nullptr) return none;
-  const float v = p[r];
-  if (v >= lo && v <= hi) return v;
-  *bits |= kErrNonFinite;
-  return none;
+// What a unit needs of its request, from as many arrays: a lane each, so that all of them
+// are one load and one wait.
+struct Request {
+  int a, n;         // its rows [a, a + n)
+  int len, prompt;  // its history
+  Rules rules;
+  int bits;
+};
+__device__ __forceinline__ Request request_of(const EditLaunch &L, int r) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int32_t *at = nullptr;
+  auto from = [&](int i, const void *p, int add) {
+    if (lane == i && p != nullptr) at = reinterpret_cast<const int32_t *>(p) + r + add;
+  };
+  from(0, L.row_offset, 0);
+  from(1, L.row_offset, 1);
+  from(2, L.hist_len, 0);
+  from(3, L.prompt_len, 0);
+  from(4, L.repetition, 0);
+  from(5, L.frequency, 0);
+  from(6, L.presence, 0);
+  int v = lane == 4 ? __float_as_int(1.0f) : 0;
+  if (at != nullptr) v = *at;
+  auto get = [&](int i) { return __builtin_amdgcn_readlane(v, i); };
+  Request q;
+  q.a = r, q.n = 1, q.bits = 0;
+  if (L.row_offset != nullptr) {
+    q.a = get(0);
+    const int b = get(1);
+    const bool bad = q.a < 0 || b < q.a || b > L.n_rows;
+    if (bad) q.bits |= kErrLength;
+    q.n = bad ? 0 : b - q.a;
+  }
+  q.len = get(2), q.prompt = get(3);
+  if (q.len < 0 || q.len > L.hist_stride) q.bits |= kErrLength, q.len = 0;
+  if (q.prompt < 0 || q.prompt > q.len) q.bits |= kErrLength, q.prompt = 0;
+  auto parameter = [&](int i, float lo, float hi, float none) {
+    const float x = __int_as_float(get(i));
+    if (x >= lo && x <= hi) return x;
+    q.bits |= kErrNonFinite;
+    return none;
+  };
+  q.rules.repetition = parameter(4, 1e-3f, 1e3f, 1.0f);
+  q.rules.frequency = parameter(5, -FLT_MAX, FLT_MAX, 0.0f);
+  q.rules.presence = parameter(6, -FLT_MAX, FLT_MAX, 0.0f);
+  q.rules.inverse = 1.0f / q.rules.repetition;
+  q.rules.bias_end = L.bias + ((int64_t)r + 1) * L.n_bias;
+  return q;
 }
 
 }  // namespace
 
-// Units of work: (request, part of its rows, chunk), chunks innermost.  kCounts: whether
-// histories, drafts or biases are given at all.
+// A workgroup takes one (request, part of its rows, chunk).  The chunks of a row follow one
+// another (for each chunk all rows in turn: 157 us for 141 where nothing is edited), but
+// the first chunks of all requests come before the others: the low tokens are the
+// frequent ones, so there is most to edit.  One and not several in turn: what the compiler
+// would keep in registers from one to the next cost half of the waves.
+// kCounts: whether histories, drafts or biases are given at all; kMask: whether masks are.
 //
-// The rows are a pipeline: the mask bits of row j + 2 and the logits of row j + 1 are on
-// their way while row j is edited and stored.
-template <typename T, bool kGrad, bool kCounts, int kThreads>
+// The rows are a pipeline: row j + 1 is on its way while row j is edited and stored; in
+// place, where the masks say what is to be read, those of row j + 2 too.  Its loads are
+// all made, so that the compiler can count which of them a step waits for: where a piece
+// is not wanted (past the vocabulary, in place where nothing changes) the lane reads the
+// row's first piece, which all lanes share.
+template <typename T, bool kGrad, bool kCounts, bool kMask, bool kInPlace, int kThreads>
 __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned chunks, unsigned parts) {
   constexpr int kPer = Elem<T>::kPerVec, kVecs = kOwn / kPer, kChunk = kThreads * kOwn;
-  constexpr uint32_t kAll = (1u << kPer) - 1;
+  constexpr uint32_t kAll = (1u << kPer) - 1, kWhole = (1u << kOwn) - 1;
+  constexpr bool kRaw = kGrad && kCounts;  // the raw logits too
   __shared__ __attribute__((aligned(16))) uint32_t word[kCounts ? kChunk : 4];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const unsigned units = L.R * parts * chunks;
-  const bool in_place = L.out == (kGrad ? L.G : L.X);
+  const bool raw_too = kRaw && L.repetition != nullptr;
   const T *source = reinterpret_cast<const T *>(kGrad ? L.G : L.X);
-  const int64_t stride = kGrad ? L.g_stride : L.row_stride;
-  for (unsigned unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const unsigned rest = unit / chunks, r = rest / parts, part = rest % parts;
-    const int chunk = unit % chunks, base = chunk * kChunk;
-    int bits = 0, a = r, n = 1;
-    if (L.row_offset != nullptr) {
-      a = L.row_offset[r];
-      const int b = L.row_offset[r + 1];
-      const bool bad = a < 0 || b < a || b > L.n_rows;
-      if (bad) bits |= kErrLength;
-      n = bad ? 0 : b - a;
-    }
-    const int j0 = (int)((int64_t)n * part / parts), j1 = (int)((int64_t)n * (part + 1) / parts);
-    Rules rules;
-    rules.repetition = parameter(L.repetition, r, 1.0f, 1e-3f, 1e3f, &bits);
-    rules.frequency = parameter(L.frequency, r, 0.0f, -FLT_MAX, FLT_MAX, &bits);
-    rules.presence = parameter(L.presence, r, 0.0f, -FLT_MAX, FLT_MAX, &bits);
-    rules.inverse = 1.0f / rules.repetition;
-    rules.bias_end = L.n_bias > 0 ? L.bias + ((int64_t)r + 1) * L.n_bias : nullptr;
-    int len = 0, prompt = 0;
-    if (kCounts && L.history != nullptr) {
-      len = L.hist_len[r];
-      if (len < 0 || len > L.hist_stride) bits |= kErrLength, len = 0;
-      prompt = L.prompt_len != nullptr ? L.prompt_len[r] : 0;
-      if (prompt < 0 || prompt > len) bits |= kErrLength, prompt = 0;
-    }
-    const int32_t *drafts = kCounts && L.drafts != nullptr ? L.drafts + (int64_t)r * L.gamma : nullptr;
-    uint32_t has = 0;  // which of the thread's tokens have a word, and the words
-    uint32_t w[kCounts ? kOwn : 1];
-    // vector u of the thread begins at token e(u); its bits are u * kPer on
-    auto e = [&](int u) { return base + (u * kThreads + tid) * kPer; };
-    // mask and draft of 64 rows, a row a lane
-    int mask_of, draft_of;
-    auto look_ahead = [&](int j) {
-      const int row = j + lane;
-      mask_of = draft_of = -1;
-      if (L.mask != nullptr && row < j1) {
-        const int m = L.mask_index != nullptr ? L.mask_index[a + row] : a + row;
-        if (m >= 0 && m < L.n_masks) mask_of = m;
-        else if (m != -1) bits |= kErrLength;
-      }
-      if (drafts != nullptr && row > j0 && row < j1 && row <= L.gamma) {
-        const int v = drafts[row - 1];
-        if ((unsigned)v < (unsigned)L.V) draft_of = v;
-        else if (v != -1) bits |= kErrToken;
-      }
-    };
-    // what row k of the 64 allows of the thread's tokens
-    auto allowed_by = [&](int k) {
-      uint32_t all = (1u << kOwn) - 1;
+  const T *raw = raw_too ? reinterpret_cast<const T *>(L.X) : source;
+  const int64_t stride = kGrad ? L.g_stride : L.row_stride, raw_stride = raw_too ? L.row_stride : stride;
+  const unsigned per_chunk = gridDim.x / chunks, late = blockIdx.x - per_chunk;
+  const bool first = !kCounts || blockIdx.x < per_chunk;
+  const unsigned unit = kCounts ? (first ? blockIdx.x : late / (chunks - 1)) : blockIdx.x / chunks;
+  const unsigned part = unit % parts, r = unit / parts + blockIdx.y * kRequestsX;
+  if (r >= (unsigned)L.R) return;
+  const int chunk = kCounts ? (first ? 0 : 1 + late % (chunks - 1)) : blockIdx.x % chunks;
+  const int base = chunk * kChunk;
+  const Request q = request_of(L, r);
+  const int a = q.a, j0 = (int)((int64_t)q.n * part / parts);
+  const int j1 = (int)((int64_t)q.n * (part + 1) / parts);
+  int bits = q.bits;
+  if (j0 == j1) {
+    if (bits && chunk == 0) flag_error(L.err, bits);
+    return;
+  }
+  const int32_t *drafts = kCounts && L.drafts != nullptr ? L.drafts + (int64_t)r * L.gamma : nullptr;
+  uint32_t has = 0;  // which of the thread's tokens have a word
+  // vector u of the thread begins at token e(u); its bits are u * kPer on
+  auto e = [&](int u) { return base + (u * kThreads + tid) * kPer; };
+  // mask and draft of 64 rows, a row a lane (out of range: as they are found)
+  int mask_of, draft_of;
+  auto look_ahead = [&](int j) {
+    const int row = j + lane;
+    mask_of = draft_of = -1;
+    if (kMask && row < j1) mask_of = L.mask_index != nullptr ? L.mask_index[a + row] : a + row;
+    if (drafts != nullptr && row > j0 && row < j1 && row <= L.gamma) draft_of = drafts[row - 1];
+  };
+  auto check_ahead = [&]() {
+    if (kMask && (mask_of < -1 || mask_of >= L.n_masks)) bits |= kErrLength, mask_of = -1;
+    if (kCounts && draft_of != -1 && (unsigned)draft_of >= (unsigned)L.V) bits |= kErrToken, draft_of = -1;
+  };
+  struct Allowed { uint32_t v[kMask ? kVecs : 1]; };  // bytes of a mask as they come
+  auto load_mask = [&](Allowed &o, int k) {
+    if constexpr (kMask) {
       const int m = __builtin_amdgcn_readlane(mask_of, k);
-      if (m < 0) return all;
-      const uint8_t *mask = reinterpret_cast<const uint8_t *>(L.mask + m * L.mask_stride);
-      all = 0;
+      const uint8_t *mask = reinterpret_cast<const uint8_t *>(L.mask + (m < 0 ? 0 : m) * L.mask_stride);
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) o.v[u] = mask[e(u) < L.V ? e(u) / 8 : 0];
+    }
+  };
+  auto bits_of = [&](const Allowed &o, int k) {
+    if constexpr (!kMask) return kWhole;
+    uint32_t all = 0;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) all |= (o.v[u] >> (e(u) & 7) & kAll) << (u * kPer);
+    return __builtin_amdgcn_readlane(mask_of, k) < 0 ? kWhole : all;
+  };
+  // the thread's bit of row k's draft, 0 where another thread has it
+  auto draft_bit = [&](int k) -> uint32_t {
+    if (!kCounts || drafts == nullptr) return 0;
+    const int at = __builtin_amdgcn_readlane(draft_of, k) - base;  // of no draft negative
+    if ((unsigned)at >= (unsigned)kChunk || at / kPer % kThreads != tid) return 0;
+    return 1u << (at / kPer / kThreads * kPer + at % kPer);
+  };
+  auto count = [&](uint32_t bit) {  // one of the thread's tokens is a draft before this row
+    if constexpr (kCounts) {
+      has |= bit;
+      if (bit != 0) {
+        const int i = __ffs(bit) - 1;
+        word[(i / kPer * kThreads + tid) * kPer + i % kPer] += 1;
+      }
+    }
+  };
+  struct Row {
+    u32x4 v[kVecs], raw[kRaw ? kVecs : 1];
+    Allowed mask;
+  };
+  // A piece that ends behind the row's last token is read whole: it is aligned, and so
+  // within the page of memory that holds the token.
+  auto load_piece = [&](const T *from, int u, bool wanted) {
+    return *reinterpret_cast<const u32x4 *>(from + (wanted && e(u) < L.V ? e(u) : 0));
+  };
+  auto load_row = [&](Row &o, int j, uint32_t allowed, uint32_t marked) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
+      o.v[u] = load_piece(source + (a + j) * stride, u, !kInPlace || (al != 0 && (al != kAll || mk != 0)));
+    }
+  };
+  auto load_raw = [&](Row &o, int j, uint32_t marked) {
+    if constexpr (kRaw)
 #pragma unroll
       for (int u = 0; u < kVecs; ++u)
-        if (e(u) < L.V) all |= ((uint32_t)mask[e(u) / 8] >> (e(u) & 7) & kAll) << (u * kPer);
-      return all;
-    };
-    // the thread's bit of row k's draft, 0 where another thread has it
-    auto draft_bit = [&](int k) -> uint32_t {
-      if (drafts == nullptr) return 0;
-      const int at = __builtin_amdgcn_readlane(draft_of, k) - base;  // of no draft negative
-      if ((unsigned)at >= (unsigned)kChunk || at / kPer % kThreads != tid) return 0;
-      return 1u << (at / kPer / kThreads * kPer + at % kPer);
-    };
-    struct Row {
-      u32x4 v[kVecs], raw[kGrad && kCounts ? kVecs : 1];
-    };
-    auto fetch = [&](Row &o, int j, uint32_t allowed, uint32_t marked, bool every) {
-      const int64_t row = a + j;
+        o.raw[u] = load_piece(raw + (a + j) * raw_stride, u, raw_too && (marked >> (u * kPer) & kAll) != 0);
+  };
+  auto finish = [&](const Row &in, int j, uint32_t allowed, uint32_t marked) {
+    T *to = reinterpret_cast<T *>(L.out) + (a + j) * L.out_stride;
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        // a piece that ends behind the row's last token is read whole: it is aligned, and
-        // so within the page of memory that holds the token
-        const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
-        if (e(u) >= L.V) continue;
-        if (every || (al != 0 && (al != kAll || mk != 0)))
-          o.v[u] = *reinterpret_cast<const u32x4 *>(source + row * stride + e(u));
-        if constexpr (kGrad && kCounts)
-          if (mk != 0 && L.repetition != nullptr)
-            o.raw[u] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const T *>(L.X) +
-                                                        row * L.row_stride + e(u));
-      }
-    };
-    auto finish = [&](const Row &in, int j, uint32_t allowed, uint32_t marked) {
-      T *to = reinterpret_cast<T *>(L.out) + (int64_t)(a + j) * L.out_stride;
+    for (int u = 0; u < kVecs; ++u) {
+      const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
+      u32x4 out = in.v[u];
+      if constexpr (kCounts) {
+        const uint32_t edit = !kGrad || raw_too ? mk & al : 0;
+        if (edit != 0) {
+          uint32_t w[kPer];
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
-        if (e(u) >= L.V || (in_place && al == kAll && mk == 0)) continue;
-        u32x4 out = in.v[u];
-        if (al != kAll || mk != 0) {
-          float x[kPer];
-          unpack<T>(in.v[u], x);
-          if constexpr (kCounts) {
-            float y[kPer];
-            if constexpr (kGrad) unpack<T>(in.raw[u], y);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (mk >> i & 1) {
-                if constexpr (!kGrad) x[i] = edited(x[i], w[u * kPer + i], rules);
-                else if (L.repetition != nullptr) x[i] = edited_gradient(x[i], y[i], w[u * kPer + i], rules);
-              }
-          }
+          for (int i = 0; i < kPer; ++i) w[i] = word[(u * kThreads + tid) * kPer + i];
 #pragma unroll
           for (int i = 0; i < kPer; ++i)
-            if (!(al >> i & 1)) x[i] = kGrad ? 0.0f : -INFINITY;
-          out = pack<T>(x);
-        }
-        if (e(u) + kPer <= L.V) {
-          *reinterpret_cast<u32x4 *>(to + e(u)) = out;
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (e(u) + i < L.V) store_piece<T>(to + e(u), out, i);
+            if (edit >> i & 1) {
+              float x = element<T>(out, i);
+              if constexpr (kGrad) x = edited_gradient(x, element<T>(in.raw[u], i), w[i], q.rules);
+              else x = edited(x, w[i], q.rules);
+              set_element<T>(out, i, x);
+            }
         }
       }
-    };
+      if (kMask && al != kAll)
+        out = masked<T>(out, al, kGrad ? 0 : sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u);
+      if (e(u) >= L.V || (kInPlace && al == kAll && mk == 0)) continue;
+      if (e(u) + kPer <= L.V) {
+        *reinterpret_cast<u32x4 *>(to + e(u)) = out;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (e(u) + i < L.V) store_piece<T>(to + e(u), out, i);
+      }
+    }
+  };
 
-    Row now;
-    look_ahead(j0);
-    if (!in_place && j0 < j1) fetch(now, j0, 0, 0, true);
-    if (kCounts && j0 < j1) {
-      __syncthreads();  // the unit before is done with the words
+  // everything that does not wait for the words is on its way before them
+  Tokens<kThreads, 4> past(L.history + (int64_t)r * L.hist_stride, q.len);
+  Tokens<kThreads, 1> ids(L.bias_ids + (int64_t)r * L.n_bias, L.n_bias);
+  Tokens<kThreads, 1> before(drafts, drafts != nullptr ? min(j0, L.gamma) : 0);
+  Row even, odd;
+  if (kCounts) ids.load();
+  if (kCounts) past.load();
+  if (kCounts) before.load();
+  look_ahead(j0);
+  if (!kInPlace) load_row(even, j0, 0, 0);
+  if (kCounts) {
 #pragma unroll
-      for (int i = 0; i < kOwn / 4; ++i)
-        reinterpret_cast<uint4 *>(word)[i * kThreads + tid] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kOwn / 4; ++i)
+      reinterpret_cast<uint4 *>(word)[i * kThreads + tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    auto here = [&](int v) { return (unsigned)(v - base) < (unsigned)kChunk; };
+    if (L.n_bias > 0) {
+      ids.each(L.V, &bits, [&](int v, int i) {
+        if (here(v)) atomicMax(&word[v - base], (uint32_t)(L.n_bias - i) << kBiasShift);
+      });
       __syncthreads();
-      auto here = [&](int v) { return (unsigned)(v - base) < (unsigned)kChunk; };
-      if (L.n_bias > 0) {
-        each_token<kThreads>(L.bias_ids + (int64_t)r * L.n_bias, L.n_bias, L.V, &bits, [&](int v, int i) {
-          if (here(v)) atomicMax(&word[v - base], (uint32_t)(L.n_bias - i) << kBiasShift);
-        });
-        __syncthreads();
-      }
-      if (len > 0)
-        each_token<kThreads>(L.history + (int64_t)r * L.hist_stride, len, L.V, &bits, [&](int v, int i) {
-          if (!here(v)) return;
-          if (i < prompt) atomicOr(&word[v - base], kPromptBit);
-          else atomicAdd(&word[v - base], 1u);
-        });
-      if (drafts != nullptr)
-        each_token<kThreads>(drafts, min(j0, L.gamma), L.V, &bits, [&](int v, int) {
-          if (here(v)) atomicAdd(&word[v - base], 1u);
-        });
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        w[i] = word[(i / kPer * kThreads + tid) * kPer + i % kPer];
-        has |= (w[i] != 0 ? 1u : 0u) << i;
-      }
     }
-    for (int jb = j0; jb < j1; jb += kWave) {
-      const int rows = min(j1 - jb, kWave);
-      if (jb > j0) look_ahead(jb);
-      uint32_t al = allowed_by(0), next_al = rows > 1 ? allowed_by(1) : 0;
-      auto count = [&](uint32_t bit) {  // one of the thread's tokens is a draft before this row
-        if constexpr (kCounts) {
-          has |= bit;
-          if (bit != 0) {
+    past.each(L.V, &bits, [&](int v, int i) {
+      if (!here(v)) return;
+      if (i < q.prompt) atomicOr(&word[v - base], kPromptBit);
+      else atomicAdd(&word[v - base], 1u);
+    });
+    before.each(L.V, &bits, [&](int v, int) {
+      if (here(v)) atomicAdd(&word[v - base], 1u);
+    });
+    __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) w[i] += bit >> i & 1;
-          }
-        }
-      };
-      count(draft_bit(0));
-      if (in_place || jb > j0) fetch(now, jb, al, has, !in_place);
-      else if constexpr (kGrad && kCounts) fetch(now, jb, 0, has, false);  // the raw logits
-      for (int k = 0; k < rows; ++k) {
-        Row next;
-        uint32_t last_al = 0, bit = 0;
-        if (k + 2 < rows) last_al = allowed_by(k + 2);
-        if (k + 1 < rows) {
-          bit = draft_bit(k + 1);
-          fetch(next, jb + k + 1, next_al, has | bit, !in_place);
-        }
-        finish(now, jb + k, al, has);
-        count(bit);
-        now = next;
-        al = next_al;
-        next_al = last_al;
-      }
-    }
-    // every chunk sees what is wrong; the first of them reports it
-    if (bits && chunk == 0) flag_error(L.err, bits);
+    for (int i = 0; i < kOwn; ++i)
+      has |= (word[(i / kPer * kThreads + tid) * kPer + i % kPer] != 0 ? 1u : 0u) << i;
   }
+  for (int jb = j0; jb < j1; jb += kWave) {
+    const int last = min(j1 - jb, kWave) - 1;
+    if (jb > j0) look_ahead(jb);
+    check_ahead();
+    count(draft_bit(0));
+    Allowed ahead;         // in place: the masks of the row after next
+    uint32_t al = kWhole;  // and what this row allows
+    if constexpr (kInPlace) {
+      Allowed first;
+      load_mask(first, 0);
+      load_mask(ahead, min(1, last));
+      al = bits_of(first, 0);
+      load_row(even, jb, al, has);
+    } else {
+      if (jb > j0) load_row(even, jb, 0, 0);
+      load_mask(even.mask, 0);
+    }
+    load_raw(even, jb, has);
+    auto step = [&](const Row &now, Row &next, int k) {
+      const int k1 = min(k + 1, last);
+      const uint32_t bit = k < last ? draft_bit(k1) : 0;
+      uint32_t next_al = kWhole;
+      if constexpr (kInPlace) {
+        next_al = bits_of(ahead, k1);
+        load_mask(ahead, min(k + 2, last));
+      } else {
+        load_mask(next.mask, k1);
+      }
+      load_row(next, jb + k1, next_al, has | bit);
+      load_raw(next, jb + k1, has | bit);
+      if constexpr (!kInPlace) al = bits_of(now.mask, k);
+      finish(now, jb + k, al, has);
+      count(bit);
+      al = next_al;
+    };
+    for (int k = 0; k <= last; k += 2) {
+      step(even, odd, k);
+      if (k < last) step(odd, even, k + 1);
+    }
+  }
+  // every chunk sees what is wrong; the first of them reports it
+  if (bits && chunk == 0) flag_error(L.err, bits);
 }
 
 // One workgroup a request.
@@ -359,26 +439,36 @@ __global__ __launch_bounds__(kBlock) void history_append_kernel(HistoryLaunch L)
 // ----------------------------------------------------------------- launches
 hipError_t launch_edit(const EditLaunch &L, hipStream_t stream) {
   const bool counts = L.history != nullptr || L.drafts != nullptr || L.n_bias > 0;
-  auto go = [&](auto type, auto grad, auto has_counts) {
+  auto go = [&](auto type, auto grad, auto has_counts, auto has_mask, auto in_place) {
     using T = decltype(type);
     constexpr bool kGrad = decltype(grad)::value, kCounts = decltype(has_counts)::value;
+    constexpr bool kMask = decltype(has_mask)::value, kInPlace = decltype(in_place)::value;
     constexpr int kThreads = kBlock;
     const unsigned chunks = (L.V + kThreads * kOwn - 1) / (kThreads * kOwn);
     const unsigned base = L.R * chunks;  // R <= 2^22, chunks <= 64
     const unsigned most = (L.n_rows + L.R - 1) / L.R;
     unsigned parts = (8 * kComputeUnits + base - 1) / base;
     if (parts > most) parts = most;
-    const unsigned units = base * parts, grid = units < (1u << 20) ? units : 1u << 20;
+    const dim3 grid((L.R < kRequestsX ? L.R : kRequestsX) * chunks * parts,
+                    (L.R + kRequestsX - 1) / kRequestsX);
     DSPARK_LAUNCH(kGrad ? "edit_logits_backward" : "edit_logits", stream,
-                  (edit_kernel<T, kGrad, kCounts, kThreads>), grid, kThreads, L, chunks, parts);
+                  (edit_kernel<T, kGrad, kCounts, kMask, kInPlace, kThreads>), grid, kThreads, L, chunks,
+                  parts);
+  };
+  // run time to compile time, one condition after another
+  auto on = [](bool b, auto f) {
+    if (b) f(std::true_type());
+    else f(std::false_type());
   };
   auto with = [&](auto type) {
-    const std::true_type yes;
-    const std::false_type no;
-    if (L.G != nullptr && counts) go(type, yes, yes);
-    else if (L.G != nullptr) go(type, yes, no);
-    else if (counts) go(type, no, yes);
-    else go(type, no, no);
+    on(L.G != nullptr, [&](auto grad) {
+      on(counts, [&](auto has_counts) {
+        on(L.mask != nullptr, [&](auto has_mask) {
+          on(L.out == (L.G != nullptr ? L.G : L.X),
+             [&](auto in_place) { go(type, grad, has_counts, has_mask, in_place); });
+        });
+      });
+    });
   };
   if (L.bf16) with(bf16_t());
   else with(float());
