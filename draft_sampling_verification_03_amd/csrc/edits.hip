@@ -24,11 +24,16 @@ namespace {
 constexpr int kCountBits = 21, kBiasShift = 22;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1, kPromptBit = 1u << kCountBits;
 constexpr int kOwn = 16;  // tokens of a thread
+// A part of a request's rows counts the history anew, so it has a row at least for so many
+// of its tokens: histories of up to 120000 for 1 to 5 rows 61 us, 79 where every row was a part.
+constexpr int kTokensARow = 4096;
 constexpr int kRequestsX = 1 << 16;  // requests along the grid's first dimension
 
 // The tokens [0, n) at p, spread over the workgroup in 16-byte pieces: load() brings the
-// first of them on their way, each() calls f(token, index) for all; -1 is skipped, what
-// lies outside the vocabulary sets *bits.
+// first of them on their way, each() calls f(token, index, mode) for all, -1 and what is
+// wrong among them.  mode is a constant: whether the indexes of the wave's call are all
+// below `border`, all from it on, or mixed.
+enum Side { kBelow, kFrom, kMixed };
 template <int kThreads, int kFlight> struct Tokens {
   const int32_t *p;
   int n, head, quads;
@@ -47,27 +52,29 @@ template <int kThreads, int kFlight> struct Tokens {
     }
   }
   __device__ __forceinline__ void load() { load(threadIdx.x); }
-  template <typename F> __device__ __forceinline__ void each(int V, int *bits, F f) {
-    auto one = [&](int v, int i) __attribute__((always_inline)) {
-      if ((unsigned)v < (unsigned)V) f(v, i);
-      else if (v != -1) *bits |= kErrToken;
-    };
+  template <typename F> __device__ __forceinline__ void each(int border, F f) {
     const int tid = threadIdx.x, tail = head + 4 * quads;
-    for (int q0 = tid;;) {
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave) * kWave;
+    auto quad = [&](const int4 &x, int at, auto mode) {
+      f(x.x, at, mode);
+      f(x.y, at + 1, mode);
+      f(x.z, at + 2, mode);
+      f(x.w, at + 3, mode);
+    };
+    for (int step = 0; step < quads; step += kFlight * kThreads) {
+      if (step > 0) load(step + tid);
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
-        const int at = head + 4 * (q0 + i * kThreads);
-        one(v[i].x, at);
-        one(v[i].y, at + 1);
-        one(v[i].z, at + 2);
-        one(v[i].w, at + 3);
+        const int q = step + i * kThreads, first = head + 4 * (q + wave), at = head + 4 * (q + tid);
+        if (q + wave >= quads) break;
+        if (first >= border) quad(v[i], at, std::integral_constant<Side, kFrom>());
+        else if (first + 4 * kWave <= border) quad(v[i], at, std::integral_constant<Side, kBelow>());
+        else quad(v[i], at, std::integral_constant<Side, kMixed>());
       }
-      q0 += kFlight * kThreads;
-      if (q0 >= quads) break;
-      load(q0);
     }
-    if (tid < head) one(p[tid], tid);
-    if (tid < n - tail) one(p[tail + tid], tail + tid);
+    const std::integral_constant<Side, kMixed> mixed;
+    if (tid < head) f(p[tid], tid, mixed);
+    if (tid < n - tail) f(p[tail + tid], tail + tid, mixed);
   }
 };
 
@@ -180,11 +187,11 @@ __device__ __forceinline__ Request request_of(const EditLaunch &L, int r) {
 
 }  // namespace
 
-// A workgroup takes one (request, part of its rows, chunk).  The chunks of a row follow one
-// another (for each chunk all rows in turn: 157 us for 141 where nothing is edited), but
-// the first chunks of all requests come before the others: the low tokens are the
-// frequent ones, so there is most to edit.  One and not several in turn: what the compiler
-// would keep in registers from one to the next cost half of the waves.
+// A workgroup takes one (request, part of its rows, chunk), chunks innermost.  A chunk is
+// not one stretch of the vocabulary but every so many of its spans, a span being what one
+// load of a wave covers: the frequent tokens are the low ones, and this way every chunk
+// has some of them to count and edit.  One unit and not several in turn: what the
+// compiler would keep in registers from one to the next cost half of the waves.
 // kCounts: whether histories, drafts or biases are given at all; kMask: whether masks are.
 //
 // The rows are a pipeline: row j + 1 is on its way while row j is edited and stored; in
@@ -195,6 +202,7 @@ __device__ __forceinline__ Request request_of(const EditLaunch &L, int r) {
 template <typename T, bool kGrad, bool kCounts, bool kMask, bool kInPlace, int kThreads>
 __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned chunks, unsigned parts) {
   constexpr int kPer = Elem<T>::kPerVec, kVecs = kOwn / kPer, kChunk = kThreads * kOwn;
+  constexpr int kSpan = kWave * kPer;  // tokens that one load of a wave covers
   constexpr uint32_t kAll = (1u << kPer) - 1, kWhole = (1u << kOwn) - 1;
   constexpr bool kRaw = kGrad && kCounts;  // the raw logits too
   __shared__ __attribute__((aligned(16))) uint32_t word[kCounts ? kChunk : 4];
@@ -203,16 +211,15 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
   const T *source = reinterpret_cast<const T *>(kGrad ? L.G : L.X);
   const T *raw = raw_too ? reinterpret_cast<const T *>(L.X) : source;
   const int64_t stride = kGrad ? L.g_stride : L.row_stride, raw_stride = raw_too ? L.row_stride : stride;
-  const unsigned per_chunk = gridDim.x / chunks, late = blockIdx.x - per_chunk;
-  const bool first = !kCounts || blockIdx.x < per_chunk;
-  const unsigned unit = kCounts ? (first ? blockIdx.x : late / (chunks - 1)) : blockIdx.x / chunks;
-  const unsigned part = unit % parts, r = unit / parts + blockIdx.y * kRequestsX;
+  const unsigned chunk = blockIdx.x % chunks, unit = blockIdx.x / chunks;
+  const unsigned r = unit / parts + blockIdx.y * kRequestsX;
+  const int part = unit % parts;
   if (r >= (unsigned)L.R) return;
-  const int chunk = kCounts ? (first ? 0 : 1 + late % (chunks - 1)) : blockIdx.x % chunks;
-  const int base = chunk * kChunk;
   const Request q = request_of(L, r);
-  const int a = q.a, j0 = (int)((int64_t)q.n * part / parts);
-  const int j1 = (int)((int64_t)q.n * (part + 1) / parts);
+  // every part counts the history anew, so a part has a row for so many of its tokens
+  const int least = q.len / kTokensARow + 1, shared = min((int)parts, max(q.n / least, 1));
+  const int a = q.a, j0 = part < shared ? (int)((int64_t)q.n * part / shared) : q.n;
+  const int j1 = part < shared ? (int)((int64_t)q.n * (part + 1) / shared) : q.n;
   int bits = q.bits;
   if (j0 == j1) {
     if (bits && chunk == 0) flag_error(L.err, bits);
@@ -221,7 +228,20 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
   const int32_t *drafts = kCounts && L.drafts != nullptr ? L.drafts + (int64_t)r * L.gamma : nullptr;
   uint32_t has = 0;  // which of the thread's tokens have a word
   // vector u of the thread begins at token e(u); its bits are u * kPer on
-  auto e = [&](int u) { return base + (u * kThreads + tid) * kPer; };
+  auto e = [&](int u) {
+    return (int)(((u * (kThreads / kWave) + tid / kWave) * chunks + chunk) * kSpan) + lane * kPer;
+  };
+  // The word of token v, -1 where another chunk has it.  There are at most 1024 spans and
+  // 64 chunks, so the product is off by less than 1024 / 65536 <= 1 / chunks: the quotient is right.
+  const unsigned inverse = (65535 + chunks) / chunks;
+  // change(word) where the token is this chunk's.
+  auto with_word = [&](int v, auto change) __attribute__((always_inline)) {
+    const unsigned span = (unsigned)v / kSpan, mine = __umul24(span, inverse) >> 16;
+    if (__umul24(mine, chunks) + chunk == span && (unsigned)v < (unsigned)L.V)
+      change(&word[mine * kSpan + (unsigned)v % kSpan]);
+    // a token that is wrong is seen by every chunk and part; the first chunk reports it
+    if (chunk == 0 && (unsigned)(v + 1) > (unsigned)L.V) bits |= kErrToken;
+  };
   // mask and draft of 64 rows, a row a lane (out of range: as they are found)
   int mask_of, draft_of;
   auto look_ahead = [&](int j) {
@@ -253,8 +273,11 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
   // the thread's bit of row k's draft, 0 where another thread has it
   auto draft_bit = [&](int k) -> uint32_t {
     if (!kCounts || drafts == nullptr) return 0;
-    const int at = __builtin_amdgcn_readlane(draft_of, k) - base;  // of no draft negative
-    if ((unsigned)at >= (unsigned)kChunk || at / kPer % kThreads != tid) return 0;
+    const int v = __builtin_amdgcn_readlane(draft_of, k);  // in the vocabulary, or -1
+    const unsigned span = (unsigned)v / kSpan, mine = __umul24(span, inverse) >> 16;
+    if (v < 0 || mine * chunks + chunk != span) return 0;
+    const unsigned at = mine * kSpan + (unsigned)v % kSpan;
+    if (at / kPer % kThreads != (unsigned)tid) return 0;
     return 1u << (at / kPer / kThreads * kPer + at % kPer);
   };
   auto count = [&](uint32_t bit) {  // one of the thread's tokens is a draft before this row
@@ -338,21 +361,19 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
     for (int i = 0; i < kOwn / 4; ++i)
       reinterpret_cast<uint4 *>(word)[i * kThreads + tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    auto here = [&](int v) { return (unsigned)(v - base) < (unsigned)kChunk; };
     if (L.n_bias > 0) {
-      ids.each(L.V, &bits, [&](int v, int i) {
-        if (here(v)) atomicMax(&word[v - base], (uint32_t)(L.n_bias - i) << kBiasShift);
+      ids.each(0, [&](int v, int i, auto) {
+        with_word(v, [&](uint32_t *w) { atomicMax(w, (uint32_t)(L.n_bias - i) << kBiasShift); });
       });
       __syncthreads();
     }
-    past.each(L.V, &bits, [&](int v, int i) {
-      if (!here(v)) return;
-      if (i < q.prompt) atomicOr(&word[v - base], kPromptBit);
-      else atomicAdd(&word[v - base], 1u);
+    past.each(q.prompt, [&](int v, int i, auto mode) {
+      with_word(v, [&](uint32_t *w) {
+        if (mode == kBelow || (mode == kMixed && i < q.prompt)) atomicOr(w, kPromptBit);
+        else atomicAdd(w, 1u);
+      });
     });
-    before.each(L.V, &bits, [&](int v, int) {
-      if (here(v)) atomicAdd(&word[v - base], 1u);
-    });
+    before.each(0, [&](int v, int, auto) { with_word(v, [&](uint32_t *w) { atomicAdd(w, 1u); }); });
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
@@ -443,11 +464,17 @@ hipError_t launch_edit(const EditLaunch &L, hipStream_t stream) {
     using T = decltype(type);
     constexpr bool kGrad = decltype(grad)::value, kCounts = decltype(has_counts)::value;
     constexpr bool kMask = decltype(has_mask)::value, kInPlace = decltype(in_place)::value;
-    constexpr int kThreads = kBlock;
+    // 256 threads count a history twice as often: 149 us for 152 (1152 rows of 151936,
+    // histories of up to 6000), but 66 for 47 (histories of up to 120000); 1024: 170 and 54
+    constexpr int kThreads = 512;
     const unsigned chunks = (L.V + kThreads * kOwn - 1) / (kThreads * kOwn);
     const unsigned base = L.R * chunks;  // R <= 2^22, chunks <= 64
     const unsigned most = (L.n_rows + L.R - 1) / L.R;
-    unsigned parts = (8 * kComputeUnits + base - 1) / base;
+    // About 4 rows a part, 2 where there is nothing to count: requests have 1 to 17 rows,
+    // and the last workgroups end together.  1152 rows: 9 a part 166 us, 4 152, 3 159, 2 175;
+    // with nothing to count 147, 137, 131, 125.  Then enough to fill the chip.
+    unsigned parts = (most + 1) / (kCounts || kInPlace ? 4 : 2);
+    if (parts * base < 4 * kComputeUnits) parts = (4 * kComputeUnits + base - 1) / base;
     if (parts > most) parts = most;
     const dim3 grid((L.R < kRequestsX ? L.R : kRequestsX) * chunks * parts,
                     (L.R + kRequestsX - 1) / kRequestsX);
