@@ -803,6 +803,7 @@ dspark_status dspark_edit_logits(int n_rows, int V, int64_t row_stride, dspark_d
   L.err = (int32_t *)ws;
   dspark_status s = check_edit(L, dt, ws, ws_bytes);
   if (s != DSPARK_OK) return s;
+  if (history == nullptr) L.hist_len = nullptr, L.hist_stride = 0;
   if (out == X && out_stride != row_stride) return DSPARK_ERR_VALUE;
   return from_hip(launch_edit(L, stream));
 }
@@ -826,6 +827,7 @@ dspark_status dspark_edit_logits_backward(int n_rows, int V, int64_t row_stride,
   L.out = dX; L.err = (int32_t *)ws;
   dspark_status s = check_edit(L, dt, ws, ws_bytes);
   if (s != DSPARK_OK) return s;
+  if (history == nullptr) L.hist_len = nullptr, L.hist_stride = 0;
   if ((dX == G && dx_stride != g_stride) || dX == X) return DSPARK_ERR_VALUE;
   return from_hip(launch_edit(L, stream));
 }

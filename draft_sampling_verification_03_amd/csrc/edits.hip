@@ -116,7 +116,8 @@ struct Rules {  // of one request
   const float *bias_end;  // entry n_bias of its biases
 };
 
-// x / r, rounded once: the product with 1 / r and what it is off by, divided again.
+// x / r to within a little over half a step: the product with 1 / r, and what that is off
+// by divided again.
 __device__ __forceinline__ float divide(float x, const Rules &k) {
   const float q = x * k.inverse;
   const float better = __builtin_fmaf(__builtin_fmaf(-q, k.repetition, x), k.inverse, q);
@@ -231,8 +232,8 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
   auto e = [&](int u) {
     return (int)(((u * (kThreads / kWave) + tid / kWave) * chunks + chunk) * kSpan) + lane * kPer;
   };
-  // The word of token v, -1 where another chunk has it.  There are at most 1024 spans and
-  // 64 chunks, so the product is off by less than 1024 / 65536 <= 1 / chunks: the quotient is right.
+  // The chunk and word of a token: there are at most 1024 spans and 32 chunks, so span *
+  // inverse / 65536 is off by less than 1024 / 65536 < 1 / chunks, and the quotient is right.
   const unsigned inverse = (65535 + chunks) / chunks;
   // change(word) where the token is this chunk's.
   auto with_word = [&](int v, auto change) __attribute__((always_inline)) {
@@ -468,16 +469,18 @@ hipError_t launch_edit(const EditLaunch &L, hipStream_t stream) {
     // histories of up to 6000), but 66 for 47 (histories of up to 120000); 1024: 170 and 54
     constexpr int kThreads = 512;
     const unsigned chunks = (L.V + kThreads * kOwn - 1) / (kThreads * kOwn);
-    const unsigned base = L.R * chunks;  // R <= 2^22, chunks <= 64
+    const unsigned along = L.R < kRequestsX ? L.R : kRequestsX, base = along * chunks;  // <= 2^21
     const unsigned most = (L.n_rows + L.R - 1) / L.R;
     // About 4 rows a part, 2 where there is nothing to count: requests have 1 to 17 rows,
     // and the last workgroups end together.  1152 rows: 9 a part 166 us, 4 152, 3 159, 2 175;
-    // with nothing to count 147, 137, 131, 125.  Then enough to fill the chip.
+    // with nothing to count 147, 137, 131, 125.  Then enough to fill the chip, and no
+    // more workgroups than a launch can have (2^32 threads).
     unsigned parts = (most + 1) / (kCounts || kInPlace ? 4 : 2);
     if (parts * base < 4 * kComputeUnits) parts = (4 * kComputeUnits + base - 1) / base;
+    if (parts > (1u << 22) / base) parts = (1u << 22) / base;
     if (parts > most) parts = most;
-    const dim3 grid((L.R < kRequestsX ? L.R : kRequestsX) * chunks * parts,
-                    (L.R + kRequestsX - 1) / kRequestsX);
+    if (parts < 1) parts = 1;
+    const dim3 grid(base * parts, (L.R + kRequestsX - 1) / kRequestsX);
     DSPARK_LAUNCH(kGrad ? "edit_logits_backward" : "edit_logits", stream,
                   (edit_kernel<T, kGrad, kCounts, kMask, kInPlace, kThreads>), grid, kThreads, L, chunks,
                   parts);

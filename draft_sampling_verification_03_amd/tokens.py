@@ -80,17 +80,20 @@ def _rotate(where, q, k, plan, positions, row_offset, kv_len, ws, stream, out):
     if row_offset is not None:
         R = _width(a, row_offset, "row_offset") - 1
         a.req(row_offset, "row_offset", I32, (R + 1,))
-    a.req(positions, "positions", I32, (n,), optional=True)
-    a.req(kv_len, "kv_len", I32, (R,), optional=True)
+    if positions is not None:
+        a.req(positions, "positions", I32, (n,))
+    if kv_len is not None:
+        a.req(kv_len, "kv_len", I32, (R,))
     index, dev = a.gpu(), q.device
     with _on_stream(stream):
         if out is None:
-            out = {"q": _empty((n, Hq, D), q.dtype, dev),
-                   "k": None if k is None else _empty((n, Hkv, D), q.dtype, dev)}
-        qo = a.rows(out.get("q"), "out['q']", q.dtype, (n, Hq, D))
-        ko = 0 if k is None else a.rows(out.get("k"), "out['k']", q.dtype, (n, Hkv, D))
+            out = {"q": q.new_empty((n, Hq, D)), "k": None if k is None else q.new_empty((n, Hkv, D))}
+            qo, ko = Hq * D, Hkv * D
+        else:
+            qo = a.rows(out.get("q"), "out['q']", q.dtype, (n, Hq, D))
+            ko = 0 if k is None else a.rows(out.get("k"), "out['k']", q.dtype, (n, Hkv, D))
+            a.gpu()
         buf = _workspace(ws, 256, dev, index, stream)
-    a.gpu()
     _launch("dspark_rotary_backward" if where == "rotary_backward" else "dspark_rotary", index, stream,
             n, Hq, Hkv, D, plan.rot, plan.layout, dt, plan.magnitude, turns, _ptr(positions), R,
             _ptr(row_offset), _ptr(kv_len), q.data_ptr(), q_stride, _ptr(k), k_stride,
@@ -145,7 +148,8 @@ def cache_append(q, k_new, v_new, k_pages, v_pages, table, kv_len, *, plan=None,
     if plan is not None:
         turns = _plan(a, plan)
         rot, layout, magnitude = plan.rot, plan.layout, plan.magnitude
-    a.req(positions, "positions", I32, (n,), optional=True)
+    if positions is not None:
+        a.req(positions, "positions", I32, (n,))
     Hq, q_stride, qo = 0, 0, 0
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
@@ -156,12 +160,12 @@ def cache_append(q, k_new, v_new, k_pages, v_pages, table, kv_len, *, plan=None,
         raise ValueError("cache_append: out is for the queries, and there are none")
     index, dev = a.gpu(), k_new.device
     with _on_stream(stream):
-        if q is not None:
-            if out is None:
-                out = _empty((n, Hq, D), dtype, dev)
+        if q is not None and out is None:
+            out, qo = q.new_empty((n, Hq, D)), Hq * D
+        elif q is not None:
             qo = a.rows(out, "out", dtype, (n, Hq, D))
+            a.gpu()
         buf = _workspace(ws, 256, dev, index, stream)
-    a.gpu()
     _launch("dspark_cache_append", index, stream, R, n, Hq, Hkv, D, page, width, n_pages, dt, rot,
             layout, magnitude, turns, _ptr(positions), _ptr(q), q_stride, _ptr(out), qo,
             k_new.data_ptr(), v_new.data_ptr(), kn, k_pages.data_ptr(), v_pages.data_ptr(), k_stride,
@@ -199,7 +203,8 @@ class _Edits:
         if drafts is not None:
             self.gamma = _width(a, drafts, "drafts")
             a.req(drafts, "drafts", I32, (R, self.gamma))
-        a.req(repetition, "repetition", F32, (R,), optional=True)
+        if repetition is not None:
+            a.req(repetition, "repetition", F32, (R,))
         if mask is not None:
             self.words = _width(a, mask, "mask")
             if mask.dim() != 2 or self.words < (V + 31) // 32:
@@ -238,8 +243,10 @@ def edit_logits(X, *, row_offset=None, history=None, hist_len=None, prompt_len=N
     e = _Edits("edit_logits", X, row_offset, history, hist_len, prompt_len, drafts, repetition, mask,
                mask_index)
     a, R = e.a, e.R
-    a.req(frequency, "frequency", F32, (R,), optional=True)
-    a.req(presence, "presence", F32, (R,), optional=True)
+    if frequency is not None:
+        a.req(frequency, "frequency", F32, (R,))
+    if presence is not None:
+        a.req(presence, "presence", F32, (R,))
     n_bias = 0
     if bias_ids is not None or bias is not None:
         n_bias = _width(a, bias_ids, "bias_ids")
@@ -325,7 +332,8 @@ class TokenHistory:
     def __init__(self, R, capacity, device="cuda"):
         from .api import Workspace
         # a multiple of four tokens: every row is read in whole 16-byte pieces
-        self.tokens = torch.full((R, -(-capacity // 4) * 4), -1, dtype=I32, device=device)
+        width = -(-capacity // 4) * 4
+        self.tokens = torch.full((R, width if width < 1 << 20 else capacity), -1, dtype=I32, device=device)
         self.lens = torch.zeros(R, dtype=I32, device=device)
         self.prompt_lens = torch.zeros(R, dtype=I32, device=device)
         self.ws = Workspace(device)

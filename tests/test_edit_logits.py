@@ -372,6 +372,39 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(X[n - 3:], want) and not X[: n - 3].any()
 
 
+@pytest.mark.parametrize("one_each", [True, False])
+def test_most_rows(one_each):
+    """The largest number of rows, one request each or all of one request."""
+    n = 1 << 22
+    X = torch.randn((n, 8), device="cuda").to(BF)
+    mask = i32([[0b10110101]])
+    allowed = torch.tensor([(0b10110101 >> v) & 1 for v in range(8)], device="cuda") != 0
+    index = torch.zeros(n, dtype=I32, device="cuda")
+    kw, ws = dict(mask=mask, mask_index=index), ds.Workspace()
+    rep = f32([2.0] * (n if one_each else 1))
+    if one_each:
+        kw.update(history=torch.full((n, 1), 4, dtype=I32, device="cuda"), hist_len=index + 1, repetition=rep)
+    else:
+        kw.update(row_offset=i32([0, n]), history=i32([[4]]), hist_len=i32([1]), repetition=rep)
+    want = X.masked_fill(~allowed, -INF)
+    x = X[:, 4].float()
+    want[:, 4] = torch.where(x > 0, x / 2, x * 2).to(BF)
+    assert torch.equal(ds.edit_logits(X, ws=ws, **kw), want) and ws.error_code() == 0
+
+
+def test_lengths_without_a_history_are_not_read():
+    """The C call with hist_len and no history."""
+    X = torch.randn((2, 64), device="cuda")
+    out, ws = torch.empty_like(X), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    drafts = i32([[3, 5], [7, 9]])
+    fre = f32([1.0, 2.0])
+    st = ds.dspark_edit_logits(2, 64, 64, 0, X, 2, None, None, -7, i32([40, 50]), None, drafts, 2, None, fre,
+                               None, 0, None, None, 0, None, 0, None, out, 64, ws, 256,
+                               torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert st == 0 and torch.equal(out, X) and not ws.any()  # row 0 stands behind no draft
+
+
 def test_streams_and_two_graphs_over_one_workspace():
     e = Edits([3, 1, 6], 5003, BF, seed=15, longest=400, n_bias=5, masks=3)
     kw, ws, side = e.args(), ds.Workspace(), torch.cuda.Stream()
