@@ -11,6 +11,14 @@
 // have a word at all, and it alone changes their words as the drafts before each row come
 // to count: the rows need no barrier.  Nearly all of a row has no word and no mask, and
 // passes through as it is; in place it is not even read.
+//
+// Bound: the rows in and out.  1152 rows of 151936 bf16, histories of up to 6000, a quarter
+// masked (702 MB; counters: 380 MB fetched, 350 written): 151 us, 4.6 TB/s, of which 10 go
+// to the counting and 10 to words, biases and drafts; the gradient of 544 rows of 129280
+// (282 MB) 69 us; fp32 rows with histories of up to 120000 46 us, two thirds of them the
+// counting (one LDS operation for 64 tokens, in each of the 16 chunks).  Masks in place, half
+// of them dense, half sparse: 169 MB fetched and 136 written, for nearly every 128 bytes
+// hold both kinds: 60 to 84 us.  One row: 8 us of latency.
 #include <float.h>
 
 #include "common.h"

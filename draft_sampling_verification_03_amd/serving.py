@@ -397,8 +397,9 @@ class PagedCache:
     n_pages pages that the requests share out among themselves:
     k [n_pages][layers][Hkv][page][D], v [n_pages][layers][Hkv][D][page].
 
-    A round: reserve(row_offset), attend(layer, ...) for every layer, and after
-    the verification commit(n_acc).  All state lives on the device and changes
+    A round: reserve(row_offset), attend(layer, ...) for every layer (with rotary=, a
+    tokens.RotaryPlan, where positions are rotated in), and after the verification
+    commit(n_acc).  All state lives on the device and changes
     in place; nothing waits for the host, and a captured round may be replayed.
     A round that finds no room (see reserve()) changes nothing in any of the three.
     error_code() reads what the device found wrong so far."""
