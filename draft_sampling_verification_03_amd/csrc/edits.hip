@@ -10,15 +10,15 @@
 // A thread owns the same 16 tokens of every row, so it keeps in a register which of them
 // have a word at all, and it alone changes their words as the drafts before each row come
 // to count: the rows need no barrier.  Nearly all of a row has no word and no mask, and
-// passes through as it is; in place it is not even read.
+// passes through as it is; in place a line of it with neither is not even read.
 //
 // Bound: the rows in and out.  1152 rows of 151936 bf16, histories of up to 6000, a quarter
 // masked (702 MB; counters: 380 MB fetched, 350 written): 151 us, 4.6 TB/s, of which 10 go
 // to the counting and 10 to words, biases and drafts; the gradient of 544 rows of 129280
 // (282 MB) 69 us; fp32 rows with histories of up to 120000 46 us, two thirds of them the
 // counting (one LDS operation for 64 tokens, in each of the 16 chunks).  Masks in place, half
-// of them dense, half sparse: 169 MB fetched and 136 written, for nearly every 128 bytes
-// hold both kinds: 60 to 84 us.  One row: 8 us of latency.
+// of them dense, half sparse: 169 MB fetched and 172 written, for nearly every 128 bytes
+// hold both kinds: 68 to 73 us.  One row: 8 us of latency.
 #include <float.h>
 
 #include "common.h"
@@ -307,11 +307,18 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
   auto load_piece = [&](const T *from, int u, bool wanted) {
     return *reinterpret_cast<const u32x4 *>(from + (wanted && e(u) < L.V ? e(u) : 0));
   };
+  // In place the 128 bytes of eight lanes are written whole or not at all: in part they cost
+  // more than the bytes they save (masks in place: 136 MB written in 84 us, 172 in 73).
+  auto line_changes = [&](int u, uint32_t al, uint32_t mk) {
+    constexpr int kLine = 8;
+    const uint64_t change = __ballot(e(u) < L.V && (al != kAll || mk != 0));
+    return (change >> (lane & (kWave - kLine)) & ((1u << kLine) - 1)) != 0;
+  };
   auto load_row = [&](Row &o, int j, uint32_t allowed, uint32_t marked) {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
-      o.v[u] = load_piece(source + (a + j) * stride, u, !kInPlace || (al != 0 && (al != kAll || mk != 0)));
+      o.v[u] = load_piece(source + (a + j) * stride, u, !kInPlace || (al != 0 && line_changes(u, al, mk)));
     }
   };
   auto load_raw = [&](Row &o, int j, uint32_t marked) {
@@ -344,7 +351,8 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
       }
       if (kMask && al != kAll)
         out = masked<T>(out, al, kGrad ? 0 : sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u);
-      if (e(u) >= L.V || (kInPlace && al == kAll && mk == 0)) continue;
+      const bool changes = !kInPlace || line_changes(u, al, mk);
+      if (e(u) >= L.V || !changes) continue;
       if (e(u) + kPer <= L.V) {
         *reinterpret_cast<u32x4 *>(to + e(u)) = out;
       } else {

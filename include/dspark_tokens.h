@@ -162,7 +162,8 @@ dspark_status dspark_cache_append(int R, int rows_capacity, int Hq, int Hkv, int
  *     v / 32 is 1 where v is allowed; mask_index [n_rows] int32, the row's mask or -1 for
  *     none (NULL: row i has mask i, n_masks >= n_rows).  mask NULL: none.
  * Output: out [n_rows][out_stride] (dt); it may be X itself (out_stride = row_stride: then
- *   only what changes is read or written).  Columns from V on and rows that no request
+ *   only the lines of a row, 128 bytes from its start on, in which something changes are
+ *   read and written).  Columns from V on and rows that no request
  *   has stay as they were.
  * A token or bias id outside [0, V) and not -1 sets DSPARK_DEVERR_TOKEN and is skipped; a
  * slice of row_offset that decreases or passes n_rows, a hist_len outside
