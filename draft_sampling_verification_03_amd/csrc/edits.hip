@@ -249,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
     if (__umul24(mine, chunks) + chunk == span && (unsigned)v < (unsigned)L.V)
       change(&word[mine * kSpan + (unsigned)v % kSpan]);
     // a token that is wrong is seen by every chunk and part; the first chunk reports it
-    if (chunk == 0 && (unsigned)(v + 1) > (unsigned)L.V) bits |= kErrToken;
+    if (chunk == 0 && (unsigned)v + 1u > (unsigned)L.V) bits |= kErrToken;
   };
   // mask and draft of 64 rows, a row a lane (out of range: as they are found)
   int mask_of, draft_of;
