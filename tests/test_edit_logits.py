@@ -148,7 +148,8 @@ class Edits:
         for r, j, row in self.each():
             rep = float(self.repetition[r])
             again = self.seen(r, j)
-            want = torch.where(again, G[row].double() * torch.where(raw[row] > 0, 1 / rep, rep), G[row].double())
+            slope = torch.where(again, torch.where(raw[row] > 0, 1 / rep, rep), 1.0)
+            want = G[row].double() * slope
             tol = torch.where(again, 2 * U * want.abs() + (2.0 ** -8 * want.abs() if self.dt == BF else 0), 0.0)
             no = self.forbidden(row)
             if no is not None:
