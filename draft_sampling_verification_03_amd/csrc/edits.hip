@@ -301,6 +301,7 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
   struct Row {
     u32x4 v[kVecs], raw[kRaw ? kVecs : 1];
     Allowed mask;
+    uint32_t lines;  // in place, bit u: the line of vector u is written
   };
   // A piece that ends behind the row's last token is read whole: it is aligned, and so
   // within the page of memory that holds the token.
@@ -308,7 +309,9 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
     return *reinterpret_cast<const u32x4 *>(from + (wanted && e(u) < L.V ? e(u) : 0));
   };
   // In place the 128 bytes of eight lanes are written whole or not at all: in part they cost
-  // more than the bytes they save (masks in place: 136 MB written in 84 us, 172 in 73).
+  // more than the bytes they save (masks in place: 136 MB written in 84 us, 172 in 73).  A
+  // vote of the whole wave, so never behind a condition of a lane; made once for a row, as
+  // it is loaded, and kept until it is stored: what is stored is what was loaded.
   auto line_changes = [&](int u, uint32_t al, uint32_t mk) {
     constexpr int kLine = 8;
     const uint64_t change = __ballot(e(u) < L.V && (al != kAll || mk != 0));
@@ -318,7 +321,9 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const uint32_t al = allowed >> (u * kPer) & kAll, mk = marked >> (u * kPer) & kAll;
-      o.v[u] = load_piece(source + (a + j) * stride, u, !kInPlace || (al != 0 && line_changes(u, al, mk)));
+      const bool line = !kInPlace || line_changes(u, al, mk);
+      if constexpr (kInPlace) o.lines = (u == 0 ? 0 : o.lines) | (line ? 1u << u : 0);
+      o.v[u] = load_piece(source + (a + j) * stride, u, line && (!kInPlace || al != 0));
     }
   };
   auto load_raw = [&](Row &o, int j, uint32_t marked) {
@@ -351,8 +356,8 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
       }
       if (kMask && al != kAll)
         out = masked<T>(out, al, kGrad ? 0 : sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u);
-      const bool changes = !kInPlace || line_changes(u, al, mk);
-      if (e(u) >= L.V || !changes) continue;
+      const bool stored = !kInPlace || (in.lines >> u & 1);
+      if (e(u) >= L.V || !stored) continue;
       if (e(u) + kPer <= L.V) {
         *reinterpret_cast<u32x4 *>(to + e(u)) = out;
       } else {

@@ -195,6 +195,72 @@ def test_values_in_place_and_gradient(case, dt):
     assert torch.equal(G[:e.n], dX[:e.n]) and ws.error_code() == 0
 
 
+def whole_pieces(V, per):
+    """Masks [14][V] of whole 16-byte pieces (`per` tokens), lines of eight of them and
+    words, of stretches with even and odd ends, and of the row's last piece."""
+    v = np.arange(V)
+    line, last = 8 * per, v >= V - 1 - (V - 1) % per
+    return np.array([(v >= 16) & (v < 24), v < 1000, (v >= 1000) & (v < 2000), v // per % 2 == 0, v // per % 2 == 1,
+                     v // line % 2 == 0, v // 32 % 2 == 1, v // per % 8 == 5, v // per % 8 != 2,
+                     (v >= 7) & (v < 331), v % 1000 < 500, v != V - 1, ~last, last])
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("V", [1001, 4096, 9000, 151936])
+@pytest.mark.parametrize("history", [False, True])
+def test_masks_of_whole_pieces_in_place(V, dt, history):
+    """In place, where lines of 128 bytes hold pieces wholly forbidden and pieces wholly
+    allowed: the values and gradients of another output, bit for bit."""
+    e = Edits([14, 1, 70], V, dt, seed=V, longest=6, n_bias=3, masks=14)
+    e.allowed = whole_pieces(V, 8 if dt == BF else 4)
+    e.mask_index = np.concatenate((np.arange(14), [3], np.random.default_rng(1).integers(-1, 14, 70)))
+    kw, grad = e.args(), e.args(grad=True)
+    if not history:
+        for name in ("history", "hist_len", "prompt_len", "drafts", "repetition", "frequency", "presence",
+                     "bias_ids", "bias"):
+            kw[name] = None
+            if name in grad:
+                grad[name] = None
+    raw = e.X.clone()
+    got = ds.edit_logits(e.X, **kw)
+    if history:
+        e.check(got, raw)
+    else:
+        for row, m in enumerate(e.mask_index):
+            want = raw[row] if m < 0 else raw[row].masked_fill(torch.from_numpy(~e.allowed[m]).cuda(), -INF)
+            assert torch.equal(got[row], want), (row, m)
+    X = raw_rows(raw)
+    assert torch.equal(ds.edit_logits(X, out=X, **kw), got)
+    G = raw_rows(torch.randn(raw.shape, device="cuda").to(dt))
+    X = raw_rows(raw)
+    dX = ds.edit_logits_backward(G, X, **grad)
+    if history:
+        e.check_gradient(dX, G, raw)
+        # the gradient without penalties has words and no slopes
+        H = G.clone()
+        want = ds.edit_logits_backward(raw_rows(H), **dict(grad, repetition=None))
+        H = raw_rows(H)
+        assert torch.equal(ds.edit_logits_backward(H, out=H, **dict(grad, repetition=None)), want)
+    ds.edit_logits_backward(G, X, out=G, **grad)
+    assert torch.equal(G, dX)
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("share", [0.85, 0.95])
+def test_random_masks_in_place(share, dt):
+    """Nearly all tokens allowed: some lines hold one piece that is wholly forbidden."""
+    V = 151936
+    g = torch.Generator(device="cuda").manual_seed(5)
+    allowed = torch.rand((64, V), generator=g, device="cuda") < share
+    X = torch.randn((64, V), generator=g, device="cuda").to(dt)
+    want = X.masked_fill(~allowed, -INF)
+    G = torch.randn((64, V), generator=g, device="cuda").to(dt)
+    mask = pack(allowed.cpu().numpy())
+    assert torch.equal(ds.edit_logits(X, mask=mask, out=X), want)
+    want = G.masked_fill(~allowed, 0)
+    assert torch.equal(ds.edit_logits_backward(G, mask=mask, out=G), want)
+
+
 def raw_rows(x):
     """x in rows of whole 16-byte pieces."""
     return torch.nn.functional.pad(x, (0, -x.shape[1] % 8))[:, :x.shape[1]]
