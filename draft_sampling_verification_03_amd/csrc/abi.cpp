@@ -22,7 +22,7 @@ static __device__ __align__(256) unsigned char scratch[DSPARK_NOALLOC_SCRATCH_BY
 
 namespace {
 
-constexpr long double kTwoPi = 6.283185307179586476925286766559L;
+constexpr double kTwoPi = 6.283185307179586476925;
 constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
 void *g_scratch_ptr[kMaxDevices];  // device address of `scratch`, per device (nullptr: not yet)
@@ -610,7 +610,7 @@ dspark_status dspark_rotary_frequencies(int rot, double base, dspark_rotary_scal
     double f = pow(base, -2.0 * i / rot);
     if (scaling == DSPARK_ROTARY_LINEAR) f /= factor;
     if (scaling == DSPARK_ROTARY_BY_TURNS) {
-      const double w = (context * f / (double)kTwoPi - slow) / (fast - slow);
+      const double w = (context * f / kTwoPi - slow) / (fast - slow);
       const double keep = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
       f *= keep + (1.0 - keep) / factor;
     }
@@ -625,11 +625,17 @@ dspark_status dspark_rotary_turns(int n, const double *freqs, uint64_t *turns) {
   for (int i = 0; i < n; ++i)
     if (!(fabs(freqs[i]) < 1048576.0)) return DSPARK_ERR_VALUE;
   for (int i = 0; i < n; ++i) {
-    // in 64 bits of fraction, so that the last bit counts below 2^-32 turns at any position;
-    // the part of a turn within [-1/2, 1/2], in units of 2^-64 (2^63 is the angle of -2^63)
-    const long double t = freqs[i] / kTwoPi;
-    const long double part = nearbyintl((t - nearbyintl(t)) * 18446744073709551616.0L);
-    turns[i] = part >= 9223372036854775808.0L ? (uint64_t)1 << 63 : (uint64_t)(int64_t)part;
+    // |f| = m 2^-down, m a whole number below 2^53 and down >= 33, times 1 / (2 pi) =
+    // (hi 2^64 + lo) 2^-128 in whole numbers, and rounded once to units of 2^-64: 2^64 |f| / (2 pi) =
+    // m (hi + lo 2^-64) 2^-down.  Whole turns leave at the top.
+    constexpr unsigned __int128 hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;
+    int e;
+    const double fraction = frexp(fabs(freqs[i]), &e);
+    const uint64_t m = (uint64_t)ldexp(fraction, 53);
+    const int down = 53 - e;
+    unsigned __int128 units = m * hi + (m * lo >> 64);  // below 2^116
+    units = down < 118 ? (units + ((unsigned __int128)1 << (down - 1))) >> down : 0;
+    turns[i] = freqs[i] < 0.0 ? 0 - (uint64_t)units : (uint64_t)units;
   }
   return DSPARK_OK;
 }

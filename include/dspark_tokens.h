@@ -61,9 +61,10 @@ dspark_status dspark_rotary_frequencies(int rot, double base, dspark_rotary_scal
                                         double factor, double context, double slow, double fast,
                                         double *freqs);
 /* The form in which the kernels take frequencies: turns a token, f / (2 pi), as
- * 64-bit fractions of one turn, so that position * turns is the angle without its
- * whole turns, exactly, however far the position.  Host memory; 1 <= n <= 128;
- * finite frequencies of any sign below 2^20 in magnitude. */
+ * 64-bit fractions of one turn, rounded once.  position * turns then drops the whole
+ * turns exactly, and the angle is off by 2^-65 turns for each token of the position: less
+ * than 2^-33 turns however far the position.  Host memory; 1 <= n <= 128; finite
+ * frequencies of any sign below 2^20 in magnitude. */
 dspark_status dspark_rotary_turns(int n, const double *freqs, uint64_t *turns);
 
 /* Positions of the rows, any int32 (negative ones turn back):

@@ -95,6 +95,22 @@ def test_turns():
     assert A.dspark_rotary_turns(1, one.ctypes.data, None) == NULL
 
 
+def test_turns_are_rounded_once_at_any_frequency():
+    """Over all accepted frequencies the turns are the nearest multiple of 2^-64 (1 / (2 pi)
+    to 128 bits adds less than 2^-40 of it), so position * turns is off by less than
+    2^-33 turns at any 32-bit position."""
+    rng = np.random.default_rng(0)
+    f = np.concatenate([np.ldexp(rng.uniform(1, 2, 120), rng.integers(-140, 20, 120)) * rng.choice([-1, 1], 120),
+                        [np.nextafter(2.0 ** 20, 0), -np.nextafter(2.0 ** 20, 0), 1e6, 1.0, 2.0 ** -33,
+                         5e-324, -5e-324, 2.2e-308]])
+    t = np.zeros(len(f), np.uint64)
+    assert A.dspark_rotary_turns(len(f), f.ctypes.data, t.ctypes.data) == OK
+    for x, got in zip(f, t):
+        off = (int(got) - Fraction(float(x)) / TWO_PI * 2 ** 64) % 2 ** 64
+        off = min(off, 2 ** 64 - off)
+        assert off <= Fraction(1, 2) + Fraction(1, 2 ** 40), (x, got, float(off))
+
+
 def test_plan():
     plan = ds.RotaryPlan(64, base=500000.0, scaling="by_turns", factor=8.0, context=8192.0,
                          magnitude=1.25, layout="interleaved", device="cpu")
