@@ -640,6 +640,8 @@ dspark_status dspark_rotary_turns(int n, const double *freqs, uint64_t *turns) {
   return DSPARK_OK;
 }
 
+static bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
 static bool bad_layout(dspark_rotary_layout layout) {
   return layout != DSPARK_ROTARY_HALF && layout != DSPARK_ROTARY_INTERLEAVED;
 }
@@ -670,7 +672,7 @@ static dspark_status rotary(bool back, int n_rows, int Hq, int Hkv, int D, int r
   if ((q == q_out && q_stride != q_out_stride) || (Hkv > 0 && k == k_out && k_stride != k_out_stride))
     return DSPARK_ERR_VALUE;
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) || !aligned16(ws) ||
-      ((uintptr_t)turns & 7u) != 0)
+      ((uintptr_t)turns & 7u) != 0 || !aligned4(positions) || !aligned4(row_offset) || !aligned4(kv_len))
     return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
   RotaryLaunch L{};
@@ -738,7 +740,8 @@ dspark_status dspark_cache_append(int R, int rows_capacity, int Hq, int Hkv, int
     return DSPARK_ERR_SHAPE;
   if (q != nullptr && q == q_out && q_stride != q_out_stride) return DSPARK_ERR_VALUE;
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k_new) || !aligned16(v_new) ||
-      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(ws) || ((uintptr_t)turns & 7u) != 0)
+      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(ws) || ((uintptr_t)turns & 7u) != 0 ||
+      !aligned4(positions) || !aligned4(table) || !aligned4(row_offset) || !aligned4(kv_len))
     return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
   AppendLaunch L{};
@@ -778,7 +781,6 @@ static dspark_status check_edit(const EditLaunch &L, dspark_dtype dt, const void
       (L.mask_index != nullptr && !L.mask))
     return DSPARK_ERR_NULL;
   if (!aligned16(L.X) || !aligned16(L.G) || !aligned16(L.out) || !aligned16(ws)) return DSPARK_ERR_ALIGN;
-  auto aligned4 = [](const void *p) { return ((uintptr_t)p & 3u) == 0; };
   if (!aligned4(L.row_offset) || !aligned4(L.history) || !aligned4(L.hist_len) ||
       !aligned4(L.prompt_len) || !aligned4(L.drafts) || !aligned4(L.bias_ids) || !aligned4(L.bias) ||
       !aligned4(L.mask) || !aligned4(L.mask_index) || !aligned4(L.repetition) ||
@@ -848,7 +850,9 @@ dspark_status dspark_history_append(int R, int width, int n_tokens, const int32_
   const bool flat = row_offset != nullptr && n_acc == nullptr;
   if (flat ? n_tokens < 0 : width < 1 || width > kLongest) return DSPARK_ERR_SHAPE;
   if (!tokens || !history || !hist_len || !hist_len_out || !ws) return DSPARK_ERR_NULL;
-  if (!aligned16(ws)) return DSPARK_ERR_ALIGN;
+  if (!aligned16(ws) || !aligned4(tokens) || !aligned4(n_acc) || !aligned4(row_offset) ||
+      !aligned4(history) || !aligned4(hist_len) || !aligned4(hist_len_out) || !aligned4(prompt_len))
+    return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
   HistoryLaunch L{};
   L.R = R; L.width = width; L.n_tokens = n_tokens; L.hist_stride = hist_stride; L.tokens = tokens;

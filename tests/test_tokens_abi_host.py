@@ -330,3 +330,21 @@ def test_objects_on_the_host():
     h = ds.TokenHistory(3, 10, device="cpu")
     assert h.tokens.shape == (3, 12) and (h.tokens == -1).all() and h.lens.tolist() == [0, 0, 0]
     assert h.prompt_lens.tolist() == [0, 0, 0] and h.ws.buf.numel() >= 256
+
+
+# ------------------------------------------------- alignment of the int32 arrays
+@pytest.mark.parametrize("name", ["positions", "row_offset", "kv_len"])
+@pytest.mark.parametrize("f", [A.dspark_rotary, A.dspark_rotary_backward])
+def test_rotary_alignment(f, name):
+    assert f(*rotary(**{name: P + 2})) == ALIGN
+
+
+@pytest.mark.parametrize("name", ["positions", "table", "row_offset", "kv_len"])
+def test_append_alignment(name):
+    assert A.dspark_cache_append(**append(**{name: P + 1})) == ALIGN
+
+
+@pytest.mark.parametrize("name", ["tokens", "n_acc", "row_offset", "history", "hist_len", "hist_len_out",
+                                  "prompt_len"])
+def test_history_alignment(name):
+    assert A.dspark_history_append(**history(**{name: P + 2})) == ALIGN
