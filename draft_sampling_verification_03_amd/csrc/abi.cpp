@@ -85,7 +85,8 @@ const char *dspark_status_string(dspark_status s) {
     case DSPARK_ERR_NULL: return "a required pointer is NULL";
     case DSPARK_ERR_SHAPE: return "a size is outside the supported limits";
     case DSPARK_ERR_DTYPE: return "unknown element type";
-    case DSPARK_ERR_VALUE: return "invalid scalar argument (temperature must be finite and > 0)";
+    case DSPARK_ERR_VALUE: return "invalid scalar argument (temperature must be finite and > 0), or an output that overlaps an "
+                                  "input";
     case DSPARK_ERR_WORKSPACE: return "workspace smaller than the *_workspace() size";
     case DSPARK_ERR_SPS_TABLE: return "SPS table missing or shorter than R*(1+gamma)+1";
     case DSPARK_ERR_MODE: return "unknown scheduler mode or missing confidences";
@@ -642,6 +643,29 @@ dspark_status dspark_rotary_turns(int n, const double *freqs, uint64_t *turns) {
 
 static bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
+// Whether two arrays of n rows share a byte: rows of `wide` bytes, `stride` bytes apart.
+// Rows of one stride may stand side by side (slices of one buffer); of two different
+// strides none may begin within the other's stretch of memory.
+struct Rows {
+  const void *p;
+  __int128 stride, wide;
+  Rows(const void *at, int64_t stride_elems, int64_t wide_elems, int es)
+      : p(at), stride((__int128)stride_elems * es), wide((__int128)wide_elems * es) {}
+};
+static bool rows_meet(const Rows &a, const Rows &b, int64_t n) {
+  if (!a.p || !b.p) return false;
+  const __int128 d = (__int128)(uintptr_t)b.p - (__int128)(uintptr_t)a.p;  // from a to b
+  if (a.stride != b.stride)
+    return d < (n - 1) * a.stride + a.wide && -d < (n - 1) * b.stride + b.wide;
+  // row i of b begins `rest` bytes behind the beginning of row i + off of a
+  __int128 off = d / a.stride, rest = d % a.stride;
+  if (rest < 0) rest += a.stride, --off;
+  auto there = [&](__int128 k) { return k > -n && k < n; };
+  return (rest < a.wide && there(off)) || (rest + b.wide > a.stride && there(off + 1));
+}
+// The same for an output that may be the input itself.
+static bool part_of(const Rows &out, const Rows &in, int64_t n) { return out.p != in.p && rows_meet(out, in, n); }
+
 static bool bad_layout(dspark_rotary_layout layout) {
   return layout != DSPARK_ROTARY_HALF && layout != DSPARK_ROTARY_INTERLEAVED;
 }
@@ -675,6 +699,12 @@ static dspark_status rotary(bool back, int n_rows, int Hq, int Hkv, int D, int r
       ((uintptr_t)turns & 7u) != 0 || !aligned4(positions) || !aligned4(row_offset) || !aligned4(kv_len))
     return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  const int es = dt == DSPARK_BF16 ? 2 : 4;
+  const Rows rq(q, q_stride, Hq * D, es), oq(q_out, q_out_stride, Hq * D, es);
+  const Rows rk(k, k_stride, Hkv * D, es), ok(k_out, k_out_stride, Hkv * D, es);
+  if (part_of(oq, rq, n_rows) || part_of(ok, rk, n_rows) || rows_meet(oq, rk, n_rows) ||
+      rows_meet(ok, rq, n_rows) || rows_meet(oq, ok, n_rows))
+    return DSPARK_ERR_VALUE;
   RotaryLaunch L{};
   L.n_rows = n_rows; L.Hq = Hq; L.Hkv = Hkv; L.D = D; L.rot = rot; L.R = R;
   L.interleaved = layout == DSPARK_ROTARY_INTERLEAVED; L.bf16 = dt == DSPARK_BF16; L.back = back;
@@ -744,6 +774,12 @@ dspark_status dspark_cache_append(int R, int rows_capacity, int Hq, int Hkv, int
       !aligned4(positions) || !aligned4(table) || !aligned4(row_offset) || !aligned4(kv_len))
     return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  const int es = dt == DSPARK_BF16 ? 2 : 4;
+  const Rows out(q_out, q_out_stride, Hq * D, es);
+  if (part_of(out, Rows(q, q_stride, Hq * D, es), rows_capacity) ||
+      rows_meet(out, Rows(k_new, kv_stride, Hkv * D, es), rows_capacity) ||
+      rows_meet(out, Rows(v_new, kv_stride, Hkv * D, es), rows_capacity))
+    return DSPARK_ERR_VALUE;
   AppendLaunch L{};
   L.R = R; L.rows_capacity = rows_capacity; L.Hq = q != nullptr ? Hq : 0; L.Hkv = Hkv; L.D = D;
   L.page_shift = shift_of(page); L.max_pages = max_pages; L.n_pages = n_pages; L.rot = rot;
@@ -787,6 +823,10 @@ static dspark_status check_edit(const EditLaunch &L, dspark_dtype dt, const void
       !aligned4(L.frequency) || !aligned4(L.presence))
     return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  const Rows out(L.out, L.out_stride, L.V, 16 / per);
+  if (part_of(out, Rows(L.X, L.row_stride, L.V, 16 / per), L.n_rows) ||
+      part_of(out, Rows(L.G, L.g_stride, L.V, 16 / per), L.n_rows))
+    return DSPARK_ERR_VALUE;
   return DSPARK_OK;
 }
 
@@ -854,6 +894,7 @@ dspark_status dspark_history_append(int R, int width, int n_tokens, const int32_
       !aligned4(history) || !aligned4(hist_len) || !aligned4(hist_len_out) || !aligned4(prompt_len))
     return DSPARK_ERR_ALIGN;
   if (ws_bytes < kWsHeader) return DSPARK_ERR_WORKSPACE;
+  if (part_of(Rows(hist_len_out, 1, 1, 4), Rows(hist_len, 1, 1, 4), R)) return DSPARK_ERR_VALUE;
   HistoryLaunch L{};
   L.R = R; L.width = width; L.n_tokens = n_tokens; L.hist_stride = hist_stride; L.tokens = tokens;
   L.n_acc = n_acc; L.row_offset = row_offset; L.hist_len = hist_len; L.history = history;

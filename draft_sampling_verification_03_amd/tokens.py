@@ -107,7 +107,8 @@ def rotary(q, k=None, *, plan, positions=None, row_offset=None, kv_len=None, ws=
     """q [rows][Hq][D] and k [rows][Hkv][D] with their positions rotated in: positions
     [rows] int32; or of the sequences row_offset [R + 1], each from 0 on or, with kv_len
     [R], the last tokens of so many; or 0, 1, ... (with kv_len [rows] alone: kv_len - 1).
-    Returns {"q", "k"}; `out` may name the inputs (in place)."""
+    Returns {"q", "k"}; `out` may name the inputs (in place) or tensors beside them in one
+    buffer, not over a part of them."""
     return _rotate("rotary", q, k, plan, positions, row_offset, kv_len, ws, stream, out)
 
 
@@ -239,7 +240,8 @@ def edit_logits(X, *, row_offset=None, history=None, hist_len=None, prompt_len=N
     mask  [n_masks][ceil(V / 32)] int32: bit v % 32 of word v / 32 allows v; mask_index
         [n_rows] int32: the row's mask, -1 for none (None: row i's is mask i)
 
-    Returns out, which may be X itself; rows that no request has keep what it held."""
+    Returns out, which may be X itself (not a view over a part of it); rows that no request
+    has keep what it held."""
     e = _Edits("edit_logits", X, row_offset, history, hist_len, prompt_len, drafts, repetition, mask,
                mask_index)
     a, R = e.a, e.R

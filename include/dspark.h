@@ -83,7 +83,8 @@ typedef enum {
   DSPARK_ERR_NULL = 1,      /* a required pointer is NULL                     */
   DSPARK_ERR_SHAPE = 2,     /* a size outside the limits above                */
   DSPARK_ERR_DTYPE = 3,     /* unknown element type                           */
-  DSPARK_ERR_VALUE = 4,     /* temp not finite and > 0, or a bad scalar       */
+  DSPARK_ERR_VALUE = 4,     /* temp not finite and > 0, a bad scalar, or an
+                               output where it may not be                     */
   DSPARK_ERR_WORKSPACE = 5, /* ws_bytes below the *_workspace() size          */
   DSPARK_ERR_SPS_TABLE = 6, /* SPS table missing or shorter than R(1+gamma)+1 */
   DSPARK_ERR_MODE = 7,      /* unknown scheduler mode or missing c / c_prev2  */

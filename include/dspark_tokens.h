@@ -85,7 +85,9 @@ dspark_status dspark_rotary_turns(int n, const double *freqs, uint64_t *turns);
  *   D a multiple of 8 up to 256, 2 <= rot <= D even; 1 <= Hq <= 1024, 0 <= Hkv <= 1024;
  *     1 <= n_rows <= 4194304; 1 <= R <= 4194304; strides multiples of 16 bytes
  * Outputs: q_out, k_out [n_rows][H][D] (dt) with strides of their own; each may be its
- *   input (in place: the same stride then), and overlaps nothing else.  cos, sin and the
+ *   input (in place: the same stride then), and overlaps nothing else: rows of one stride may
+ *   stand side by side (heads of one buffer), with two different strides neither array may
+ *   reach into the other's first to last byte (DSPARK_ERR_VALUE).  cos, sin and the
  *   rotation are fp32; the result is rounded once. */
 dspark_status dspark_rotary(int n_rows, int Hq, int Hkv, int D, int rot, dspark_rotary_layout layout,
                             dspark_dtype dt, float magnitude, const uint64_t *turns,
@@ -114,7 +116,8 @@ dspark_status dspark_rotary_backward(int n_rows, int Hq, int Hkv, int D, int rot
  *     and keys both
  *   positions [rows_capacity] int32: positions for the rotation that are not the
  *     tokens' places in the cache; NULL: those
- *   q, q_out: NULL both with keys and values alone (Hq is then not read); q_out may be q
+ *   q, q_out: NULL both with keys and values alone (Hq is then not read); q_out may be q,
+ *     and overlaps neither part of it nor k_new and v_new (as for dspark_rotary)
  *   k_new, v_new [rows_capacity][Hkv][D], kv_stride elements from row to row
  *   row_offset [R + 1], or NULL: one row each (rows_capacity = R)
  * Rows that no request has (from row_offset[R] on) are neither read nor written.  Rows
@@ -164,8 +167,8 @@ dspark_status dspark_cache_append(int R, int rows_capacity, int Hq, int Hkv, int
  *     none (NULL: row i has mask i, n_masks >= n_rows).  mask NULL: none.
  * Output: out [n_rows][out_stride] (dt); it may be X itself (out_stride = row_stride: then
  *   only the lines of a row, 128 bytes from its start on, in which something changes are
- *   read and written).  Columns from V on and rows that no request
- *   has stay as they were.
+ *   read and written), and otherwise overlaps nothing of X (as for dspark_rotary:
+ *   DSPARK_ERR_VALUE).  Columns from V on and rows that no request has stay as they were.
  * A token or bias id outside [0, V) and not -1 sets DSPARK_DEVERR_TOKEN and is skipped; a
  * slice of row_offset that decreases or passes n_rows, a hist_len outside
  * [0, hist_stride] or prompt_len outside [0, hist_len] sets DSPARK_DEVERR_LENGTH and
@@ -187,7 +190,7 @@ dspark_status dspark_edit_logits(int n_rows, int V, int64_t row_stride, dspark_d
  *   dX = v allowed ? (s_v ? (x > 0 ? G / repetition : G repetition) : G) : 0
  * (the counts are constants; biases and the other penalties only add).  X is read only
  * where repetition is given.  G [n_rows][g_stride]; dX [n_rows][dx_stride] may be G
- * itself, but not X.  Everything else as above. */
+ * itself, but not a part of it or X.  Everything else as above. */
 dspark_status dspark_edit_logits_backward(int n_rows, int V, int64_t row_stride, dspark_dtype dt,
                                           const void *X, const void *G, int64_t g_stride, int R,
                                           const int32_t *row_offset, const int32_t *history,
@@ -200,7 +203,8 @@ dspark_status dspark_edit_logits_backward(int n_rows, int V, int64_t row_stride,
 
 /* --------------------------------------------------------- history_append --
  * The histories that dspark_edit_logits reads grow: request rho's new tokens go to
- * history[rho][hist_len[rho] ..] and its length to hist_len_out (which may be hist_len).
+ * history[rho][hist_len[rho] ..] and its length to hist_len_out (which may be hist_len, not a
+ * part of it).
  *   tokens [R][width]: the first n_acc[rho] + 1 (the y of dspark_verify; -1: none), or
  *     with n_acc and row_offset NULL all of them;
  *   tokens [n_tokens] with row_offset [R + 1] alone: request rho's are those in

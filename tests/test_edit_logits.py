@@ -500,6 +500,42 @@ def test_streams_and_two_graphs_over_one_workspace():
     assert ws.error_code() == 0
 
 
+def test_outputs_beside_the_input_and_over_it():
+    """Columns and rows of one buffer may hold input and output; an output that lies over
+    a part of the input is refused, and nothing is launched."""
+    e = Edits([2, 3], 250, BF, seed=16, longest=40, n_bias=2, masks=2)
+    kw, grad = e.args(), e.args(grad=True)
+    want = ds.edit_logits(e.X, **kw)
+    buf = torch.zeros((12, 512), dtype=BF, device="cuda")
+    for x, out in ((buf[:5, :250], buf[:5, 256:506]), (buf[:5, 256:506], buf[:5, :250]),
+                   (buf[:5, :250], buf[5:10, :250]), (buf[0:10:2, :250], buf[1:11:2, :250]),
+                   (buf[1:11:2, :250], buf[0:10:2, :250])):
+        buf.zero_()
+        x.copy_(e.X)
+        ds.edit_logits(x, out=out, **kw)
+        assert torch.equal(out, want) and torch.equal(x, e.X)
+    wide = torch.arange(12 * 512, device="cuda").view(12, 512).to(BF)
+    before = wide.clone()
+    flat = wide.view(24, 256)
+    for x, out in ((flat[:5, :250], flat[1:6, :250]), (flat[1:6, :250], flat[:5, :250]),
+                   (wide[:5, :250], wide[:5, 8:258]), (wide[:5, :250], flat[2:7, :250])):
+        with pytest.raises(ds.DSparkError, match="VALUE"):
+            ds.edit_logits(x, out=out, **kw)
+        with pytest.raises(ds.DSparkError, match="VALUE"):
+            ds.edit_logits_backward(x, raw_rows(e.X), out=out, **grad)
+        with pytest.raises(ds.DSparkError, match="VALUE"):
+            ds.edit_logits_backward(raw_rows(e.X), x, out=out, **grad)
+    assert torch.equal(wide, before)
+    one = Edits([1], 250, BF, seed=17, longest=40)
+    buf[3, :250].copy_(one.X[0])
+    ds.edit_logits(buf[3:4, :250], out=buf[4:5, :250], **one.args())
+    assert torch.equal(buf[4:5, :250], ds.edit_logits(one.X, **one.args()))
+    lens = i32([1, 2, 3, 4])
+    with pytest.raises(ds.DSparkError, match="VALUE"):
+        ds.history_append(i32([[0] * 8] * 3), lens[:3], i32([[1]] * 3), out=lens[1:])
+    assert lens.tolist() == [1, 2, 3, 4]
+
+
 # ---------------------------------------------------------------- histories
 def test_history_append():
     rng = np.random.default_rng(1)

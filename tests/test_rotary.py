@@ -457,3 +457,35 @@ def test_a_round_without_room_appends_nothing(captured):
         assert same(snapshot(cache), before)
         assert cache.missing.item() == 2  # one more page for each request
         assert (out["out"] == 3).all() and (out["lse"] == 3).all()
+
+
+@pytest.mark.parametrize("n", [1, 7])
+def test_outputs_beside_the_inputs_and_over_them(n):
+    """Inputs and outputs may stand side by side in one buffer; an output that lies over
+    part of its input, or over any of the other's, is refused."""
+    plan = ds.RotaryPlan(64)
+    buf = rnd(7, n, 12, 64)
+    q, k, qo, ko = buf[:, :4], buf[:, 4:6], buf[:, 6:10], buf[:, 10:]
+    want = ds.rotary(q.contiguous(), k.contiguous(), plan=plan)
+    keep = buf[:, :6].clone()
+    ds.rotary(q, k, plan=plan, out={"q": qo, "k": ko})
+    assert torch.equal(qo, want["q"]) and torch.equal(ko, want["k"]) and torch.equal(buf[:, :6], keep)
+    buf = rnd(7, n + 1, 12, 64)
+    keep = buf.clone()
+    q, k = buf[:n, :4], buf[:n, 4:6]
+    for out in (dict(q=buf[:n, 1:5], k=buf[:n, 10:]), dict(q=buf[:n, 2:6], k=buf[:n, 10:]),
+                dict(q=q, k=buf[:n, 3:5]), dict(q=q, k=buf[:n, 5:7]), dict(q=buf[:n, 6:10], k=buf[:n, 9:11])):
+        for f in (ds.rotary, ds.rotary_backward):
+            with pytest.raises(ds.DSparkError, match="VALUE"):
+                f(q, k, plan=plan, out=out)
+    if n > 1:
+        with pytest.raises(ds.DSparkError, match="VALUE"):
+            ds.rotary(q, plan=plan, out={"q": buf[1:, :4]})
+    assert torch.equal(buf, keep)
+    c = Case([n], [40], 4, 2, 64, 16, F, packed=True)
+    before = c.k.clone(), c.v.clone()
+    with pytest.raises(ds.DSparkError, match="VALUE"):
+        wide = torch.cat((c.q, c.kn, c.vn), 1)
+        ds.cache_append(wide[:, :4], wide[:, 4:6], wide[:, 6:], c.k, c.v, c.table, c.kv_len, plan=plan,
+                        row_offset=c.row_offset, out=wide[:, 2:6])
+    assert torch.equal(c.k.view(I32), before[0].view(I32)) and torch.equal(c.v.view(I32), before[1].view(I32))

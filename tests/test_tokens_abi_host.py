@@ -348,3 +348,47 @@ def test_append_alignment(name):
                                   "prompt_len"])
 def test_history_alignment(name):
     assert A.dspark_history_append(**history(**{name: P + 2})) == ALIGN
+
+
+# --------------------------------- outputs that overlap an input without being it
+@pytest.mark.parametrize("over", [
+    dict(q_out=P + 512), dict(q_out=P + 16), dict(q_out=P - 512), dict(q_out=P + 512, q_out_stride=264),
+    dict(q_out=P3), dict(q_out=P3 + 1024), dict(k_out=P), dict(k_out=P + 2048), dict(k_out=P3 + 256),
+    dict(k_out=P3 - 32), dict(q_out=P2, k_out=P2 + 512), dict(q_out=P2, k_out=P2 + 256, k_out_stride=256),
+    dict(q_out=P, k_out=P + 128),
+])
+@pytest.mark.parametrize("f", [A.dspark_rotary, A.dspark_rotary_backward])
+def test_rotary_overlap(f, over):
+    """q [8][4][64] at P, k [8][2][64] at P3, bf16."""
+    assert f(*rotary(**dict(dict(k=P3, k_out=P3), **over))) == VALUE
+
+
+@pytest.mark.parametrize("over", [
+    dict(q_out=P + 1024), dict(q_out=P + 16), dict(q_out=P - 2048), dict(q_out=P + 64, q_out_stride=520),
+    dict(q_out=P3), dict(q_out=P3 + 256), dict(q_out=0x40000 + 2816), dict(q_out=0x40000 - 12 * 1024 + 16),
+])
+def test_append_overlap(over):
+    """q [12][8][64] at P, new keys and values [12][2][64] behind it, bf16."""
+    assert A.dspark_cache_append(**append(**dict(dict(k_new=P3, v_new=0x40000), **over))) == VALUE
+
+
+@pytest.mark.parametrize("over", [dict(out=P + 2016), dict(out=P + 16), dict(out=P - 7 * 2016),
+                                  dict(out=P + 4096, out_stride=1016), dict(out=P - 2000, row_stride=2016,
+                                                                            out_stride=2016)])
+def test_edit_overlap(over):
+    assert A.dspark_edit_logits(**edit(**over)) == VALUE
+
+
+@pytest.mark.parametrize("over", [dict(dX=P2 + 2016), dict(dX=P2 - 16), dict(dX=P + 2016), dict(dX=P - 2016),
+                                  dict(dX=P + 2016, repetition=None), dict(dX=P2 + 32, dx_stride=1016)])
+def test_edit_backward_overlap(over):
+    a = edit(G=P2, g_stride=1008, dX=P3, dx_stride=1008)
+    for name in ("frequency", "presence", "n_bias", "bias_ids", "bias", "out", "out_stride"):
+        a.pop(name)
+    a.update(over)
+    assert A.dspark_edit_logits_backward(**a) == VALUE
+
+
+@pytest.mark.parametrize("over", [dict(hist_len_out=P + 4), dict(hist_len_out=P - 12)])
+def test_history_overlap(over):
+    assert A.dspark_history_append(**history(**over)) == VALUE
