@@ -118,7 +118,8 @@ def decode(rounds, x0, W1, W2, U_of_round, target_rows, *, SPS=None, mode=0, thr
     logprobs      number of alternatives (0: none) to report beside the log
                   probability and entropy of every emitted token
     token_history tokens.TokenHistory that holds every token up to the anchors (included);
-                  the emitted tokens join it
+                  the emitted tokens join it.  A round whose tokens a history has no
+                  room for raises RuntimeError, with cache and histories as they were
     edits         arguments of tokens.edit_logits for the target's rows (repetition,
                   bias_ids, ...), or a callable (prev, the rows' previous tokens) -> such
                   arguments (a grammar's mask and mask_index of the round's rows)
@@ -154,6 +155,8 @@ def _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold, c
         if logprobs > 0:
             rec.update(top_ids=[], top_logp=[])
     hist, past = None, []
+    if token_history is not None:
+        said, room = token_history.lens.cpu().numpy().astype(np.int64), token_history.tokens.shape[1]
     for i in range(rounds):
         t = first_round + i
         U = U_of_round(t)
@@ -195,6 +198,14 @@ def _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold, c
                  else token_history.edit(P, **how))
         v = api.verify(s["ell"], s["row_offset"], P, U, W1, W2, anchors, d["x"], d["q_stats"],
                        d["q_x"], temp=temp, seed=seed, round=t, ws=ws_v, stream=stream)
+        if token_history is not None and (said + ell + 1 > room).any():
+            # edits by a history that lacks tokens would be another law's
+            full = np.flatnonzero(said + v["n_acc"].cpu().numpy() + 1 > room)
+            if full.size:
+                if cache is not None:
+                    cache.commit(torch.full_like(v["n_acc"], -1), stream=stream)
+                raise RuntimeError(f"decode: round {t} passes the room of {room} tokens in request "
+                                   f"{full[0]}'s history")
         if cache is not None:
             cache.commit(v["n_acc"], stream=stream)
         if token_history is not None:
@@ -207,6 +218,8 @@ def _decode(rounds, x0, W1, W2, U_of_round, target_rows, SPS, mode, threshold, c
         y = v["y"].cpu().numpy()
         if lp is not None:
             _record_logprobs(rec, lp, s["row_offset"].cpu().numpy(), n, gamma)
+        if token_history is not None:
+            said += n + 1
         for rho in range(R):
             streams[rho].extend(int(tok) for tok in y[rho, : n[rho] + 1])
         anchors = torch.as_tensor(y[np.arange(R), n]).to(W1.device, dtype=torch.int32)

@@ -262,3 +262,45 @@ def test_a_captured_round(room):
     if room:
         assert a["cache"].error_code() == 0 and a["hist"].error_code() == 0
         assert b["cache"].error_code() == 0 and b["hist"].error_code() == 0
+
+
+def test_decode_stops_where_a_history_is_full():
+    """The round whose tokens do not fit raises and changes neither the cache nor any
+    history; a history that they just fill takes them."""
+    R, gamma, rounds = 3, 3, 8
+    rng = np.random.default_rng(11)
+    prompts = [rng.integers(0, V, n).tolist() for n in (2, 17, 5)]
+    W1, W2, U = head(4, R, gamma)
+    repetition = torch.tensor([2.0, 1.0, 0.5], device="cuda")
+
+    def run(capacity, rounds):
+        cache = ds.PagedCache(R, 60, Hkv=HKV, D=D, layers=LAYERS, page=16, dtype=torch.float32)
+        model = RotaryModel(1, R, prompts)
+        x0 = prefill(model, cache, prompts)
+        hist = ds.TokenHistory(R, capacity)
+        hist.tokens = torch.full((R, capacity), -1, dtype=I32, device="cuda")
+        hist.start(i32(sum(prompts, [])), offsets([len(p) for p in prompts]))
+        try:
+            return decode.decode(rounds, x0, W1, W2, U, model.rows, cache=cache, token_history=hist,
+                                 edits=dict(repetition=repetition)), cache, hist
+        except RuntimeError as e:
+            return e, cache, hist
+
+    want, cache, hist = run(200, rounds)
+    said = [prompts[r] + want["streams"][r] for r in range(R)]
+    lens = np.array([len(p) for p in prompts]) + np.cumsum(np.array(want["n_acc"]) + 1, 0)  # after each round
+    assert hist.lens.tolist() == lens[-1].tolist()
+    longest = int(lens[-1].max())
+    got, cache, hist = run(longest, rounds)
+    assert got["streams"] == want["streams"] and hist.lens.tolist() == lens[-1].tolist()
+    for capacity in (longest - 1, 19):  # 17 and at least 8 tokens do not fit
+        whole = int((lens.max(1) <= capacity).sum())  # rounds that fit
+        assert whole < rounds
+        got, cache, hist = run(capacity, rounds)
+        assert isinstance(got, RuntimeError) and f"round {whole}" in str(got) and "history" in str(got)
+        kept = lens[whole - 1].tolist() if whole else [len(p) for p in prompts]
+        assert hist.lens.tolist() == kept and cache.lens.tolist() == [n - 1 for n in kept]
+        for r in range(R):
+            assert hist.tokens[r, : kept[r]].tolist() == said[r][: kept[r]]
+            assert (hist.tokens[r, kept[r]:] == -1).all()
+        assert hist.error_code() == 0 and cache.error_code() == 0
