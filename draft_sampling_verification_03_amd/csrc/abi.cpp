@@ -889,7 +889,8 @@ dspark_status dspark_history_append(int R, int width, int n_tokens, const int32_
   if (R < 1 || R > (1 << 20) || hist_stride < 1 || hist_stride > kLongest) return DSPARK_ERR_SHAPE;
   const bool flat = row_offset != nullptr && n_acc == nullptr;
   if (flat ? n_tokens < 0 : width < 1 || width > kLongest) return DSPARK_ERR_SHAPE;
-  if (!tokens || !history || !hist_len || !hist_len_out || !ws) return DSPARK_ERR_NULL;
+  if ((!tokens && !(flat && n_tokens == 0)) || !history || !hist_len || !hist_len_out || !ws)
+    return DSPARK_ERR_NULL;
   if (!aligned16(ws) || !aligned4(tokens) || !aligned4(n_acc) || !aligned4(row_offset) ||
       !aligned4(history) || !aligned4(hist_len) || !aligned4(hist_len_out) || !aligned4(prompt_len))
     return DSPARK_ERR_ALIGN;

@@ -208,7 +208,8 @@ dspark_status dspark_edit_logits_backward(int n_rows, int V, int64_t row_stride,
  *   tokens [R][width]: the first n_acc[rho] + 1 (the y of dspark_verify; -1: none), or
  *     with n_acc and row_offset NULL all of them;
  *   tokens [n_tokens] with row_offset [R + 1] alone: request rho's are those in
- *     [row_offset[rho], row_offset[rho + 1]), a prompt's;
+ *     [row_offset[rho], row_offset[rho + 1]), a prompt's (tokens may be NULL with
+ *     n_tokens = 0: no request has any);
  *   with n_acc and row_offset both, tokens [R][width], and row_offset is what
  *     dspark_cache_reserve left in its workspace: as in dspark_cache_commit, n_acc[rho] + 1
  *     has to be within the request's rows, so that a round which found no pages (and

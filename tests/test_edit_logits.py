@@ -574,6 +574,18 @@ def test_history_append():
     assert prompt.tolist() == [off[r + 1] - off[r] if off[r + 1] > off[r] else want_prompt[r] for r in range(R)]
 
 
+def test_history_append_of_no_tokens():
+    """A flat list without a token (no request has a prompt) changes nothing."""
+    hist = ds.TokenHistory(3, 10)
+    hist.start(i32([7, 8]), i32([0, 0, 2, 2]))
+    for _ in range(2):
+        hist.start(torch.empty(0, dtype=I32, device="cuda"), i32([0] * 4))
+        assert hist.lens.tolist() == [0, 2, 0] and hist.prompt_lens.tolist() == [0, 2, 0]
+        assert hist.tokens[1].tolist() == [7, 8] + [-1] * 10 and hist.error_code() == 0
+    hist.start(torch.empty(0, dtype=I32, device="cuda"), i32([0, 0, 1, 1]))  # a token that is not there
+    assert hist.error_code() == LENGTH and hist.lens.tolist() == [0, 2, 0]
+
+
 @pytest.mark.parametrize("what", ["n_acc", "length", "offsets", "end", "rows"])
 def test_history_append_refuses_bad_data(what):
     """The request that is wrong stays as it is, the others grow."""

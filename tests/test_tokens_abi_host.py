@@ -392,3 +392,10 @@ def test_edit_backward_overlap(over):
 @pytest.mark.parametrize("over", [dict(hist_len_out=P + 4), dict(hist_len_out=P - 12)])
 def test_history_overlap(over):
     assert A.dspark_history_append(**history(**over)) == VALUE
+
+
+@pytest.mark.parametrize("over", [dict(), dict(row_offset=P), dict(n_acc=None, row_offset=None),
+                                  dict(n_acc=None, row_offset=P, n_tokens=1)])
+def test_history_without_tokens(over):
+    """Only a flat list of none needs no tokens."""
+    assert A.dspark_history_append(**history(**dict(dict(tokens=None, n_tokens=0), **over))) == NULL
