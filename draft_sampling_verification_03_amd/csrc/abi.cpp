@@ -655,8 +655,8 @@ struct Rows {
 static bool rows_meet(const Rows &a, const Rows &b, int64_t n) {
   if (!a.p || !b.p) return false;
   const __int128 d = (__int128)(uintptr_t)b.p - (__int128)(uintptr_t)a.p;  // from a to b
-  if (a.stride != b.stride)
-    return d < (n - 1) * a.stride + a.wide && -d < (n - 1) * b.stride + b.wide;
+  if (d >= (n - 1) * a.stride + a.wide || -d >= (n - 1) * b.stride + b.wide) return false;
+  if (a.stride != b.stride) return true;
   // row i of b begins `rest` bytes behind the beginning of row i + off of a
   __int128 off = d / a.stride, rest = d % a.stride;
   if (rest < 0) rest += a.stride, --off;

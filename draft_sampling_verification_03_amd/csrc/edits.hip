@@ -18,7 +18,8 @@
 // (282 MB) 69 us; fp32 rows with histories of up to 120000 46 us, two thirds of them the
 // counting (one LDS operation for 64 tokens, in each of the 16 chunks).  Masks in place, half
 // of them dense, half sparse: 169 MB fetched and 172 written, for nearly every 128 bytes
-// hold both kinds: 68 to 73 us.  One row: 8 us of latency.
+// hold both kinds: 68 to 73 us (fp32: 117).  The 1152 rows in place 129 us (fp32: 162), the
+// gradient 48.  One row: 7 us of latency.
 #include <float.h>
 
 #include "common.h"
@@ -445,7 +446,8 @@ __global__ __launch_bounds__(kThreads) void edit_kernel(EditLaunch L, unsigned c
   if (bits && chunk == 0) flag_error(L.err, bits);
 }
 
-// One workgroup a request.
+// One workgroup a request: 2 us for a round's tokens, but a prompt of 100000 takes 48 and one
+// of a million 872.
 __global__ __launch_bounds__(kBlock) void history_append_kernel(HistoryLaunch L) {
   const int r = blockIdx.x, tid = threadIdx.x;
   const int len = L.hist_len[r];

@@ -172,7 +172,8 @@ dspark_status dspark_cache_append(int R, int rows_capacity, int Hq, int Hkv, int
  * A token or bias id outside [0, V) and not -1 sets DSPARK_DEVERR_TOKEN and is skipped; a
  * slice of row_offset that decreases or passes n_rows, a hist_len outside
  * [0, hist_stride] or prompt_len outside [0, hist_len] sets DSPARK_DEVERR_LENGTH and
- * counts as empty, 0 and 0; a mask_index outside [-1, n_masks) sets it and counts as -1;
+ * counts as empty, 0 and 0 (rows that two of the other slices share, as only offsets out of
+ * order make them, are unspecified); a mask_index outside [-1, n_masks) sets it and counts as -1;
  * a parameter out of its range sets DSPARK_DEVERR_NONFINITE and counts as none.
  * Workspace: 256 bytes (the error word). */
 dspark_status dspark_edit_logits(int n_rows, int V, int64_t row_stride, dspark_dtype dt,
