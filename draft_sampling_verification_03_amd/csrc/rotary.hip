@@ -11,13 +11,13 @@
 // of its rows go to LDS once and serve all of the stretch's heads.
 //
 // Bound: queries, keys and values are read and written once.  8191 rows of 32 + 8 heads of
-// 128, bf16 (168 MB): 35 us, 4.8 TB/s (29 in a trace of two batches in turn); 23838 new rows of 12 + 2 * 4 heads of 96, fp32, into
-// pages of 64 (366 MB; counters: 183 fetched, 184 written): 91 us, 4.0 TB/s, where keys and
-// values alone (146 MB) take 42: their 16 slots of a page are 64 bytes a row.  Four items of
-// a thread read ahead of the first one's writing (95 us; rotary 40), or neighbouring
-// groups on one XCD (98), gain nothing.  1152 rows of 128 requests
-// (28 MB): 13.7 us, for values of groups that are not full are stored two bytes at a time, one
-// turn after another.  Single tokens: 3.7 us, one launch.
+// 128, bf16 (168 MB): 35 us, 4.8 TB/s (29 in a trace of two batches in turn); 23838 new rows
+// of 12 + 2 * 4 heads of 96, fp32, into pages of 64 (366 MB; counters: 183 fetched, 184
+// written): 91 us, 4.0 TB/s, where keys and values alone (146 MB) take 42: their 16 slots of
+// a page are 64 bytes a row.  Four items of a thread read ahead of the first one's writing
+// (95 us; rotary 40), or neighbouring groups on one XCD (98), gain nothing.  1152 rows of
+// 128 requests (28 MB): 13.7 us, for values of groups that are not full are stored two bytes
+// at a time, one turn after another.  Single tokens: 3.7 us, one launch.
 #include <limits.h>
 
 #include "common.h"
